@@ -13,6 +13,7 @@ one chunk's tiles so that those waits run out.  The product path never loads it.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import subprocess
@@ -46,7 +47,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     os.makedirs(build_dir, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     newest_hdr = max([os.path.getmtime(h) for h in _headers()] + [0.0])
-    objs = []
+    objs, cmds = [], []
     for src in srcs:
         obj = os.path.join(build_dir, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
@@ -58,7 +59,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             cmd += ["-Xptxas", "-v"]
         if verbose:
             print(" ".join(cmd), flush=True)
-        subprocess.check_call(cmd)
+        cmds.append(cmd)
+    with concurrent.futures.ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+        list(pool.map(subprocess.check_call, cmds))
     if (force or not os.path.exists(lib_path)
             or os.path.getmtime(lib_path) < max(os.path.getmtime(o) for o in objs)):
         tmp = lib_path + f".tmp{os.getpid()}"

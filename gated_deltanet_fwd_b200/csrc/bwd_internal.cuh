@@ -1,0 +1,101 @@
+// bwd_internal.cuh -- declarations shared by the kernels of the layer core's backward passes.
+#pragma once
+
+#include "gdn_internal.cuh"
+
+namespace gdn {
+namespace bwd {
+
+constexpr size_t HEADER = 1024;  // status word and padding at the start of the rule's workspace
+
+// Arguments of gdn_chunk_bwd after the host checks.
+struct Args {
+  const void *q, *k, *v, *dout;
+  TokStrides ts;
+  const float *g, *beta, *S0, *dST;
+  const int32_t* cu;
+  gdn_dtype dt;
+  float scale;
+  int N, B;
+  int64_t T;
+  int Hk, Hv, dk, dv, C;
+  void *dq, *dk_, *dv_, *dg, *dbeta;
+  float* dS0;
+  void* ws;
+  size_t ws_bytes;
+  int* status;
+};
+
+size_t simt_workspace_bytes(int N, int64_t n_tok, int Hv, int dk, int dv, int C);
+cudaError_t launch_simt(const Args& a, cudaStream_t s);
+
+// A "slot" is the ordinal of a chunk among all chunks of all sequences, in sequence order.
+__host__ __device__ inline int64_t max_slots(int N, int64_t n_tok, int C) {
+  return (n_tok + C - 1) / C + N;
+}
+
+// The smallest magnitude of beta used in T' (see bwd_simt.cu): 2^-30.
+__device__ __forceinline__ float floor_beta(float b) {
+  return fabsf(b) < 9.313225746e-10f ? copysignf(9.313225746e-10f, b) : b;
+}
+
+// Sequence n's tokens and the slot of its first chunk; false for a malformed cu_seqlens met up to n
+// (nothing may be read through it).
+__device__ __forceinline__ bool seq_range(const int32_t* cu, int64_t T, int n, int C, int64_t& s_beg,
+                                          int64_t& s_end, int64_t& slot0) {
+  if (!cu) {
+    s_beg = (int64_t)n * T;
+    s_end = s_beg + T;
+    slot0 = (int64_t)n * ((T + C - 1) / C);
+    return true;
+  }
+  int64_t base = 0;
+  for (int m = 0; m <= n; ++m) {
+    const int64_t a = cu[m], b = cu[m + 1];
+    if (a < 0 || b < a || b > T) return false;
+    if (m < n) base += (b - a + C - 1) / C;
+    s_beg = a;
+    s_end = b;
+  }
+  slot0 = base;
+  return true;
+}
+
+struct Chunk {
+  int n, L;
+  int64_t t0;
+};
+
+// The chunk of a slot; false past the last one or for a malformed cu_seqlens (reported).
+__device__ __forceinline__ bool find_chunk(const int32_t* cu, int64_t T, int N, int C, int64_t slot,
+                                           Chunk& ch, int* status) {
+  if (!cu) {
+    const int64_t per = (T + C - 1) / C;
+    if (per == 0 || slot >= per * N) return false;
+    ch.n = (int)(slot / per);
+    const int64_t c = slot - (int64_t)ch.n * per;
+    ch.t0 = (int64_t)ch.n * T + c * C;
+    ch.L = (int)(T - c * C < C ? T - c * C : C);
+    return true;
+  }
+  int64_t base = 0;
+  for (int m = 0; m < N; ++m) {
+    const int64_t a = cu[m], b = cu[m + 1];
+    if (a < 0 || b < a || b > T) {
+      if (threadIdx.x == 0) report(status, GDN_ERR_DEVICE_ARG);
+      return false;
+    }
+    const int64_t nch = (b - a + C - 1) / C;
+    if (slot < base + nch) {
+      ch.n = m;
+      ch.t0 = a + (slot - base) * C;
+      ch.L = (int)(b - ch.t0 < C ? b - ch.t0 : C);
+      return true;
+    }
+    base += nch;
+  }
+  return false;
+}
+
+}  // namespace bwd
+}  // namespace gdn

@@ -1,0 +1,162 @@
+// gates_bwd.cu -- gradients of the two gates, and the sum over partial rows that the backward kernels
+// with per-channel sums share.
+//
+//   da = -dg e^{A_log} sigmoid(a + dt_bias)       db = dbeta beta (1 - beta),  beta = sigmoid(b)
+//   dA_log = sum over tokens of dg g              ddt_bias = sum over tokens of da
+//
+// HBM-bound in principle (four elements in, two out per token and head), but at the layer's 32 heads
+// it is a few microseconds of latency.  A thread owns VEC consecutive heads and walks tokens, so its two
+// sums stay in registers; the block adds its threads through shared memory and writes one partial row
+// [dA_log | ddt_bias]; the second kernel adds the partial rows in order.
+#include "gdn_internal.cuh"
+
+namespace gdn {
+namespace {
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) gates_bwd_kernel(
+    const T* __restrict__ a, const T* __restrict__ b, const float* __restrict__ A_log,
+    const float* __restrict__ dt_bias, const T* __restrict__ dg, const T* __restrict__ dbeta,
+    int64_t n_tok, int Hv, T* __restrict__ da, T* __restrict__ db, float* __restrict__ part) {
+  const int cols = Hv / VEC;                      // head groups
+  const int tile = cols < 256 ? cols : 256;       // of this block's width
+  const int per = 256 / tile;                     // tokens at once
+  const int cg = blockIdx.y * tile + threadIdx.x % tile, row = threadIdx.x / tile;
+  const bool on = row < per && cg < cols;
+  const int h = cg * VEC;
+  float eA[VEC], bias[VEC], sA[VEC] = {}, sb[VEC] = {};
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    eA[i] = on ? expf(__ldg(A_log + h + i)) : 0.0f;
+    bias[i] = on ? __ldg(dt_bias + h + i) : 0.0f;
+  }
+  if (on) {
+    for (int64_t t = (int64_t)blockIdx.x * per + row; t < n_tok; t += (int64_t)gridDim.x * per) {
+      const int64_t at = t * Hv + h;
+      float av[VEC], bv[VEC], gv[VEC], ev[VEC];
+      if constexpr (VEC == 8) {
+        load8(a + at, av);
+        load8(b + at, bv);
+        load8(dg + at, gv);
+        load8(dbeta + at, ev);
+      } else {
+        av[0] = to_f(a[at]);
+        bv[0] = to_f(b[at]);
+        gv[0] = to_f(dg[at]);
+        ev[0] = to_f(dbeta[at]);
+      }
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float u = av[i] + bias[i];
+        const float x = -gv[i] * eA[i];
+        sA[i] = fmaf(x, softplusf_(u), sA[i]);
+        av[i] = x * sigmoidf_(u);
+        sb[i] += av[i];
+        // beta (1 - beta) from e = e^-|b|, which neither overflows nor cancels
+        const float e = expf(-fabsf(bv[i])), q = 1.0f / (1.0f + e);
+        bv[i] = ev[i] * (e * q * q);
+      }
+      if constexpr (VEC == 8) {
+        store8(da + at, av);
+        store8(db + at, bv);
+      } else {
+        da[at] = from_f<T>(av[0]);
+        db[at] = from_f<T>(bv[0]);
+      }
+    }
+  }
+  __shared__ float sh[256 * 2 * VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    sh[threadIdx.x * 2 * VEC + i] = sA[i];
+    sh[threadIdx.x * 2 * VEC + VEC + i] = sb[i];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < tile * 2 * VEC; e += 256) {
+    const int c = e / (2 * VEC), i = e % (2 * VEC);
+    if (blockIdx.y * tile + c >= cols) continue;
+    float acc = 0.0f;
+    for (int r = 0; r < per; ++r) acc += sh[(r * tile + c) * 2 * VEC + i];
+    const int head = (blockIdx.y * tile + c) * VEC + i % VEC;
+    part[(int64_t)blockIdx.x * 2 * Hv + (i < VEC ? 0 : Hv) + head] = acc;
+  }
+}
+
+// Column c of the partial rows summed over them, to out[c] (c < split) or out2[c - split].  A block takes
+// 32 columns, its 8 warps every 8th row; each adds in 64 bits, then the 8 sums are added in order.
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ part,
+                                                        int64_t parts, int64_t stride,
+                                                        int64_t width, int64_t split, float* __restrict__ out,
+                                                        float* __restrict__ out2) {
+  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  double acc = 0.0;
+  if (c < width)
+    for (int64_t p = wp; p < parts; p += 8) acc += (double)part[p * stride + c];
+  __shared__ double sh[8][32];
+  sh[wp][lane] = acc;
+  __syncthreads();
+  if (wp == 0 && c < width) {
+    double t = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += sh[i][lane];
+    if (c < split)
+      out[c] = (float)t;
+    else
+      out2[c - split] = (float)t;
+  }
+}
+
+template <typename T, int VEC>
+cudaError_t run(const T* a, const T* b, const float* A_log, const float* dt_bias, const T* dg,
+                const T* dbeta, int64_t n_tok, int Hv, T* da, T* db, float* dA, float* ddt, float* part,
+                int64_t max_parts, cudaStream_t s) {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int cols = Hv / VEC, tile = cols < 256 ? cols : 256, per = 256 / tile;
+  int64_t blocks = (n_tok + per - 1) / per;
+  const int64_t cap = 2 * (int64_t)sms < max_parts ? 2 * (int64_t)sms : max_parts;
+  if (blocks > cap) blocks = cap;
+  const dim3 grid((unsigned)blocks, (unsigned)((cols + tile - 1) / tile));
+  if (blocks > 0)
+    gates_bwd_kernel<T, VEC><<<grid, 256, 0, s>>>(a, b, A_log, dt_bias, dg, dbeta, n_tok, Hv, da,
+                                                  db, part);
+  const cudaError_t e = cudaGetLastError();
+  const int64_t width = 2 * (int64_t)Hv;
+  return e == cudaSuccess ? launch_sum_parts(part, blocks, width, Hv, dA, ddt, width, s) : e;
+}
+
+template <typename T>
+cudaError_t pick(const void* a, const void* b, const float* A_log, const float* dt_bias,
+                 const void* dg, const void* dbeta, int64_t n_tok, int Hv, void* da, void* db,
+                 float* dA, float* ddt, float* part, int64_t max_parts, cudaStream_t s) {
+  // vector loads need whole 16-byte groups of heads
+  const bool vec = Hv % 8 == 0 && aligned16(a) && aligned16(b) && aligned16(dg) &&
+                   aligned16(dbeta) && aligned16(da) && aligned16(db);
+  return vec ? run<T, 8>((const T*)a, (const T*)b, A_log, dt_bias, (const T*)dg, (const T*)dbeta,
+                         n_tok, Hv, (T*)da, (T*)db, dA, ddt, part, max_parts, s)
+             : run<T, 1>((const T*)a, (const T*)b, A_log, dt_bias, (const T*)dg, (const T*)dbeta,
+                         n_tok, Hv, (T*)da, (T*)db, dA, ddt, part, max_parts, s);
+}
+
+}  // namespace
+
+cudaError_t launch_sum_parts(const float* part, int64_t parts, int64_t width, int64_t split,
+                             float* out, float* out2, int64_t stride, cudaStream_t s) {
+  sum_parts_kernel<<<(unsigned)((width + 31) / 32), 256, 0, s>>>(part, parts, stride, width, split,
+                                                                 out, out2);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gates_bwd(const void* a, const void* b, gdn_dtype dt, const float* A_log,
+                             const float* dt_bias, const void* dg, const void* dbeta,
+                             int64_t n_tok, int Hv, void* da, void* db, float* dA, float* ddt,
+                             float* part, int64_t max_parts, cudaStream_t s) {
+  return dt == GDN_BF16 ? pick<__nv_bfloat16>(a, b, A_log, dt_bias, dg, dbeta, n_tok, Hv, da, db,
+                                              dA, ddt, part, max_parts, s)
+                        : pick<float>(a, b, A_log, dt_bias, dg, dbeta, n_tok, Hv, da, db, dA, ddt,
+                                      part, max_parts, s);
+}
+
+}  // namespace gdn

@@ -157,6 +157,52 @@ cudaError_t launch_decode_fused(const void* mix, const void* a, const void* b, c
                                 float norm_eps, float scale, float* state, int N, int Hk, int Hv,
                                 void* y, cudaStream_t s);
 
+// ---- training: backward passes and 8-bit activation checkpoints.  `part` holds up to max_parts partial
+// rows of the sums over tokens.
+
+cudaError_t launch_gates_bwd(const void* a, const void* b, gdn_dtype dt, const float* A_log,
+                             const float* dt_bias, const void* dg, const void* dbeta,
+                             int64_t n_tok, int Hv, void* da, void* db, float* dA, float* ddt,
+                             float* part, int64_t max_parts, cudaStream_t s);
+
+cudaError_t launch_rmsnorm_ckpt8(const void* x, const void* z, gdn_dtype dt, const float* w,
+                                 float eps, int64_t rows, int dim, void* y, int8_t* xc, float* xs,
+                                 int8_t* zc, float* zs, cudaStream_t s);
+
+// xs, zs set: x and z are int8 codes with one scale per row
+cudaError_t launch_rmsnorm_bwd(const void* dy, const void* x, const float* xs, const void* z,
+                               const float* zs, gdn_dtype dt, const float* w, float eps,
+                               int64_t rows, int dim, void* dx, void* dz, float* dw, float* part,
+                               int64_t max_parts, cudaStream_t s);
+
+struct ConvBwdArgs {
+  const void* dy;
+  const void* x;        // of dtype, or int8 codes when xs is set
+  const float* xs;      // [tokens, C / xgroup] or null
+  int xgroup;
+  const float *w, *bias;
+  int64_t n_tok, T;
+  int C, K, N, n_l2, group;
+  const int32_t* cu;
+  float eps;
+  const float *cs_in, *dcs_out;
+  void* dx;
+  float *dw, *dbias, *dcs_in;
+  float* part;          // [ranges][C * K + C]
+  int64_t max_parts;
+};
+cudaError_t launch_conv_bwd(const ConvBwdArgs& a, gdn_dtype dt, cudaStream_t s);
+
+cudaError_t launch_act_pack8(const void* x, gdn_dtype dt, int64_t groups, int group, int8_t* codes,
+                             float* scales, cudaStream_t s);
+cudaError_t launch_act_unpack8(const int8_t* codes, const float* scales, gdn_dtype dt,
+                               int64_t groups, int group, void* x, cudaStream_t s);
+
+// The first `width` columns of `parts` partial rows (`stride` apart) added in row order: column c to
+// out[c] below `split`, to out2[c - split] from there on.
+cudaError_t launch_sum_parts(const float* part, int64_t parts, int64_t width, int64_t split,
+                             float* out, float* out2, int64_t stride, cudaStream_t s);
+
 // Element distances between consecutive tokens of q, k and v (dense: Hk*dk, Hk*dk, Hv*dv).
 struct TokStrides {
   int64_t q, k, v;

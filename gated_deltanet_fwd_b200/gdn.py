@@ -43,6 +43,20 @@ SIGNATURES = {
     "gdn_workspace_status": (_I, [_P, _P, ctypes.POINTER(_I)]),
     "gdn_recurrent_step": (_I, [_P, _P, _P, _P, _P, _I, _F, _P, _I, _I, _I, _I, _I, _P, _P]),
     "gdn_gated_rmsnorm": (_I, [_P, _P, _I, _P, _F, _I64, _I, _P, _P]),
+    "gdn_chunk_bwd_workspace_size": (_SZ, [_I, _I, _I, _I64, _I, _I, _I, _I, _I]),
+    "gdn_chunk_bwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I, _F, _P, _P, _P, _I, _I,
+                           _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "gdn_gates_bwd_workspace_size": (_SZ, [_I64, _I]),
+    "gdn_gates_bwd": (_I, [_P, _P, _I, _P, _P, _P, _P, _I64, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "gdn_gated_rmsnorm_bwd_workspace_size": (_SZ, [_I64, _I]),
+    "gdn_gated_rmsnorm_bwd": (_I, [_P, _P, _P, _P, _P, _I, _P, _F, _I64, _I, _P, _P, _P, _P, _SZ,
+                                   _P]),
+    "gdn_causal_conv1d_silu_bwd_workspace_size": (_SZ, [_I, _I64, _I, _I]),
+    "gdn_causal_conv1d_silu_bwd": (_I, [_P, _P, _P, _I, _I, _P, _P, _I, _I64, _I, _I, _P, _I, _I,
+                                        _I, _F, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "gdn_act_pack8": (_I, [_P, _I, _I64, _I, _I, _P, _P, _P]),
+    "gdn_act_unpack8": (_I, [_P, _P, _I, _I64, _I, _I, _P, _P]),
+    "gdn_gated_rmsnorm_ckpt8": (_I, [_P, _P, _I, _P, _F, _I64, _I, _P, _P, _P, _P, _P, _P]),
     "gdn_decode_layer_step": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _P, _P, _P, _P, _P, _F, _F, _F,
                                    _P, _I, _I, _I, _I, _I, _P, _P]),
 }
@@ -268,3 +282,250 @@ def gdn_gated_rmsnorm(x, z, w, eps=1e-6, y=None):
         _ptr(x), _ptr(z), _dt(x), _ptr(w), float(eps), x.numel() // dim, dim, _ptr(y),
         _stream(x)))
     return y
+
+
+# ---------------------------------------------------------------- training: backward passes ----
+
+def _ws(need, given, device):
+    """The workspace to pass and its bytes: the caller's, or a new one of `need` bytes."""
+    w = torch.empty(need, dtype=torch.uint8, device=device) if given is None else given
+    return w, w.numel() * w.element_size()
+
+
+def _kept(x):
+    """An activation, or its 8-bit checkpoint (codes, scales): (tensor, scales or None)."""
+    if isinstance(x, (tuple, list)):
+        codes, scales = x
+        if codes.dtype != torch.int8 or scales.dtype != torch.float32:
+            raise TypeError("a checkpoint is (int8 codes, fp32 scales)")
+        if not scales.numel() or codes.numel() % scales.numel():
+            if codes.numel() or scales.numel():
+                raise ValueError("codes and scales of a checkpoint do not match")
+        return codes, scales
+    return x, None
+
+
+def _run(name, device, *args):
+    """Calls the entry point on `device` and on torch's current stream there (the last argument)."""
+    with torch.cuda.device(device):
+        stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        _check(name, getattr(load(), name)(*args, stream))
+
+
+def _all_cuda(*ts):
+    """Contiguous CUDA tensors of one device (None is skipped)."""
+    _cuda(*ts)
+    if len({t.device for t in ts if t is not None}) > 1:
+        raise ValueError("tensors must be on one device")
+
+
+def _same(dtype, *ts):
+    if any(t is not None and t.dtype != dtype for t in ts):
+        raise TypeError(f"expected tensors of {dtype}")
+
+
+def _shape(shape, *ts):
+    if any(t is not None and tuple(t.shape) != tuple(shape) for t in ts):
+        raise ValueError(f"expected tensors of shape {tuple(shape)}")
+
+
+def chunk_bwd_workspace_size(dtype, N, B, T, Hk, Hv, dk, dv, chunk=64):
+    """Bytes of workspace for gdn_chunk_bwd with activations of the torch dtype."""
+    dt = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}[dtype]
+    return int(load().gdn_chunk_bwd_workspace_size(dt, N, B, T, Hk, Hv, dk, dv, chunk))
+
+
+def gdn_chunk_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, cu_seqlens=None,
+                  dfinal_state=None, chunk=64, dq=None, dk=None, dv=None, dg=None, dbeta=None,
+                  dinitial_state=None, output_dinitial_state=None, workspace=None):
+    """Gradients of gdn_chunk_fwd: (dq, dk, dv, dg, dbeta, dinitial_state).
+
+    q, k, v (possibly strided views), g, beta, scale, initial_state, cu_seqlens as given to the forward;
+    dout [B, T, Hv, dv]; dfinal_state [N, Hv, dv, dk] fp32 or None (zero).  dg and dbeta are of
+    the activations' dtype.  dinitial_state is computed when initial_state is given, unless
+    output_dinitial_state says otherwise; else None.
+    """
+    _all_cuda(g, beta, dout, initial_state, cu_seqlens, dfinal_state, dq, dk, dv, dg, dbeta,
+              dinitial_state, workspace)
+    if any(t.device != g.device for t in (q, k, v)):
+        raise ValueError("tensors must be on one device")
+    qs, ks, vs = _tok_stride(q), _tok_stride(k), _tok_stride(v)
+    if qs is None or ks is None or vs is None:
+        raise ValueError("q, k, v must be CUDA [B, T, H, d] tensors with each token's heads packed")
+    B, T, Hk, d_k = q.shape
+    Hv, d_v = v.shape[2], v.shape[3]
+    N = cu_seqlens.numel() - 1 if cu_seqlens is not None else B
+    _same(q.dtype, k, v, dout, dq, dk, dv, dg, dbeta)
+    _same(torch.float32, g, beta, initial_state, dfinal_state, dinitial_state)
+    _same(torch.int32, cu_seqlens)
+    _shape((B, T, Hk, d_k), k, dq, dk)
+    _shape((B, T, Hv, d_v), v, dout, dv)
+    _shape((B, T, Hv), g, beta, dg, dbeta)
+    _shape((N, Hv, d_v, d_k), initial_state, dfinal_state, dinitial_state)
+    new = lambda t, shape: torch.empty(shape, dtype=q.dtype, device=q.device) if t is None else t  # noqa: E731
+    dq, dk, dv = new(dq, (B, T, Hk, d_k)), new(dk, (B, T, Hk, d_k)), new(dv, (B, T, Hv, d_v))
+    dg, dbeta = new(dg, (B, T, Hv)), new(dbeta, (B, T, Hv))
+    if output_dinitial_state is None:
+        output_dinitial_state = initial_state is not None
+    if dinitial_state is None and output_dinitial_state:
+        dinitial_state = torch.empty((N, Hv, d_v, d_k), dtype=torch.float32, device=q.device)
+    lib, dt = load(), _dt(q)
+    ws, ws_b = _ws(lib.gdn_chunk_bwd_workspace_size(dt, N, B, T, Hk, Hv, d_k, d_v, chunk),
+                   workspace, q.device)
+    _run("gdn_chunk_bwd", q.device,
+        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(g), _ptr(beta), _ptr(dout), dt,
+        float(d_k ** -0.5 if scale is None else scale), _ptr(initial_state), _ptr(dfinal_state),
+        _ptr(cu_seqlens), N, B, T, Hk, Hv, d_k, d_v, chunk, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
+        _ptr(dbeta), _ptr(dinitial_state), _ptr(ws), ws_b)
+    return dq, dk, dv, dg, dbeta, dinitial_state
+
+
+def gdn_gates_bwd(a, b, A_log, dt_bias, dg, dbeta, da=None, db=None, dA_log=None, ddt_bias=None,
+                  workspace=None):
+    """Gradients of gdn_gates: (da, db, dA_log, ddt_bias).  a, b, dg, dbeta: [..., Hv] of one dtype."""
+    _all_cuda(a, b, A_log, dt_bias, dg, dbeta, da, db, dA_log, ddt_bias, workspace)
+    Hv = A_log.numel()
+    _same(a.dtype, b, dg, dbeta, da, db)
+    _same(torch.float32, A_log, dt_bias, dA_log, ddt_bias)
+    _shape(a.shape, b, dg, dbeta, da, db)
+    _shape((Hv,), A_log, dt_bias, dA_log, ddt_bias)
+    if a.shape[-1] != Hv:
+        raise ValueError("the last dimension of a must be the number of heads")
+    da = torch.empty_like(a) if da is None else da
+    db = torch.empty_like(b) if db is None else db
+    dA_log = torch.empty_like(A_log) if dA_log is None else dA_log
+    ddt_bias = torch.empty_like(dt_bias) if ddt_bias is None else ddt_bias
+    n_tok, lib = a.numel() // Hv, load()
+    ws, ws_b = _ws(lib.gdn_gates_bwd_workspace_size(n_tok, Hv), workspace, a.device)
+    _run("gdn_gates_bwd", a.device,
+        _ptr(a), _ptr(b), _dt(a), _ptr(A_log), _ptr(dt_bias), _ptr(dg), _ptr(dbeta), n_tok, Hv,
+        _ptr(da), _ptr(db), _ptr(dA_log), _ptr(ddt_bias), _ptr(ws), ws_b)
+    return da, db, dA_log, ddt_bias
+
+
+def gdn_gated_rmsnorm_bwd(dy, x, z, w, eps=1e-6, dx=None, dz=None, dw=None, workspace=None):
+    """Gradients of gdn_gated_rmsnorm: (dx, dz, dw).
+
+    x and z are the forward's inputs, or their 8-bit checkpoints as (codes, scales) pairs.
+    """
+    (x, xs), (z, zs) = _kept(x), _kept(z)
+    if (xs is None) != (zs is None):
+        raise ValueError("x and z must both be activations or both be checkpoints")
+    _all_cuda(dy, x, xs, z, zs, w, dx, dz, dw, workspace)
+    dim = dy.shape[-1]
+    n_rows = dy.numel() // dim
+    _shape(dy.shape, x, z, dx, dz)
+    _shape((dim,), w, dw)
+    _same(dy.dtype, dx, dz)
+    _same(torch.int8 if xs is not None else dy.dtype, x, z)
+    _same(torch.float32, w, dw)
+    if xs is not None and (xs.numel() != n_rows or zs.numel() != n_rows):
+        raise ValueError("the norm's checkpoints have one scale per row")
+    dx = torch.empty_like(dy) if dx is None else dx
+    dz = torch.empty_like(dy) if dz is None else dz
+    dw = torch.empty_like(w) if dw is None else dw
+    lib = load()
+    ws, ws_b = _ws(lib.gdn_gated_rmsnorm_bwd_workspace_size(n_rows, dim), workspace, dy.device)
+    _run("gdn_gated_rmsnorm_bwd", dy.device,
+        _ptr(dy), _ptr(x), _ptr(xs), _ptr(z), _ptr(zs), _dt(dy), _ptr(w), float(eps), n_rows, dim,
+        _ptr(dx), _ptr(dz), _ptr(dw), _ptr(ws), ws_b)
+    return dx, dz, dw
+
+
+def gdn_causal_conv1d_silu_bwd(dy, x, w, bias=None, cu_seqlens=None, n_l2norm_ch=0, l2norm_group=0,
+                               l2_eps=1e-6, conv_state_in=None, dconv_state_out=None, dx=None,
+                               dw=None, dbias=None, dconv_state_in=None, workspace=None):
+    """Gradients of gdn_causal_conv1d_silu: (dx, dw, dbias, dconv_state_in).
+
+    x [B, T, C] is the forward's input, or its 8-bit checkpoint as a (codes, scales) pair.  dbias is
+    None without bias; dconv_state_in [N, C, K-1] is computed when conv_state_in is given.
+    """
+    x, xs = _kept(x)
+    _all_cuda(dy, x, xs, w, bias, cu_seqlens, conv_state_in, dconv_state_out, dx, dw, dbias,
+              dconv_state_in, workspace)
+    B, T, C = dy.shape
+    K = w.shape[1]
+    N = cu_seqlens.numel() - 1 if cu_seqlens is not None else B
+    _shape((B, T, C), x, dx)
+    _shape((C, K), w, dw)
+    _shape((C,), bias, dbias)
+    _shape((N, C, K - 1), conv_state_in, dconv_state_out, dconv_state_in)
+    _same(dy.dtype, dx)
+    _same(torch.int8 if xs is not None else dy.dtype, x)
+    _same(torch.float32, w, bias, conv_state_in, dconv_state_out, dw, dbias, dconv_state_in)
+    _same(torch.int32, cu_seqlens)
+    group = 0
+    if xs is not None:
+        if xs.shape[:-1] != dy.shape[:-1] or C % xs.shape[-1]:
+            raise ValueError("scales must be [B, T, C / group]")
+        group = C // xs.shape[-1]
+    dx = torch.empty_like(dy) if dx is None else dx
+    dw = torch.empty_like(w) if dw is None else dw
+    dbias = torch.empty_like(bias) if dbias is None and bias is not None else dbias
+    if dconv_state_in is None and conv_state_in is not None:
+        dconv_state_in = torch.empty_like(conv_state_in)
+    lib = load()
+    ws, ws_b = _ws(lib.gdn_causal_conv1d_silu_bwd_workspace_size(B, T, C, K), workspace, dy.device)
+    _run("gdn_causal_conv1d_silu_bwd", dy.device,
+        _ptr(dy), _ptr(x), _ptr(xs), group, _dt(dy), _ptr(w), _ptr(bias), B, T, C, K,
+        _ptr(cu_seqlens), N, n_l2norm_ch, l2norm_group, float(l2_eps), _ptr(conv_state_in),
+        _ptr(dconv_state_out), _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dconv_state_in), _ptr(ws),
+        ws_b)
+    return dx, dw, dbias, dconv_state_in
+
+
+# ------------------------------------------------------- training: 8-bit activation checkpoints ----
+
+def gdn_act_pack8(x, group=128, codes=None, scales=None):
+    """x [..., dim] -> (codes int8 of x's shape, scales fp32 [..., dim / group])."""
+    _all_cuda(x, codes, scales)
+    dim = x.shape[-1]
+    if group < 1 or dim % group:
+        raise ValueError("group must divide the last dimension")
+    codes = torch.empty(x.shape, dtype=torch.int8, device=x.device) if codes is None else codes
+    if scales is None:
+        scales = torch.empty((*x.shape[:-1], dim // group), dtype=torch.float32, device=x.device)
+    _shape(x.shape, codes)
+    _shape((*x.shape[:-1], dim // group), scales)
+    _same(torch.int8, codes)
+    _same(torch.float32, scales)
+    _run("gdn_act_pack8", x.device, _ptr(x), _dt(x), x.numel() // dim, dim, group, _ptr(codes),
+         _ptr(scales))
+    return codes, scales
+
+
+def gdn_act_unpack8(codes, scales, dtype=torch.bfloat16, x=None):
+    """The values that (codes, scales) of gdn_act_pack8 stand for, as a tensor of `dtype`."""
+    _all_cuda(codes, scales, x)
+    _same(torch.int8, codes)
+    _same(torch.float32, scales)
+    dim = codes.shape[-1]
+    if codes.shape[:-1] != scales.shape[:-1] or dim % scales.shape[-1]:
+        raise ValueError("scales must be [..., dim / group]")
+    x = torch.empty(codes.shape, dtype=dtype, device=codes.device) if x is None else x
+    _shape(codes.shape, x)
+    _run("gdn_act_unpack8", codes.device,
+        _ptr(codes), _ptr(scales), _dt(x), codes.numel() // dim, dim, dim // scales.shape[-1],
+        _ptr(x))
+    return x
+
+
+def gdn_gated_rmsnorm_ckpt8(x, z, w, eps=1e-6, y=None):
+    """gdn_gated_rmsnorm that keeps 8-bit checkpoints: (y, (x codes, scales), (z codes, scales)).
+
+    The pairs go to gdn_gated_rmsnorm_bwd; y may be x (in place).
+    """
+    _all_cuda(x, z, w, y)
+    dim = x.shape[-1]
+    y = torch.empty_like(x) if y is None else y
+    _shape(x.shape, z, y)
+    _shape((dim,), w)
+    _same(x.dtype, z, y)
+    _same(torch.float32, w)
+    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)  # noqa: E731
+    xc, zc = new(x.shape, torch.int8), new(x.shape, torch.int8)
+    xs, zs = new((*x.shape[:-1], 1), torch.float32), new((*x.shape[:-1], 1), torch.float32)
+    _run("gdn_gated_rmsnorm_ckpt8", x.device,
+        _ptr(x), _ptr(z), _dt(x), _ptr(w), float(eps), x.numel() // dim, dim, _ptr(y), _ptr(xc),
+        _ptr(xs), _ptr(zc), _ptr(zs))
+    return y, (xc, xs), (zc, zs)

@@ -274,6 +274,118 @@ gdn_status gdn_decode_layer_step(const void* mix, const void* a, const void* b, 
 gdn_status gdn_gated_rmsnorm(const void* x, const void* z, gdn_dtype dtype, const float* w,
                              float eps, int64_t n_rows, int dim, void* y, void* stream);
 
+/* ---------------------------------------------------------------- training: backward passes ----
+ *
+ * Shared conventions.  Gradients have the type of what they are gradients of, except dg and dbeta of
+ * the rule and of the gates, which are of `dtype` (as the layer's a and b are): with bf16 operands they
+ * carry the operands' rounding, and fp32 storage would hold noise.  Sums over tokens (dw, dbias,
+ * dA_log, ddt_bias) are fp32, added in a fixed order: the same call on the same device gives the same
+ * bits.  `workspace` is device scratch, 256-byte aligned, of at least the matching _workspace_size()
+ * bytes; its contents on entry are ignored; calls that may overlap on the GPU need separate ones (two
+ * captured graphs too).  Gradients are written, not accumulated.  No output may overlap an input,
+ * another output or the workspace.
+ */
+
+/*
+ * gdn_chunk_bwd -- gradients of gdn_chunk_fwd ([P2] §2.2: the chunked mode is the training path).  The
+ * forward's intermediate states are recomputed from its inputs; nothing is kept from the forward.
+ * q, k, v, strides, g, beta, dtype, scale, cu_seqlens, N, B, T, Hk, Hv, dk, dv, chunk, initial_state:
+ *                  the forward's (as gdn_chunk_fwd_strided); chunk changes no result beyond rounding.
+ * dout           : [B, T, Hv, dv] dtype, gradient of out.
+ * dfinal_state   : [N, Hv, dv, dk] fp32 or NULL (zero), gradient of final_state.
+ * dq, dk_out     : [B, T, Hk, dk] dtype, dense; summed over the v-heads that share a k-head.
+ * dv_out         : [B, T, Hv, dv] dtype, dense.
+ * dg, dbeta      : [B, T, Hv] dtype.
+ * dinitial_state : [N, Hv, dv, dk] fp32 or NULL (not written).
+ * Supported: what gdn_chunk_fwd supports.  Tokens behind the last sequence (cu_seqlens[N] < T) are
+ * neither read nor written.  A malformed cu_seqlens lands in the workspace's status word
+ * (gdn_workspace_status).  All pointers but dg, dbeta and cu_seqlens 16-byte aligned.
+ */
+size_t gdn_chunk_bwd_workspace_size(gdn_dtype dtype, int N, int B, int64_t T, int Hk, int Hv,
+                                    int dk, int dv, int chunk);
+gdn_status gdn_chunk_bwd(const void* q, int64_t q_tok_stride, const void* k, int64_t k_tok_stride,
+                         const void* v, int64_t v_tok_stride, const float* g, const float* beta,
+                         const void* dout, gdn_dtype dtype, float scale,
+                         const float* initial_state, const float* dfinal_state,
+                         const int32_t* cu_seqlens, int N, int B, int64_t T, int Hk, int Hv, int dk,
+                         int dv, int chunk, void* dq, void* dk_out, void* dv_out, void* dg,
+                         void* dbeta, float* dinitial_state, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_gates_bwd -- gradients of gdn_gates:
+ *     da = -dg exp(A_log) sigmoid(a + dt_bias)      db = dbeta beta (1 - beta)
+ *     dA_log = sum over tokens of dg g              ddt_bias = sum over tokens of da
+ * a, b, dg, dbeta, da, db : [n_tok, Hv] dtype.   A_log, dt_bias, dA_log, ddt_bias : [Hv] fp32.
+ * n_tok = 0 writes zeros to dA_log and ddt_bias.
+ */
+size_t gdn_gates_bwd_workspace_size(int64_t n_tok, int Hv);
+gdn_status gdn_gates_bwd(const void* a, const void* b, gdn_dtype dtype, const float* A_log,
+                         const float* dt_bias, const void* dg, const void* dbeta, int64_t n_tok,
+                         int Hv, void* da, void* db, float* dA_log, float* ddt_bias,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_gated_rmsnorm_bwd -- gradients of gdn_gated_rmsnorm.
+ * dy, dx, dz     : [n_rows, dim] dtype.   w, dw : [dim] fp32.
+ * x, z           : [n_rows, dim] dtype, the forward's inputs -- or, with x_scales and z_scales set (both or
+ *                  neither), their 8-bit checkpoints: int8 codes [n_rows, dim] with one fp32 scale
+ *                  per row, as gdn_gated_rmsnorm_ckpt8 or gdn_act_pack8 (group = dim) write them.
+ * Supported dims as gdn_gated_rmsnorm; dy, x, z, dx, dz 16-byte aligned.  n_rows = 0 writes zeros to dw.
+ */
+size_t gdn_gated_rmsnorm_bwd_workspace_size(int64_t n_rows, int dim);
+gdn_status gdn_gated_rmsnorm_bwd(const void* dy, const void* x, const float* x_scales,
+                                 const void* z, const float* z_scales, gdn_dtype dtype,
+                                 const float* w, float eps, int64_t n_rows, int dim, void* dx,
+                                 void* dz, float* dw, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * gdn_causal_conv1d_silu_bwd -- gradients of gdn_causal_conv1d_silu, whose arguments it shares.
+ * dy, dx          : [B, T, C] dtype.
+ * x               : [B, T, C] dtype, the forward's input -- or, with x_scales set, its 8-bit checkpoint:
+ *                   int8 codes [B, T, C] and fp32 scales [B, T, C / x_group] as gdn_act_pack8 writes
+ *                   them (x_group is not read otherwise).
+ * dw              : [C, K] fp32.   dbias : [C] fp32, NULL exactly when bias is.
+ * conv_state_in   : as given to the forward, or NULL (zero history).
+ * dconv_state_out : [N, C, K-1] fp32 gradient of the history left behind, or NULL (zero).
+ * dconv_state_in  : [N, C, K-1] fp32 or NULL (not written).
+ * Supported: as gdn_causal_conv1d_silu.  dx of tokens behind the last sequence is not written.
+ */
+size_t gdn_causal_conv1d_silu_bwd_workspace_size(int B, int64_t T, int C, int K);
+gdn_status gdn_causal_conv1d_silu_bwd(const void* dy, const void* x, const float* x_scales,
+                                      int x_group, gdn_dtype dtype, const float* w,
+                                      const float* bias, int B, int64_t T, int C, int K,
+                                      const int32_t* cu_seqlens, int N, int n_l2norm_ch,
+                                      int l2norm_group, float l2_eps, const float* conv_state_in,
+                                      const float* dconv_state_out, void* dx, float* dw,
+                                      float* dbias, float* dconv_state_in, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------- training: 8-bit activation checkpoints ----
+ *
+ * gdn_act_pack8 / gdn_act_unpack8 -- an activation kept between forward and backward in 8 bits.  Each
+ * group of `group` consecutive channels with largest magnitude m holds codes rint(x * fl(127 / m)) (half
+ * to even) in int8 and one fp32 scale fl(m / 127); a code stands for code * scale, off by at most
+ * m / 254.  m below 2^-100 counts as zero; a group with an infinity or a NaN reads back as NaN.
+ * x              : [n_rows, dim] dtype.   codes : [n_rows, dim] int8.   scales : [n_rows, dim / group].
+ * Supported: group in {8, 16, 32, 64, 128, 256}, dim a multiple of it; x, codes 16-byte aligned.
+ */
+gdn_status gdn_act_pack8(const void* x, gdn_dtype dtype, int64_t n_rows, int dim, int group,
+                         int8_t* codes, float* scales, void* stream);
+gdn_status gdn_act_unpack8(const int8_t* codes, const float* scales, gdn_dtype dtype,
+                           int64_t n_rows, int dim, int group, void* x, void* stream);
+
+/*
+ * gdn_gated_rmsnorm_ckpt8 -- gdn_gated_rmsnorm that also writes the 8-bit checkpoints of x and z (one
+ * group per row) in the same pass, for gdn_gated_rmsnorm_bwd.  y is gdn_gated_rmsnorm's and may be x
+ * itself, as after gdn_chunk_fwd: the checkpoint is then what remains of x.
+ */
+gdn_status gdn_gated_rmsnorm_ckpt8(const void* x, const void* z, gdn_dtype dtype, const float* w,
+                                   float eps, int64_t n_rows, int dim, void* y, int8_t* x_codes,
+                                   float* x_scales, int8_t* z_codes, float* z_scales,
+                                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif
