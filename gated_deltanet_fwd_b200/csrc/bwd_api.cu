@@ -64,6 +64,10 @@ int64_t conv_parts(int64_t n_tok, int C) {
   const int64_t need = (n_tok + 15) / 16;
   return need < 1 ? 1 : need < most ? need : most;
 }
+// The shape of the tensor-core backward pass of the rule, as of the forward.
+bool tensor_cores(gdn_dtype dtype, int dk, int dv, int chunk) {
+  return dtype == GDN_BF16 && dk == 128 && dv == 128 && chunk == 64;
+}
 bool norm_dim_ok(int dim) {
   return dim == 8 || dim == 16 || dim == 32 || dim == 64 || dim == 128 || dim == 256;
 }
@@ -271,9 +275,12 @@ gdn_status gdn_causal_conv1d_silu_bwd(const void* dy, const void* x, const float
 size_t gdn_chunk_bwd_workspace_size(gdn_dtype dtype, int N, int B, int64_t T, int Hk, int Hv,
                                     int dk, int dv, int chunk) {
   (void)Hk;
-  (void)dtype;
   if (N < 0 || B < 0 || T < 0 || Hv < 1 || dk < 1 || dv < 1 || chunk < 1) return 256;
-  return round256(bwd::simt_workspace_bytes(N, (int64_t)B * T, Hv, dk, dv, chunk));
+  const int64_t n_tok = (int64_t)B * T;
+  if (n_tok == 0) return bwd::HEADER;
+  return round256(tensor_cores(dtype, dk, dv, chunk)
+                      ? bwd::tc_workspace_bytes(N, n_tok, Hv)
+                      : bwd::simt_workspace_bytes(N, n_tok, Hv, dk, dv, chunk));
 }
 
 gdn_status gdn_chunk_bwd(const void* q, int64_t q_tok_stride, const void* k, int64_t k_tok_stride,
@@ -336,7 +343,8 @@ gdn_status gdn_chunk_bwd(const void* q, int64_t q_tok_stride, const void* k, int
   a.status = reinterpret_cast<int*>(workspace);
   const cudaStream_t s = as_stream(stream);
   if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return GDN_ERR_CUDA;
-  return from_cuda(bwd::launch_simt(a, s));
+  return from_cuda(n_tok > 0 && tensor_cores(dtype, dk, dv, chunk) ? bwd::launch_tc(a, s)
+                                                                   : bwd::launch_simt(a, s));
 }
 
 }  // extern "C"

@@ -1,0 +1,619 @@
+// bwd_chain.cu -- the two serial walks of the tensor-core backward pass (bwd_tc.cuh): one CTA per
+// (sequence, v-head) carries the fp32 state S (forward) or its gradient dS (backward) through the
+// chunks in tensor memory.
+//
+// Tensor-memory lane j is value row j, as in chunk_chain.cu, so the carried matrix and the epilogue
+// results are A operands from tensor memory and every B operand is a TMA-loaded tile:
+//   forward, chunk by chunk from the first (X' = -(S K^T) Gamma):
+//     D  = S_bf16 K^T          N 64,  K 128   critical
+//     E  = V^T T~^T            N 64,  K 64    early
+//     E += X' T~^T             N 64,  K 64    critical
+//     S  = Gamma_63 S + (beta d E) K      N 128, K 64   critical
+//   backward, from the last chunk (X = beta (scale D2 + d D)):
+//     D  = dS_bf16 K^T         N 64,  K 128   critical
+//     D2 = dO^T P              N 64,  K 64    early
+//     W  = X T~                N 64,  K 64    critical: dW^T = dV^T
+//     dS = Gamma_63 dS + (scale Gamma dO^T) Q - (Gamma W) K     N 128, K 64 twice, the second critical
+// Warp roles (320 threads): warps 0-3 the critical epilogues; warps 4-7 the side work (the carried matrix
+// scaled by Gamma_63, its bf16 copy to the workspace in the same pass over it, scale Gamma dO^T, and
+// U or dv to memory); warp 8 the TMA producer; warp 9 the MMA issuer.  What bounds it is the latency of
+// the critical sequence of one chunk (see the figures in the design notes), not traffic.
+//
+// A chunk that ends inside a tile: rows of K, Q, V, dO behind the sequence end hold whatever follows in
+// memory, so the producer waits for that chunk's copies itself, clears those rows and only then
+// publishes the stage.  Waits are bounded: one that runs out records GDN_ERR_TIMEOUT, and from
+// then on every role skips its work but keeps the barrier sequence, so the CTA leaves together with
+// nothing in flight.
+#include "bwd_tc.cuh"
+#include "ptx.cuh"
+
+namespace gdn {
+namespace bwd {
+namespace {
+
+using namespace ptx;
+
+constexpr int THREADS = 320;
+constexpr int W_PROD = 8;  // warp 9 issues the MMAs
+
+// shared memory, from a 1024-aligned base; a stage holds one chunk's tiles: K, [Q,] V or dO, T~ [and P],
+// the record.  64-row tiles are two 64-column halves 8192 bytes apart.
+template <bool BACK>
+struct Sm {
+  static constexpr uint32_t K = 0, Q = 16384, X = BACK ? 32768 : 16384, TP = X + 16384,
+                            GD = TP + (BACK ? 16384 : 8192), STAGE = GD + 1024;
+  static constexpr uint32_t TX = GD + GD_BYTES;  // bytes of a full stage
+  static constexpr int STAGES = BACK ? 2 : 3;
+  static constexpr uint32_t BAR = STAGES * STAGE, BYTES = BAR + 256 + 1024;
+  static_assert(STAGE % 1024 == 0 && BYTES <= 232448, "stage layout");
+};
+
+enum { B_FULL0 = 0, B_EMPTY0 = 3, B_FIX = 6, B_K = 7, B_U = 8, B_S = 9, B_DRAIN = 10, B_N = 11 };
+
+// named barriers: hand-offs to the MMA issuer and between the two groups
+enum { NB_X = 1, NB_U = 2, NB_S = 3, NB_SR = 4, NB_G = 5 };
+constexpr int NB_ALL = 288;  // both groups + issuer warp
+constexpr int NB_EI = 160;   // one group + issuer warp
+constexpr int NB_EH = 256;   // both groups
+
+// tensor-memory columns
+constexpr uint32_t TM_S = 0, TM_D = 128, TM_D2 = 192, TM_U = 256, TM_SB = 320, TM_X = 384,
+                   TM_UT = 416, TM_UD = 448;
+
+struct ChainParams {
+  const float* S_in;   // initial state, or gradient of the final one; null: zero
+  float* S_out;        // gradient of the initial state (backward only); null: not wanted
+  const int32_t* cu;
+  unsigned char* ws;
+  __nv_bfloat16* dv;   // backward only
+  int* status;
+  int64_t T;
+  TcLayout at;
+  float scale;
+  int N, Hk, Hv;
+};
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ uint64_t dadd(uint64_t d, uint32_t bytes) {
+  return d + (uint64_t)(bytes >> 4);
+}
+__device__ __forceinline__ void ld64(uint32_t taddr, float (&v)[64]) {
+  tmem_ld16(taddr + 0, *reinterpret_cast<float(*)[16]>(v + 0));
+  tmem_ld16(taddr + 16, *reinterpret_cast<float(*)[16]>(v + 16));
+  tmem_ld16(taddr + 32, *reinterpret_cast<float(*)[16]>(v + 32));
+  tmem_ld16(taddr + 48, *reinterpret_cast<float(*)[16]>(v + 48));
+}
+// 32 bytes to global memory, 32-byte aligned: a whole sector per thread
+__device__ __forceinline__ void store32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+template <bool BACK>
+__global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
+    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_q,
+    const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_tp,
+    const ChainParams P) {
+  using L_ = Sm<BACK>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L_::BAR);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L_::BAR + B_N * 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::BAR + B_N * 8 + 4);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.x % P.Hv, n = blockIdx.x / P.Hv;
+  const int hk = h / (P.Hv / P.Hk);
+  int64_t s_beg, s_end, slot0;
+  if (!seq_range(P.cu, P.T, n, tm::C, s_beg, s_end, slot0)) {
+    if (tid == 0) report(P.status, GDN_ERR_DEVICE_ARG);
+    return;  // nothing allocated yet
+  }
+  const size_t sidx = ((size_t)n * P.Hv + h) * tm::STATE_FLOATS;
+  const int nch = (int)((s_end - s_beg + tm::C - 1) / tm::C);
+  if (nch == 0) {  // empty sequence: the gradient passes through
+    if (BACK && P.S_out)
+      for (int e = tid; e < tm::D * tm::D; e += THREADS)
+        P.S_out[sidx + e] = P.S_in ? P.S_in[sidx + e] : 0.0f;
+    return;
+  }
+  // step i works on chunk chunk_of(i)
+  auto chunk_of = [&](int i) { return BACK ? nch - 1 - i : i; };
+  auto rows_of = [&](int c) { return (int)min((int64_t)tm::C, s_end - s_beg - (int64_t)tm::C * c); };
+
+  if (tid == 0) {
+    for (int i = 0; i < L_::STAGES; ++i) {
+      mbar_init(&bars[B_FULL0 + i], 1);
+      mbar_init(&bars[B_EMPTY0 + i], 1);
+    }
+    for (int i = B_FIX; i < B_N; ++i) mbar_init(&bars[i], 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto fail = [&](int code) {
+    report(P.status, code);
+    *abort_flag = 1;
+  };
+  // a bounded wait, skipped once the CTA is aborting
+  auto wait = [&](int b, uint32_t parity) -> bool {
+    if (*abort_flag) return false;
+    if (mbar_wait(&bars[b], parity)) return true;
+    fail(GDN_ERR_TIMEOUT);
+    return false;
+  };
+  // the same for a whole warp: one answer, so that its lanes stay together
+  auto wait_w = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+  auto wait_full = [&](int i) {
+    return wait_w(B_FULL0 + i % L_::STAGES, (uint32_t)(i / L_::STAGES) & 1);
+  };
+  auto record = [&](int i) {
+    return reinterpret_cast<const float*>(smem + (i % L_::STAGES) * L_::STAGE + L_::GD);
+  };
+
+  if (warp < 4) {
+    // -------------------------------------------------------------- critical epilogues -------
+    const int j = 32 * warp + lane;  // value row = tensor-memory lane
+    const uint32_t lo = (uint32_t)(32 * warp) << 16;
+    {
+      const float* src = P.S_in ? P.S_in + sidx + (size_t)j * tm::D : nullptr;
+#pragma unroll
+      for (int blk = 0; blk < 4; ++blk) {  // 32 columns at a time
+        float v[32];
+#pragma unroll
+        for (int q4 = 0; q4 < 8; ++q4) {
+          const float4 f = src ? __ldg(reinterpret_cast<const float4*>(src + 32 * blk) + q4)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[4 * q4] = f.x;
+          v[4 * q4 + 1] = f.y;
+          v[4 * q4 + 2] = f.z;
+          v[4 * q4 + 3] = f.w;
+        }
+        tmem_st16(tmem + lo + TM_S + 32 * blk, *reinterpret_cast<float(*)[16]>(v));
+        tmem_st16(tmem + lo + TM_S + 32 * blk + 16, *reinterpret_cast<float(*)[16]>(v + 16));
+        uint32_t pk[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) pk[q] = pack2(v[2 * q], v[2 * q + 1]);
+        tmem_st16u(tmem + lo + TM_SB + 16 * blk, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      named_bar_arrive(NB_SR, NB_EH);  // the side group may take the matrix over
+      named_bar(NB_S, NB_ALL);
+    }
+    for (int i = 0; i < nch; ++i) {
+      const float* gd = record(i);
+      wait_full(i);  // the chunk's record is visible to this thread
+      // ---- X'
+      if (wait_w(B_K, i & 1)) {
+        tc_fence_after();
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float d[32], d2[32];
+          tmem_ld16(tmem + lo + TM_D + 32 * hh, *reinterpret_cast<float(*)[16]>(d));
+          tmem_ld16(tmem + lo + TM_D + 32 * hh + 16, *reinterpret_cast<float(*)[16]>(d + 16));
+          if (BACK) {
+            tmem_ld16(tmem + lo + TM_D2 + 32 * hh, *reinterpret_cast<float(*)[16]>(d2));
+            tmem_ld16(tmem + lo + TM_D2 + 32 * hh + 16, *reinterpret_cast<float(*)[16]>(d2 + 16));
+          }
+          tmem_ld_wait();
+          uint32_t pk[16];
+#pragma unroll
+          for (int q4 = 0; q4 < 8; ++q4) {
+            const float* x = d + 4 * q4;
+            if (!BACK) {
+              const float4 gm = *reinterpret_cast<const float4*>(gd + 32 * hh + 4 * q4);
+              pk[2 * q4] = pack2(-gm.x * x[0], -gm.y * x[1]);
+              pk[2 * q4 + 1] = pack2(-gm.z * x[2], -gm.w * x[3]);
+            } else {
+              const float* y = d2 + 4 * q4;
+              const float4 dd = *reinterpret_cast<const float4*>(gd + 64 + 32 * hh + 4 * q4);
+              const float4 be = *reinterpret_cast<const float4*>(gd + 128 + 32 * hh + 4 * q4);
+              pk[2 * q4] = pack2(be.x * fmaf(dd.x, x[0], P.scale * y[0]),
+                                 be.y * fmaf(dd.y, x[1], P.scale * y[1]));
+              pk[2 * q4 + 1] = pack2(be.z * fmaf(dd.z, x[2], P.scale * y[2]),
+                                     be.w * fmaf(dd.w, x[3], P.scale * y[3]));
+            }
+          }
+          tmem_st16u(tmem + lo + TM_X + 16 * hh, pk);
+        }
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      named_bar_arrive(NB_X, NB_EI);
+      // ---- the update's operand (and U)
+      if (wait_w(B_U, i & 1)) {
+        tc_fence_after();
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float u[32];
+          tmem_ld32(tmem + lo + TM_U + 32 * hh, u);
+          uint32_t pk[16], pd[16];
+#pragma unroll
+          for (int q4 = 0; q4 < 8; ++q4) {
+            const float* x = u + 4 * q4;
+            if (!BACK) {
+              const float4 dd = *reinterpret_cast<const float4*>(gd + 64 + 32 * hh + 4 * q4);
+              const float4 be = *reinterpret_cast<const float4*>(gd + 128 + 32 * hh + 4 * q4);
+              const float u0 = be.x * x[0], u1 = be.y * x[1], u2 = be.z * x[2], u3 = be.w * x[3];
+              pk[2 * q4] = pack2(u0, u1);
+              pk[2 * q4 + 1] = pack2(u2, u3);
+              pd[2 * q4] = pack2(u0 * dd.x, u1 * dd.y);
+              pd[2 * q4 + 1] = pack2(u2 * dd.z, u3 * dd.w);
+            } else {
+              const float4 gm = *reinterpret_cast<const float4*>(gd + 32 * hh + 4 * q4);
+              pd[2 * q4] = pack2(-gm.x * x[0], -gm.y * x[1]);
+              pd[2 * q4 + 1] = pack2(-gm.z * x[2], -gm.w * x[3]);
+            }
+          }
+          if (!BACK) tmem_st16u(tmem + lo + TM_UT + 16 * hh, pk);
+          tmem_st16u(tmem + lo + TM_UD + 16 * hh, pd);
+        }
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      // a full barrier, not an arrival: the group then never runs a barrier instance ahead of the
+      // issuer, even when an abort makes it skip its waits
+      named_bar(NB_U, NB_ALL);
+      // ---- refresh of the bf16 copy (not after the last chunk)
+      const bool s_ok = wait_w(B_S, i & 1);
+      if (i + 1 < nch) {
+        if (s_ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float v[64];
+            ld64(tmem + lo + TM_S + 64 * hh, v);
+            tmem_ld_wait();
+            uint32_t pk[32];
+#pragma unroll
+            for (int q = 0; q < 32; ++q) pk[q] = pack2(v[2 * q], v[2 * q + 1]);
+            tmem_st16u(tmem + lo + TM_SB + 32 * hh, *reinterpret_cast<uint32_t(*)[16]>(pk));
+            tmem_st16u(tmem + lo + TM_SB + 32 * hh + 16,
+                       *reinterpret_cast<uint32_t(*)[16]>(pk + 16));
+          }
+        }
+        tc_fence_before();
+        named_bar_arrive(NB_SR, NB_EH);  // the matrix is read: the side group may scale it
+        tmem_st_wait();
+        tc_fence_before();
+        named_bar(NB_S, NB_ALL);
+      }
+    }
+  } else if (warp < 8) {
+    // -------------------------------------------------------------- side group (warps 4-7) ---
+    const int j = 32 * (warp - 4) + lane;
+    const uint32_t lo = (uint32_t)(32 * (warp - 4)) << 16;
+    // The carried matrix entering step i: its bf16 copy to the workspace, then scaled by Gamma_63 in
+    // tensor memory (after the critical group has read it).  Backward: also scale Gamma dO^T.
+    auto take = [&](int i) {
+      named_bar(NB_SR, NB_EH);
+      tc_fence_after();
+      if (!wait_full(i)) return;
+      const float* gd = record(i);
+      const float gl = gd[63];
+      if (BACK) {  // rows of dO in pairs: the A operand holds two consecutive tokens per column
+        const unsigned char* x = smem + (i % L_::STAGES) * L_::STAGE + L_::X + (j >> 6) * 8192;
+        const int c8 = (j & 63) >> 3, cb = (j & 7) * 2;
+        uint32_t pk[32];
+#pragma unroll
+        for (int q = 0; q < 32; ++q) {
+          const int r = 2 * q;
+          const uint32_t o0 = *reinterpret_cast<const uint16_t*>(
+              x + r * 128 + ((c8 ^ (r & 7)) << 4) + cb);
+          const uint32_t o1 = *reinterpret_cast<const uint16_t*>(
+              x + (r + 1) * 128 + ((c8 ^ ((r + 1) & 7)) << 4) + cb);
+          const float2 gm = *reinterpret_cast<const float2*>(gd + r);
+          pk[q] = pack2(P.scale * gm.x * __uint_as_float(o0 << 16),
+                        P.scale * gm.y * __uint_as_float(o1 << 16));
+        }
+        tmem_st16u(tmem + lo + TM_UT, *reinterpret_cast<uint32_t(*)[16]>(pk));
+        tmem_st16u(tmem + lo + TM_UT + 16, *reinterpret_cast<uint32_t(*)[16]>(pk + 16));
+      }
+      unsigned char* tile = P.ws + (BACK ? P.at.ds : P.at.s) +
+                            ((size_t)(slot0 + chunk_of(i)) * P.Hv + h) * 32768 + j * 128;
+#pragma unroll
+      for (int hh = 0; hh < 4; ++hh) {
+        float v[32];
+        tmem_ld32(tmem + lo + TM_S + 32 * hh, v);
+        uint32_t pk[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) pk[q] = pack2(v[2 * q], v[2 * q + 1]);
+#pragma unroll
+        for (int q = 0; q < 32; ++q) v[q] *= gl;
+        tmem_st16(tmem + lo + TM_S + 32 * hh, *reinterpret_cast<float(*)[16]>(v));
+        tmem_st16(tmem + lo + TM_S + 32 * hh + 16, *reinterpret_cast<float(*)[16]>(v + 16));
+        unsigned char* dst = tile + (hh >> 1) * 16384 + (hh & 1) * 64;
+        store32(dst, pk);
+        store32(dst + 32, pk + 8);
+      }
+      tmem_st_wait();
+    };
+    named_bar_arrive(NB_S, NB_ALL);
+    take(0);
+    tc_fence_before();
+    if (BACK) named_bar_arrive(NB_G, NB_EI);
+    for (int i = 0; i < nch; ++i) {
+      named_bar(NB_U, NB_ALL);  // matrix scaled; a full barrier (see the other group)
+      tc_fence_after();
+      const int c = chunk_of(i);
+      uint32_t ob[32];
+      bool ok = __all_sync(0xffffffffu, !*abort_flag) != 0;
+      if (!BACK) {  // U^T of the chunk, written by the critical group before the barrier
+        if (ok) {
+          float t[32];
+          tmem_ld32(tmem + lo + TM_UT, t);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) ob[q] = __float_as_uint(t[q]);
+        }
+      } else {  // dW^T: complete since the critical group has waited for it
+        ok = wait_w(B_U, i & 1) && ok;
+        if (ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float t[32];
+            tmem_ld32(tmem + lo + TM_U + 32 * hh, t);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) ob[16 * hh + q] = pack2(t[2 * q], t[2 * q + 1]);
+          }
+        }
+      }
+      tc_fence_before();
+      if (i + 1 < nch) {
+        named_bar_arrive(NB_S, NB_ALL);  // U / dW read
+        take(i + 1);
+        tc_fence_before();
+        if (BACK) named_bar_arrive(NB_G, NB_EI);
+      }
+      if (!ok) continue;
+      if (!BACK) {
+        unsigned char* dst =
+            P.ws + P.at.u + ((size_t)(slot0 + c) * P.Hv + h) * 16384 + j * 128;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) store32(dst + 32 * q, ob + 8 * q);
+      } else {
+        // lanes j, j ^ 1 swap halves: an even lane stores row 2q at columns j, j + 1, an odd lane row
+        // 2q + 1 at columns j - 1, j -- each warp store two contiguous 64-byte row segments
+        const int64_t t0 = s_beg + (int64_t)tm::C * c;
+        const int L = rows_of(c);
+        const int odd = j & 1;
+        const int64_t rs = (int64_t)P.Hv * tm::D;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(P.dv + (t0 + odd) * rs + h * tm::D + (j & ~1));
+        const uint32_t sel = odd ? 0x7632u : 0x5410u;
+#pragma unroll 8
+        for (int q = 0; q < 32; ++q) {
+          const uint32_t mine = ob[q];
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+          const uint32_t pair = odd ? __byte_perm(other, mine, sel) : __byte_perm(mine, other, sel);
+          if (2 * q + odd < L) *dst = pair;
+          dst += rs;  // two token rows of bf16, counted in 4-byte units
+        }
+      }
+    }
+  } else if (warp == W_PROD) {
+    // -------------------------------------------------------------- TMA producer -------------
+    if (lane == 0) {
+      prefetch_tensormap(&map_k);
+      prefetch_tensormap(&map_x);
+      prefetch_tensormap(&map_tp);
+      if (BACK) prefetch_tensormap(&map_q);
+    }
+    int issued = 0;
+    for (int i = 0; i < nch; ++i) {
+      const int st = i % L_::STAGES, c = chunk_of(i), L = rows_of(c);
+      bool go = true;
+      if (lane == 0) {
+        if (i >= L_::STAGES) go = wait(B_EMPTY0 + st, ((uint32_t)(i / L_::STAGES) & 1) ^ 1);
+        go = go && !*abort_flag;
+      }
+      if (!__shfl_sync(0xffffffffu, (int)go, 0)) break;
+      unsigned char* sp = smem + st * L_::STAGE;
+      // a partial chunk's copies are awaited here, on a barrier of their own
+      const bool part = L < tm::C;
+      uint64_t* fb = part ? &bars[B_FIX] : &bars[B_FULL0 + st];
+      if (lane == 0) {
+        const int32_t t0 = (int32_t)(s_beg + (int64_t)tm::C * c);
+        const size_t sh = (size_t)(slot0 + c) * P.Hv + h;
+        mbar_arrive_expect_tx(fb, L_::TX);
+        tma_load_3d(sp + L_::K, &map_k, fb, 0, hk, t0);
+        tma_load_3d(sp + L_::K + 8192, &map_k, fb, 64, hk, t0);
+        if (BACK) {
+          tma_load_3d(sp + L_::Q, &map_q, fb, 0, hk, t0);
+          tma_load_3d(sp + L_::Q + 8192, &map_q, fb, 64, hk, t0);
+        }
+        tma_load_3d(sp + L_::X, &map_x, fb, 0, h, t0);
+        tma_load_3d(sp + L_::X + 8192, &map_x, fb, 64, h, t0);
+        tma_load_2d(sp + L_::TP, &map_tp, fb, 0, (int32_t)(sh * 128));
+        bulk_load(sp + L_::GD, P.ws + P.at.gd + sh * GD_BYTES, GD_BYTES, fb);
+      }
+      if (part) {  // once per sequence: its last chunk
+        bool ok = mbar_wait(fb, 0);
+        if (!ok && lane == 0) fail(GDN_ERR_TIMEOUT);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          constexpr int TILES = BACK ? 6 : 4;  // 64-row half tiles of K, [Q,] X, one after the other
+          for (int e = lane; e < TILES * (tm::C - L) * 8; e += 32) {
+            const int tile = e / ((tm::C - L) * 8), rest = e - tile * ((tm::C - L) * 8);
+            *reinterpret_cast<uint4*>(sp + tile * 8192 + (L + rest / 8) * 128 + (rest % 8) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_FULL0 + st]);
+        } else {
+          mbar_wait(fb, 0);  // its copies may still be under way
+          break;
+        }
+      }
+      issued = i + 1;
+    }
+    // never leave the CTA with copies still landing in shared memory (each wait bounded)
+    if (lane == 0)
+      for (int i = issued > L_::STAGES ? issued - L_::STAGES : 0; i < issued; ++i)
+        if (!mbar_wait(&bars[B_FULL0 + i % L_::STAGES], (uint32_t)(i / L_::STAGES) & 1))
+          report(P.status, GDN_ERR_TIMEOUT);
+  } else {
+    // -------------------------------------------------------------- MMA issuer ---------------
+    const uint32_t id_k = idesc_bf16(128, 64, 0, 0);             // A tensor memory, B K-major
+    const uint32_t id_e = idesc_bf16(128, 64, 1, BACK ? 1 : 0);  // A smem MN-major
+    const uint32_t id_u = idesc_bf16(128, 64, 0, BACK ? 1 : 0);  // T~^T forward, T~ backward
+    const uint32_t id_s = idesc_bf16(128, 128, 0, 1);            // B = K or Q, MN-major
+    const bool leader = lane == 0;
+    for (int i = 0; i < nch; ++i) {
+      const int st = i % L_::STAGES;
+      const uint32_t sp = sbase + st * L_::STAGE;
+      const bool have = wait_full(i);
+      const uint64_t dK = sdesc_sw128(sp + L_::K, 16, 1024);       // K as K-major B
+      const uint64_t dKn = sdesc_sw128(sp + L_::K, 8192, 1024);    // K as MN-major B
+      const uint64_t dQn = sdesc_sw128(sp + L_::Q, 8192, 1024);
+      const uint64_t dXt = sdesc_sw128(sp + L_::X, 8192, 1024);    // V^T / dO^T as MN-major A
+      const uint64_t dT = BACK ? sdesc_sw128(sp + L_::TP, 8192, 1024)   // T~ as MN-major B
+                               : sdesc_sw128(sp + L_::TP, 16, 1024);    // T~ as K-major B
+      const uint64_t dP = sdesc_sw128(sp + L_::TP + 8192, 8192, 1024);  // P as MN-major B
+      constexpr uint32_t t_step = BACK ? 2048 : 32;
+      if (have && leader && !*abort_flag) {
+        tc_fence_after();
+        // state-independent; its columns were read before the previous chunk's NB_U
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          if (BACK)
+            mma_bf16_ss(tmem + TM_D2, dadd(dXt, ks * 2048), dadd(dP, ks * 2048), id_e, ks > 0);
+          else
+            mma_bf16_ss(tmem + TM_U, dadd(dXt, ks * 2048), dadd(dT, ks * 32), id_e, ks > 0);
+        }
+      }
+      __syncwarp();
+      named_bar(NB_S, NB_ALL);  // bf16 copy in place, U / dW of the previous chunk read
+      const bool go = have && !*abort_flag;
+      if (go && leader) {
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_bf16_ts(tmem + TM_D, tmem + TM_SB + 8 * ks,
+                      dadd(dK, (ks >> 2) * 8192 + (ks & 3) * 32), id_k, ks > 0);
+        mma_commit(&bars[B_K]);
+      }
+      __syncwarp();
+      named_bar(NB_X, NB_EI);  // X' written
+      if (go && leader && !*abort_flag) {
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_bf16_ts(tmem + TM_U, tmem + TM_X + 8 * ks, dadd(dT, ks * t_step), id_u,
+                      !BACK || ks > 0);
+        mma_commit(&bars[B_U]);
+      }
+      __syncwarp();
+      if (BACK) {
+        named_bar(NB_G, NB_EI);  // dS scaled, scale Gamma dO^T written
+        if (go && leader && !*abort_flag) {
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_bf16_ts(tmem + TM_S, tmem + TM_UT + 8 * ks, dadd(dQn, ks * 2048), id_s, 1);
+        }
+        __syncwarp();
+      }
+      named_bar(NB_U, NB_ALL);  // the update's operand written; matrix scaled
+      if (go && leader && !*abort_flag) {
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_bf16_ts(tmem + TM_S, tmem + TM_UD + 8 * ks, dadd(dKn, ks * 2048), id_s, 1);
+        mma_commit(&bars[B_S]);
+        mma_commit(&bars[B_EMPTY0 + st]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) {
+      // every MMA has completed before tensor memory is read back or released
+      mma_commit(&bars[B_DRAIN]);
+      if (!mbar_wait(&bars[B_DRAIN], 0)) fail(GDN_ERR_TIMEOUT);
+    }
+  }
+
+  // the issuer's drain (and any abort) is visible to every thread after this barrier
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (BACK && warp < 4 && P.S_out && !*abort_flag) {
+    const int j = 32 * warp + lane;
+    const uint32_t lo = (uint32_t)(32 * warp) << 16;
+    float* dst = P.S_out + sidx + (size_t)j * tm::D;
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      float v[64];
+      ld64(tmem + lo + TM_S + 64 * hh, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int q4 = 0; q4 < 16; ++q4)
+        reinterpret_cast<float4*>(dst + 64 * hh)[q4] =
+            make_float4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool BACK>
+cudaError_t launch_t(const Args& a, cudaStream_t s) {
+  const int64_t n_tok = (int64_t)a.B * a.T, units = (int64_t)a.N * a.Hv;
+  const int64_t slots = max_slots(a.N, n_tok, tm::C);
+  // TMA coordinates are 32-bit: rows of 64 columns of the state tiles are the largest
+  if (units > 0x7fffffff || n_tok > 0x7fffffff || slots * a.Hv > 0x7fffffff / 256)
+    return cudaErrorInvalidConfiguration;
+  ChainParams p;
+  unsigned char* ws = reinterpret_cast<unsigned char*>(a.ws);
+  p.S_in = BACK ? a.dST : a.S0;
+  p.S_out = BACK ? a.dS0 : nullptr;
+  p.cu = a.cu;
+  p.ws = ws;
+  p.dv = reinterpret_cast<__nv_bfloat16*>(a.dv_);
+  p.status = a.status;
+  p.T = a.T;
+  p.at = tc_layout(slots, a.Hv);
+  p.scale = a.scale;
+  p.N = a.N;
+  p.Hk = a.Hk;
+  p.Hv = a.Hv;
+  CUtensorMap mk, mq, mx, mt;
+  if (!make_tok_map(&mk, a.k, a.Hk, n_tok, a.ts.k) || !make_tok_map(&mq, a.q, a.Hk, n_tok, a.ts.q) ||
+      !make_tok_map(&mx, BACK ? a.dout : a.v, a.Hv, n_tok,
+                    BACK ? (int64_t)a.Hv * tm::D : a.ts.v) ||
+      !make_rows64_map(&mt, ws + p.at.tp, slots * a.Hv * 128, BACK ? 128 : 64))
+    return cudaErrorInvalidValue;
+  const cudaError_t e =
+      cudaFuncSetAttribute(bwd_chain_kernel<BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Sm<BACK>::BYTES);
+  if (e != cudaSuccess) return e;
+  bwd_chain_kernel<BACK><<<(unsigned)units, THREADS, Sm<BACK>::BYTES, s>>>(mk, mq, mx, mt, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_bwd_chain(const Args& a, bool back, cudaStream_t s) {
+  return back ? launch_t<true>(a, s) : launch_t<false>(a, s);
+}
+
+}  // namespace bwd
+}  // namespace gdn

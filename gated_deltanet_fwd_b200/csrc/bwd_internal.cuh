@@ -26,8 +26,15 @@ struct Args {
   int* status;
 };
 
+// Record of a (slot, v-head) on the tensor-core path: Gamma, d, beta (floored), gamma log2 e; 64 fp32 each
+constexpr size_t GD_BYTES = 1024;
+
 size_t simt_workspace_bytes(int N, int64_t n_tok, int Hv, int dk, int dv, int C);
 cudaError_t launch_simt(const Args& a, cudaStream_t s);
+
+// Tensor-core path (bf16, dk = dv = 128, chunk 64, at least one token); see bwd_tc.cuh.
+size_t tc_workspace_bytes(int N, int64_t n_tok, int Hv);
+cudaError_t launch_tc(const Args& a, cudaStream_t s);
 
 // A "slot" is the ordinal of a chunk among all chunks of all sequences, in sequence order.
 __host__ __device__ inline int64_t max_slots(int N, int64_t n_tok, int C) {

@@ -1,0 +1,50 @@
+// bwd_tc.cuh -- layout of the tensor-core backward pass of the chunked rule (bf16, dk = dv = 128,
+// chunks of 64 tokens); the mathematics is in bwd_simt.cu.
+//
+// Four kernels, one after the other on the caller's stream:
+//   chunk_prep<BWD>   (chunk_prep.cu)  per (chunk, k-head): T~, P and the decay records
+//   bwd_chain<false>  (bwd_chain.cu)   per (sequence, v-head), forward: states S entering each chunk, and U
+//   bwd_chain<true>   (bwd_chain.cu)   per (sequence, v-head), backward: dS leaving each chunk, and dv
+//   bwd_grads         (bwd_grads.cu)   per (chunk, k-head): dq, dk, dg, dbeta
+// Only the two chains are serial; they carry the fp32 state (or its gradient) in tensor memory and leave
+// bf16 copies, the same roundings their own next product uses, so that everything else is parallel.
+//
+// T' = diag(beta) T~ (chunk_prep.cu): with X = V - diag(Gamma) K S^T,
+//   U = beta o (T~ X),   dW = T~^T (beta o dU),   dbeta_r = dW_r . U_r / beta_r^2.
+//
+// Workspace from its 256-byte-aligned base (n = slots * Hv, a slot being a chunk's ordinal):
+//   [0, 1024)        status word, padding
+//   TP [n][128][64]  bf16: rows 0..63 T~, rows 64..127 P
+//   GD [n][4][64]    fp32: Gamma, d, beta (floored), gamma log2 e
+//   S  [n][2][128][64]  bf16: two 64-column halves of the state (rows: value index)
+//   DS [n][2][128][64]  bf16: the gradient of the state leaving the chunk
+//   U  [n][128][64]  bf16: U^T (rows: value index, columns: tokens of the chunk)
+#pragma once
+
+#include "bwd_internal.cuh"
+#include "chunk_tm.cuh"
+
+namespace gdn {
+namespace bwd {
+
+struct TcLayout {
+  size_t tp, gd, s, ds, u, end;
+};
+
+__host__ __device__ inline TcLayout tc_layout(int64_t slots, int Hv) {
+  const size_t n = (size_t)slots * Hv;
+  TcLayout l;
+  l.tp = HEADER;
+  l.gd = l.tp + n * 16384;
+  l.s = l.gd + n * GD_BYTES;
+  l.ds = l.s + n * 32768;
+  l.u = l.ds + n * 32768;
+  l.end = l.u + n * 16384;
+  return l;
+}
+
+cudaError_t launch_bwd_chain(const Args& a, bool back, cudaStream_t s);
+cudaError_t launch_bwd_grads(const Args& a, cudaStream_t s);
+
+}  // namespace bwd
+}  // namespace gdn

@@ -21,6 +21,12 @@
 // the four 16 x 16 diagonal blocks, one column per lane, then the off-diagonal blocks by distance
 // with tf32 mma.sync block products).  T', P, Gamma and d go to the workspace (layout in
 // chunk_tm.cuh).
+//
+// For the backward pass (BWD; bwd_tc.cuh) the same inverse is written as T' = diag(beta) T~ with
+// T~ = (I + A~)^{-1}, A~[r,s] = e^{gamma_r - gamma_s} beta_s k_r.k_s: T~ has an exact unit diagonal, so
+// its bf16 copy loses only what the small off-diagonal entries lose, and beta is applied in fp32 by
+// whoever uses it.  The record then holds Gamma, d, beta and gamma log2 e.
+#include "bwd_internal.cuh"
 #include "chunk_tm.cuh"
 #include "gdn_internal.cuh"
 #include "ptx.cuh"
@@ -178,6 +184,7 @@ __device__ __forceinline__ void solve64(const float* Af, float* Tf, float* Mb, i
   named_bar(bar, 128);
 }
 
+template <bool BWD>
 __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepParams P) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -328,6 +335,10 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
           b1 = bxp[(t0 + 32 + lane) * P.Hv + h];
         }
       }
+      if (BWD) {
+        if (lane < L) b0 = bwd::floor_beta(b0);
+        if (32 + lane < L) b1 = bwd::floor_beta(b1);
+      }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const float y0 = __shfl_up_sync(0xffffffffu, x0, o);
@@ -368,7 +379,7 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
         const int h = hk * G + h0 + gi;
         const float* gl2 = gl2_all + gi * 128;
         const float gr = gl2[r];
-        const float br = R < 64 ? gl2[64 + r] : 1.0f;
+        const float br = R < 64 && !BWD ? gl2[64 + r] : 1.0f;
         float v[32];
 #pragma unroll
         for (int b16 = 0; b16 < 2; ++b16) {
@@ -377,7 +388,8 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
             for (int q = 16 * b16; q < 16 * b16 + 16; ++q) {
               const int s = cb + q;
               const bool keep = R < 64 ? (s < r) : (s <= r);
-              v[q] = keep ? br * ex2f(gr - gl2[s]) * d[q] : 0.0f;
+              const float bs = BWD ? (R < 64 ? gl2[64 + s] : 1.0f) : br;
+              v[q] = keep ? bs * ex2f(gr - gl2[s]) * d[q] : 0.0f;
             }
           } else {  // the 16 columns lie above the diagonal
 #pragma unroll
@@ -422,17 +434,22 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
 #pragma unroll
       for (int q = 0; q < 32; ++q) {
         const int s = s0 + q;
-        tv[q] = (s <= r) ? Tf[r * AS + s] * gl2[64 + s] : 0.0f;
+        tv[q] = (s <= r) ? (BWD ? Tf[r * AS + s] : Tf[r * AS + s] * gl2[64 + s]) : 0.0f;
       }
       uint4* dst = reinterpret_cast<uint4*>(tp + (size_t)r * 128 + s0 * 2);
 #pragma unroll
       for (int q8 = 0; q8 < 4; ++q8) dst[q8] = pack8(tv + 8 * q8);
       // Gamma_r and d_s (gamma is constant past the sequence end, so gamma_63 is the chunk's total)
       if (t4 < 64) {
+        constexpr size_t gd_bytes = BWD ? bwd::GD_BYTES : tm::GD_BYTES;
         float* gd = reinterpret_cast<float*>(P.ws + P.gd_off +
-                                             ((size_t)slot * P.Hv + h) * tm::GD_BYTES);
+                                             ((size_t)slot * P.Hv + h) * gd_bytes);
         gd[t4] = ex2f(gl2[t4]);
         gd[64 + t4] = ex2f(gl2[63] - gl2[t4]);
+        if (BWD) {
+          gd[128 + t4] = gl2[64 + t4];
+          gd[192 + t4] = gl2[t4];
+        }
       }
     }
     __syncthreads();  // gates / A / T buffers free for the next pair
@@ -454,6 +471,35 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
 
 unsigned long long* g_prep_trace = nullptr;  // trace builds: device buffer of 8 stamps per CTA
 
+namespace {
+
+template <bool BWD>
+cudaError_t launch_prep_t(const PrepParams& p, int64_t slots, cudaStream_t s) {
+  static int sms_of[64] = {};  // per device; idempotent, a benign race between host threads
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int sms = dev < 64 ? sms_of[dev] : 0;
+  if (sms == 0) {
+    e = cudaFuncSetAttribute(chunk_prep_kernel<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             PP_SMEM);
+    // all of the unified L1 / shared-memory space as shared memory: two CTAs per SM
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(chunk_prep_kernel<BWD>,
+                               cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) sms_of[dev] = sms;
+  }
+  // persistent: two CTAs per SM, each taking every grid-th (slot, k-head) item
+  const int64_t items = slots * p.Hk;
+  const int64_t grid = items < 2 * (int64_t)sms ? items : 2 * (int64_t)sms;
+  chunk_prep_kernel<BWD><<<(unsigned)grid, PP_THREADS, PP_SMEM, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_chunk_prep(const void* q, const void* k, TokStrides ts, const float* g,
                               const float* beta, const int32_t* cu, int N, int B, int64_t T,
                               int Hk, int Hv, void* ws, int* status, cudaStream_t s,
@@ -473,7 +519,7 @@ cudaError_t launch_chunk_prep(const void* q, const void* k, TokStrides ts, const
   p.q_stride = ts.q;
   p.k_stride = ts.k;
   p.T = T;
-  p.gd_off = (int64_t)tm::gd_offset(N, n_tok, Hv);
+  p.gd_off = (int64_t)(fuse.bwd_gd_off ? fuse.bwd_gd_off : tm::gd_offset(N, n_tok, Hv));
   p.N = N;
   p.Hk = Hk;
   p.Hv = Hv;
@@ -482,26 +528,7 @@ cudaError_t launch_chunk_prep(const void* q, const void* k, TokStrides ts, const
   p.b = fuse.b;
   p.A_log = fuse.A_log;
   p.dt_bias = fuse.dt_bias;
-  static bool attr_set = false;  // idempotent attribute; a benign race between host threads
-  static int sms = 0;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(chunk_prep_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, PP_SMEM);
-    // all of the unified L1 / shared-memory space as shared memory: two CTAs per SM
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(chunk_prep_kernel,
-                               cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-    int dev = 0;
-    if (e == cudaSuccess) e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
-  // persistent: two CTAs per SM, each taking every grid-th (slot, k-head) item
-  const int64_t items = slots * Hk;
-  const int64_t grid = items < 2 * (int64_t)sms ? items : 2 * (int64_t)sms;
-  chunk_prep_kernel<<<(unsigned)grid, PP_THREADS, PP_SMEM, s>>>(p);
-  return cudaGetLastError();
+  return fuse.bwd_gd_off ? launch_prep_t<true>(p, slots, s) : launch_prep_t<false>(p, slots, s);
 }
 
 }  // namespace gdn

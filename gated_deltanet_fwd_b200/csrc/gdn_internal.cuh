@@ -224,6 +224,7 @@ struct ChunkFusion {
   const __nv_bfloat16* b = nullptr;
   const float* A_log = nullptr;
   const float* dt_bias = nullptr;
+  size_t bwd_gd_off = 0;  // set: the backward pass's operands, its records at this byte offset
 };
 
 // TMA tensor maps (tma_maps.cu), 128-byte swizzle, bf16:
