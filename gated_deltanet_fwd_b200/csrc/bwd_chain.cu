@@ -13,11 +13,17 @@
 //     D  = dS_bf16 K^T         N 64,  K 128   critical
 //     D2 = dO^T P              N 64,  K 64    early
 //     W  = X T~                N 64,  K 64    critical: dW^T = dV^T
-//     dS = Gamma_63 dS + (scale Gamma dO^T) Q - (Gamma W) K     N 128, K 64 twice, the second critical
-// Warp roles (320 threads): warps 0-3 the critical epilogues; warps 4-7 the side work (the carried matrix
-// scaled by Gamma_63, its bf16 copy to the workspace in the same pass over it, scale Gamma dO^T, and
-// U or dv to memory); warp 8 the TMA producer; warp 9 the MMA issuer.  What bounds it is the latency of
-// the critical sequence of one chunk (see the figures in the design notes), not traffic.
+//     dS = Gamma_63 dS + dO^T (scale Gamma Q) - (Gamma W) K     N 128, K 64 twice, the second critical
+// Warp roles (448 threads): warps 0-7 the critical epilogues (warps w and w + 4 share 32 lanes and split the
+// columns); warps 8-11 the side work (the carried matrix scaled by Gamma_63 and, in the same pass over
+// it, its bf16 copy to the workspace; scale Gamma Q in place; U or dv to memory); warp 12 the TMA
+// producer; warp 13 the MMA issuer.  What bounds it is the latency of the critical sequence of one
+// chunk, not traffic.  Three things that shorten it, by clock stamps of a 64-chunk run:
+//   - MMAs are issued under elect.sync, which tells the compiler that one thread is active: 35 to 45
+//     cycles apart (A in tensor memory) against 134 under a plain lane test;
+//   - the bf16 copy leaves through shared memory and one bulk copy: stores of 32 bytes a lane, 256 bytes
+//     apart, held up every warp of the SM for 1300 of a chunk's 6300 cycles;
+//   - two warps per lane quarter halve each epilogue's columns.
 //
 // A chunk that ends inside a tile: rows of K, Q, V, dO behind the sequence end hold whatever follows in
 // memory, so the producer waits for that chunk's copies itself, clears those rows and only then
@@ -33,8 +39,8 @@ namespace {
 
 using namespace ptx;
 
-constexpr int THREADS = 320;
-constexpr int W_PROD = 8;  // warp 9 issues the MMAs
+constexpr int THREADS = 448;
+constexpr int W_SIDE = 8, W_PROD = 12;  // warp 13 issues the MMAs
 
 // shared memory, from a 1024-aligned base; a stage holds one chunk's tiles: K, [Q,] V or dO, T~ [and P],
 // the record.  64-row tiles are two 64-column halves 8192 bytes apart.
@@ -44,21 +50,24 @@ struct Sm {
                             GD = TP + (BACK ? 16384 : 8192), STAGE = GD + 1024;
   static constexpr uint32_t TX = GD + GD_BYTES;  // bytes of a full stage
   static constexpr int STAGES = BACK ? 2 : 3;
-  static constexpr uint32_t BAR = STAGES * STAGE, BYTES = BAR + 256 + 1024;
+  static constexpr uint32_t COPY = STAGES * STAGE;     // bf16 copy of the carried matrix on its way out
+  static constexpr uint32_t UOUT = COPY + 32768;       // forward: U^T on its way out
+  static constexpr uint32_t BAR = UOUT + (BACK ? 0 : 16384), BYTES = BAR + 256 + 1024;
   static_assert(STAGE % 1024 == 0 && BYTES <= 232448, "stage layout");
 };
 
 enum { B_FULL0 = 0, B_EMPTY0 = 3, B_FIX = 6, B_K = 7, B_U = 8, B_S = 9, B_DRAIN = 10, B_N = 11 };
 
 // named barriers: hand-offs to the MMA issuer and between the two groups
-enum { NB_X = 1, NB_U = 2, NB_S = 3, NB_SR = 4, NB_G = 5 };
-constexpr int NB_ALL = 288;  // both groups + issuer warp
-constexpr int NB_EI = 160;   // one group + issuer warp
-constexpr int NB_EH = 256;   // both groups
+enum { NB_X = 1, NB_U = 2, NB_S = 3, NB_SR = 4, NB_G = 5, NB_SIDE = 6 };
+constexpr int NB_ALL = 416;  // both groups + issuer warp
+constexpr int NB_CI = 288;   // critical group + issuer warp
+constexpr int NB_SI = 160;   // side group + issuer warp
+constexpr int NB_CS = 384;   // both groups
 
 // tensor-memory columns
 constexpr uint32_t TM_S = 0, TM_D = 128, TM_D2 = 192, TM_U = 256, TM_SB = 320, TM_X = 384,
-                   TM_UT = 416, TM_UD = 448;
+                   TM_UD = 416;
 
 struct ChainParams {
   const float* S_in;   // initial state, or gradient of the final one; null: zero
@@ -80,17 +89,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ uint64_t dadd(uint64_t d, uint32_t bytes) {
   return d + (uint64_t)(bytes >> 4);
 }
-__device__ __forceinline__ void ld64(uint32_t taddr, float (&v)[64]) {
-  tmem_ld16(taddr + 0, *reinterpret_cast<float(*)[16]>(v + 0));
+// 32 fp32 columns of this warp's lanes (no wait)
+__device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
+  tmem_ld16(taddr, *reinterpret_cast<float(*)[16]>(v));
   tmem_ld16(taddr + 16, *reinterpret_cast<float(*)[16]>(v + 16));
-  tmem_ld16(taddr + 32, *reinterpret_cast<float(*)[16]>(v + 32));
-  tmem_ld16(taddr + 48, *reinterpret_cast<float(*)[16]>(v + 48));
 }
-// 32 bytes to global memory, 32-byte aligned: a whole sector per thread
-__device__ __forceinline__ void store32(void* p, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
+__device__ __forceinline__ void ld64(uint32_t taddr, float* v) {
+  ld32(taddr, v);
+  ld32(taddr + 32, v + 32);
 }
 
 template <bool BACK>
@@ -130,7 +136,8 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
   if (tid == 0) {
     for (int i = 0; i < L_::STAGES; ++i) {
       mbar_init(&bars[B_FULL0 + i], 1);
-      mbar_init(&bars[B_EMPTY0 + i], 1);
+      // the MMAs that read a stage and, forward, the side group's last look at its record
+      mbar_init(&bars[B_EMPTY0 + i], BACK ? 1 : 2);
     }
     for (int i = B_FIX; i < B_N; ++i) mbar_init(&bars[i], 1);
     *abort_flag = 0;
@@ -161,108 +168,103 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
   auto wait_full = [&](int i) {
     return wait_w(B_FULL0 + i % L_::STAGES, (uint32_t)(i / L_::STAGES) & 1);
   };
+  // forward: two buffers in turn, since the next chunk's V^T T~^T starts before this one's are read
+  auto u_col = [&](int i) { return !BACK && (i & 1) ? TM_D2 : TM_U; };
   auto record = [&](int i) {
     return reinterpret_cast<const float*>(smem + (i % L_::STAGES) * L_::STAGE + L_::GD);
   };
 
-  if (warp < 4) {
+  if (warp < W_SIDE) {
     // -------------------------------------------------------------- critical epilogues -------
-    const int j = 32 * warp + lane;  // value row = tensor-memory lane
-    const uint32_t lo = (uint32_t)(32 * warp) << 16;
+    const int half = warp >> 2;
+    const int j = 32 * (warp & 3) + lane;  // value row = tensor-memory lane
+    const uint32_t lo = (uint32_t)(32 * (warp & 3)) << 16;
+    // bf16 copy of this thread's 64 columns of the carried matrix
+    auto copy_out = [&](const float* v) {
+      uint32_t pk[32];
+#pragma unroll
+      for (int q = 0; q < 32; ++q) pk[q] = pack2(v[2 * q], v[2 * q + 1]);
+      tmem_st16u(tmem + lo + TM_SB + 32 * half, *reinterpret_cast<uint32_t(*)[16]>(pk));
+      tmem_st16u(tmem + lo + TM_SB + 32 * half + 16, *reinterpret_cast<uint32_t(*)[16]>(pk + 16));
+    };
     {
-      const float* src = P.S_in ? P.S_in + sidx + (size_t)j * tm::D : nullptr;
+      const float* src = P.S_in ? P.S_in + sidx + (size_t)j * tm::D + 64 * half : nullptr;
+      float v[64];
 #pragma unroll
-      for (int blk = 0; blk < 4; ++blk) {  // 32 columns at a time
-        float v[32];
-#pragma unroll
-        for (int q4 = 0; q4 < 8; ++q4) {
-          const float4 f = src ? __ldg(reinterpret_cast<const float4*>(src + 32 * blk) + q4)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-          v[4 * q4] = f.x;
-          v[4 * q4 + 1] = f.y;
-          v[4 * q4 + 2] = f.z;
-          v[4 * q4 + 3] = f.w;
-        }
-        tmem_st16(tmem + lo + TM_S + 32 * blk, *reinterpret_cast<float(*)[16]>(v));
-        tmem_st16(tmem + lo + TM_S + 32 * blk + 16, *reinterpret_cast<float(*)[16]>(v + 16));
-        uint32_t pk[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q) pk[q] = pack2(v[2 * q], v[2 * q + 1]);
-        tmem_st16u(tmem + lo + TM_SB + 16 * blk, pk);
+      for (int q4 = 0; q4 < 16; ++q4) {
+        const float4 f = src ? __ldg(reinterpret_cast<const float4*>(src) + q4)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[4 * q4] = f.x;
+        v[4 * q4 + 1] = f.y;
+        v[4 * q4 + 2] = f.z;
+        v[4 * q4 + 3] = f.w;
       }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        tmem_st16(tmem + lo + TM_S + 64 * half + 16 * q, *reinterpret_cast<float(*)[16]>(v + 16 * q));
+      copy_out(v);
       tmem_st_wait();
       tc_fence_before();
-      named_bar_arrive(NB_SR, NB_EH);  // the side group may take the matrix over
+      named_bar_arrive(NB_SR, NB_CS);  // the side group may take the matrix over
       named_bar(NB_S, NB_ALL);
     }
     for (int i = 0; i < nch; ++i) {
-      const float* gd = record(i);
+      const float* gd = record(i) + 32 * half;
+      const uint32_t tm_u = tmem + lo + u_col(i) + 32 * half;
       wait_full(i);  // the chunk's record is visible to this thread
       // ---- X'
       if (wait_w(B_K, i & 1)) {
         tc_fence_after();
+        float d[32], d2[32];
+        ld32(tmem + lo + TM_D + 32 * half, d);
+        if (BACK) ld32(tmem + lo + TM_D2 + 32 * half, d2);
+        tmem_ld_wait();
+        uint32_t pk[16];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float d[32], d2[32];
-          tmem_ld16(tmem + lo + TM_D + 32 * hh, *reinterpret_cast<float(*)[16]>(d));
-          tmem_ld16(tmem + lo + TM_D + 32 * hh + 16, *reinterpret_cast<float(*)[16]>(d + 16));
-          if (BACK) {
-            tmem_ld16(tmem + lo + TM_D2 + 32 * hh, *reinterpret_cast<float(*)[16]>(d2));
-            tmem_ld16(tmem + lo + TM_D2 + 32 * hh + 16, *reinterpret_cast<float(*)[16]>(d2 + 16));
+        for (int q4 = 0; q4 < 8; ++q4) {
+          const float* x = d + 4 * q4;
+          if (!BACK) {
+            const float4 gm = *reinterpret_cast<const float4*>(gd + 4 * q4);
+            pk[2 * q4] = pack2(-gm.x * x[0], -gm.y * x[1]);
+            pk[2 * q4 + 1] = pack2(-gm.z * x[2], -gm.w * x[3]);
+          } else {
+            const float* y = d2 + 4 * q4;
+            const float4 dd = *reinterpret_cast<const float4*>(gd + 64 + 4 * q4);
+            const float4 be = *reinterpret_cast<const float4*>(gd + 128 + 4 * q4);
+            pk[2 * q4] = pack2(be.x * fmaf(dd.x, x[0], P.scale * y[0]),
+                               be.y * fmaf(dd.y, x[1], P.scale * y[1]));
+            pk[2 * q4 + 1] = pack2(be.z * fmaf(dd.z, x[2], P.scale * y[2]),
+                                   be.w * fmaf(dd.w, x[3], P.scale * y[3]));
           }
-          tmem_ld_wait();
-          uint32_t pk[16];
-#pragma unroll
-          for (int q4 = 0; q4 < 8; ++q4) {
-            const float* x = d + 4 * q4;
-            if (!BACK) {
-              const float4 gm = *reinterpret_cast<const float4*>(gd + 32 * hh + 4 * q4);
-              pk[2 * q4] = pack2(-gm.x * x[0], -gm.y * x[1]);
-              pk[2 * q4 + 1] = pack2(-gm.z * x[2], -gm.w * x[3]);
-            } else {
-              const float* y = d2 + 4 * q4;
-              const float4 dd = *reinterpret_cast<const float4*>(gd + 64 + 32 * hh + 4 * q4);
-              const float4 be = *reinterpret_cast<const float4*>(gd + 128 + 32 * hh + 4 * q4);
-              pk[2 * q4] = pack2(be.x * fmaf(dd.x, x[0], P.scale * y[0]),
-                                 be.y * fmaf(dd.y, x[1], P.scale * y[1]));
-              pk[2 * q4 + 1] = pack2(be.z * fmaf(dd.z, x[2], P.scale * y[2]),
-                                     be.w * fmaf(dd.w, x[3], P.scale * y[3]));
-            }
-          }
-          tmem_st16u(tmem + lo + TM_X + 16 * hh, pk);
         }
+        tmem_st16u(tmem + lo + TM_X + 16 * half, pk);
         tmem_st_wait();
       }
       tc_fence_before();
-      named_bar_arrive(NB_X, NB_EI);
-      // ---- the update's operand (and U)
+      named_bar_arrive(NB_X, NB_CI);
+      // ---- the update's operand
       if (wait_w(B_U, i & 1)) {
         tc_fence_after();
+        float u[32];
+        ld32(tm_u, u);
+        tmem_ld_wait();
+        uint32_t pd[16];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float u[32];
-          tmem_ld32(tmem + lo + TM_U + 32 * hh, u);
-          uint32_t pk[16], pd[16];
-#pragma unroll
-          for (int q4 = 0; q4 < 8; ++q4) {
-            const float* x = u + 4 * q4;
-            if (!BACK) {
-              const float4 dd = *reinterpret_cast<const float4*>(gd + 64 + 32 * hh + 4 * q4);
-              const float4 be = *reinterpret_cast<const float4*>(gd + 128 + 32 * hh + 4 * q4);
-              const float u0 = be.x * x[0], u1 = be.y * x[1], u2 = be.z * x[2], u3 = be.w * x[3];
-              pk[2 * q4] = pack2(u0, u1);
-              pk[2 * q4 + 1] = pack2(u2, u3);
-              pd[2 * q4] = pack2(u0 * dd.x, u1 * dd.y);
-              pd[2 * q4 + 1] = pack2(u2 * dd.z, u3 * dd.w);
-            } else {
-              const float4 gm = *reinterpret_cast<const float4*>(gd + 32 * hh + 4 * q4);
-              pd[2 * q4] = pack2(-gm.x * x[0], -gm.y * x[1]);
-              pd[2 * q4 + 1] = pack2(-gm.z * x[2], -gm.w * x[3]);
-            }
+        for (int q4 = 0; q4 < 8; ++q4) {
+          const float* x = u + 4 * q4;
+          float4 f;
+          if (!BACK) {
+            const float4 dd = *reinterpret_cast<const float4*>(gd + 64 + 4 * q4);
+            const float4 be = *reinterpret_cast<const float4*>(gd + 128 + 4 * q4);
+            f = make_float4(be.x * dd.x, be.y * dd.y, be.z * dd.z, be.w * dd.w);
+          } else {
+            const float4 gm = *reinterpret_cast<const float4*>(gd + 4 * q4);
+            f = make_float4(-gm.x, -gm.y, -gm.z, -gm.w);
           }
-          if (!BACK) tmem_st16u(tmem + lo + TM_UT + 16 * hh, pk);
-          tmem_st16u(tmem + lo + TM_UD + 16 * hh, pd);
+          pd[2 * q4] = pack2(f.x * x[0], f.y * x[1]);
+          pd[2 * q4 + 1] = pack2(f.z * x[2], f.w * x[3]);
         }
+        tmem_st16u(tmem + lo + TM_UD + 16 * half, pd);
         tmem_st_wait();
       }
       tc_fence_before();
@@ -274,119 +276,150 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
       if (i + 1 < nch) {
         if (s_ok) {
           tc_fence_after();
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float v[64];
-            ld64(tmem + lo + TM_S + 64 * hh, v);
-            tmem_ld_wait();
-            uint32_t pk[32];
-#pragma unroll
-            for (int q = 0; q < 32; ++q) pk[q] = pack2(v[2 * q], v[2 * q + 1]);
-            tmem_st16u(tmem + lo + TM_SB + 32 * hh, *reinterpret_cast<uint32_t(*)[16]>(pk));
-            tmem_st16u(tmem + lo + TM_SB + 32 * hh + 16,
-                       *reinterpret_cast<uint32_t(*)[16]>(pk + 16));
-          }
+          float v[64];
+          ld64(tmem + lo + TM_S + 64 * half, v);
+          tmem_ld_wait();
+          tc_fence_before();
+          named_bar_arrive(NB_SR, NB_CS);  // the matrix is read: the side group may scale it
+          copy_out(v);
+          tmem_st_wait();
+        } else {
+          named_bar_arrive(NB_SR, NB_CS);
         }
-        tc_fence_before();
-        named_bar_arrive(NB_SR, NB_EH);  // the matrix is read: the side group may scale it
-        tmem_st_wait();
         tc_fence_before();
         named_bar(NB_S, NB_ALL);
       }
     }
-  } else if (warp < 8) {
-    // -------------------------------------------------------------- side group (warps 4-7) ---
-    const int j = 32 * (warp - 4) + lane;
-    const uint32_t lo = (uint32_t)(32 * (warp - 4)) << 16;
-    // The carried matrix entering step i: its bf16 copy to the workspace, then scaled by Gamma_63 in
-    // tensor memory (after the critical group has read it).  Backward: also scale Gamma dO^T.
-    auto take = [&](int i) {
-      named_bar(NB_SR, NB_EH);
-      tc_fence_after();
+  } else if (warp < W_PROD) {
+    // -------------------------------------------------------------- side group (warps 8-11) --
+    const int quad = warp & 3, t4 = tid - 32 * W_SIDE;
+    const int j = 32 * quad + lane;
+    const uint32_t lo = (uint32_t)(32 * quad) << 16;
+    // Backward: Q of step i becomes scale Gamma Q, in place (the B operand of the dO term).
+    auto scale_q = [&](int i) {
       if (!wait_full(i)) return;
       const float* gd = record(i);
-      const float gl = gd[63];
-      if (BACK) {  // rows of dO in pairs: the A operand holds two consecutive tokens per column
-        const unsigned char* x = smem + (i % L_::STAGES) * L_::STAGE + L_::X + (j >> 6) * 8192;
-        const int c8 = (j & 63) >> 3, cb = (j & 7) * 2;
-        uint32_t pk[32];
+      unsigned char* qt = smem + (i % L_::STAGES) * L_::STAGE + L_::Q;
 #pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          const int r = 2 * q;
-          const uint32_t o0 = *reinterpret_cast<const uint16_t*>(
-              x + r * 128 + ((c8 ^ (r & 7)) << 4) + cb);
-          const uint32_t o1 = *reinterpret_cast<const uint16_t*>(
-              x + (r + 1) * 128 + ((c8 ^ ((r + 1) & 7)) << 4) + cb);
-          const float2 gm = *reinterpret_cast<const float2*>(gd + r);
-          pk[q] = pack2(P.scale * gm.x * __uint_as_float(o0 << 16),
-                        P.scale * gm.y * __uint_as_float(o1 << 16));
+      for (int e = 0; e < 8; ++e) {  // 16-byte pieces; piece / 8 is a row of one of the halves
+        const int piece = e * 128 + t4;
+        uint4* p = reinterpret_cast<uint4*>(qt) + piece;
+        const float f = P.scale * gd[(piece >> 3) & 63];
+        uint4 w = *p;
+        uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          x[q] = pack2(f * __uint_as_float(x[q] << 16), f * __uint_as_float(x[q] & 0xffff0000u));
+        *p = w;
+      }
+      fence_proxy_async_smem();
+    };
+    // The carried matrix entering step i: its bf16 copy to the workspace, then scaled by Gamma_63 in
+    // tensor memory (after the critical group has read it).  The copy is the swizzled image that
+    // the MMAs of the parallel kernel read: row j, 16-byte piece c at (c ^ j % 8).
+    auto take = [&](int i) {
+      // the previous copy has left shared memory (forward: U may still be on its way)
+      if (t4 == 0) bulk_wait_read<BACK ? 0 : 1>();
+      named_bar(NB_SR, NB_CS);
+      tc_fence_after();
+      const bool ok = wait_full(i) && __all_sync(0xffffffffu, !*abort_flag);
+      if (ok) {
+        const float gl = record(i)[63];
+        unsigned char* row = smem + L_::COPY + j * 128;
+#pragma unroll
+        for (int hh = 0; hh < 4; ++hh) {
+          float v[32];
+          ld32(tmem + lo + TM_S + 32 * hh, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float* x = v + 8 * q;
+            *reinterpret_cast<uint4*>(row + (hh >> 1) * 16384 +
+                                      (((4 * (hh & 1) + q) ^ (j & 7)) << 4)) =
+                make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]),
+                           pack2(x[6], x[7]));
+          }
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[q] *= gl;
+          tmem_st16(tmem + lo + TM_S + 32 * hh, *reinterpret_cast<float(*)[16]>(v));
+          tmem_st16(tmem + lo + TM_S + 32 * hh + 16, *reinterpret_cast<float(*)[16]>(v + 16));
         }
-        tmem_st16u(tmem + lo + TM_UT, *reinterpret_cast<uint32_t(*)[16]>(pk));
-        tmem_st16u(tmem + lo + TM_UT + 16, *reinterpret_cast<uint32_t(*)[16]>(pk + 16));
+        tmem_st_wait();
+        fence_proxy_async_smem();
       }
-      unsigned char* tile = P.ws + (BACK ? P.at.ds : P.at.s) +
-                            ((size_t)(slot0 + chunk_of(i)) * P.Hv + h) * 32768 + j * 128;
-#pragma unroll
-      for (int hh = 0; hh < 4; ++hh) {
-        float v[32];
-        tmem_ld32(tmem + lo + TM_S + 32 * hh, v);
-        uint32_t pk[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q) pk[q] = pack2(v[2 * q], v[2 * q + 1]);
-#pragma unroll
-        for (int q = 0; q < 32; ++q) v[q] *= gl;
-        tmem_st16(tmem + lo + TM_S + 32 * hh, *reinterpret_cast<float(*)[16]>(v));
-        tmem_st16(tmem + lo + TM_S + 32 * hh + 16, *reinterpret_cast<float(*)[16]>(v + 16));
-        unsigned char* dst = tile + (hh >> 1) * 16384 + (hh & 1) * 64;
-        store32(dst, pk);
-        store32(dst + 32, pk + 8);
+      return ok;
+    };
+    auto send = [&](int i, bool ok) {
+      named_bar(NB_SIDE, 128);
+      if (t4 == 0 && ok) {
+        const size_t sh = (size_t)(slot0 + chunk_of(i)) * P.Hv + h;
+        bulk_store(P.ws + (BACK ? P.at.ds : P.at.s) + sh * 32768, smem + L_::COPY, 32768);
+        bulk_commit();
       }
-      tmem_st_wait();
     };
     named_bar_arrive(NB_S, NB_ALL);
-    take(0);
-    tc_fence_before();
-    if (BACK) named_bar_arrive(NB_G, NB_EI);
+    if (BACK) scale_q(0);
+    {
+      const bool ok = take(0);
+      tc_fence_before();
+      if (BACK) named_bar_arrive(NB_G, NB_SI);
+      send(0, ok);
+    }
     for (int i = 0; i < nch; ++i) {
+      if (!BACK && t4 == 0) bulk_wait_read<1>();  // the previous U has left shared memory
       named_bar(NB_U, NB_ALL);  // matrix scaled; a full barrier (see the other group)
-      tc_fence_after();
       const int c = chunk_of(i);
+      // E^T or dW^T: complete since the critical group has waited for it
+      bool ok = wait_w(B_U, i & 1);
       uint32_t ob[32];
-      bool ok = __all_sync(0xffffffffu, !*abort_flag) != 0;
-      if (!BACK) {  // U^T of the chunk, written by the critical group before the barrier
-        if (ok) {
+      if (ok) {
+        tc_fence_after();
+        const float* be = record(i) + 128;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
           float t[32];
-          tmem_ld32(tmem + lo + TM_UT, t);
+          ld32(tmem + lo + u_col(i) + 32 * hh, t);
+          tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < 32; ++q) ob[q] = __float_as_uint(t[q]);
-        }
-      } else {  // dW^T: complete since the critical group has waited for it
-        ok = wait_w(B_U, i & 1) && ok;
-        if (ok) {
-          tc_fence_after();
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float t[32];
-            tmem_ld32(tmem + lo + TM_U + 32 * hh, t);
-#pragma unroll
-            for (int q = 0; q < 16; ++q) ob[16 * hh + q] = pack2(t[2 * q], t[2 * q + 1]);
+          for (int q = 0; q < 16; ++q) {
+            if (!BACK) {
+              t[2 * q] *= be[32 * hh + 2 * q];
+              t[2 * q + 1] *= be[32 * hh + 2 * q + 1];
+            }
+            ob[16 * hh + q] = pack2(t[2 * q], t[2 * q + 1]);
           }
         }
       }
       tc_fence_before();
-      if (i + 1 < nch) {
-        named_bar_arrive(NB_S, NB_ALL);  // U / dW read
-        take(i + 1);
-        tc_fence_before();
-        if (BACK) named_bar_arrive(NB_G, NB_EI);
-      }
-      if (!ok) continue;
-      if (!BACK) {
-        unsigned char* dst =
-            P.ws + P.at.u + ((size_t)(slot0 + c) * P.Hv + h) * 16384 + j * 128;
+      if (i + 1 < nch) named_bar_arrive(NB_S, NB_ALL);  // U / dW read
+      if (!BACK && ok) {
+        // U^T, the same kind of image
+        unsigned char* row = smem + L_::UOUT + j * 128;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) store32(dst + 32 * q, ob + 8 * q);
-      } else {
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<uint4*>(row + ((q ^ (j & 7)) << 4)) =
+              make_uint4(ob[4 * q], ob[4 * q + 1], ob[4 * q + 2], ob[4 * q + 3]);
+        fence_proxy_async_smem();
+      }
+      if (!BACK) {
+        named_bar(NB_SIDE, 128);
+        if (t4 == 0) {
+          mbar_arrive(&bars[B_EMPTY0 + i % L_::STAGES]);
+          if (ok) {
+            const size_t sh = (size_t)(slot0 + c) * P.Hv + h;
+            bulk_store(P.ws + P.at.u + sh * 16384, smem + L_::UOUT, 16384);
+            bulk_commit();
+          }
+        }
+      }
+      if (i + 1 < nch) {
+        if (BACK) scale_q(i + 1);
+        const bool copied = take(i + 1);
+        tc_fence_before();
+        if (BACK) named_bar_arrive(NB_G, NB_SI);
+        send(i + 1, copied);
+      }
+      if (BACK && ok) {
         // lanes j, j ^ 1 swap halves: an even lane stores row 2q at columns j, j + 1, an odd lane row
         // 2q + 1 at columns j - 1, j -- each warp store two contiguous 64-byte row segments
         const int64_t t0 = s_beg + (int64_t)tm::C * c;
@@ -405,9 +438,10 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
         }
       }
     }
+    if (t4 == 0) bulk_wait<0>();  // nothing on its way out of shared memory
   } else if (warp == W_PROD) {
     // -------------------------------------------------------------- TMA producer -------------
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tensormap(&map_k);
       prefetch_tensormap(&map_x);
       prefetch_tensormap(&map_tp);
@@ -426,7 +460,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
       // a partial chunk's copies are awaited here, on a barrier of their own
       const bool part = L < tm::C;
       uint64_t* fb = part ? &bars[B_FIX] : &bars[B_FULL0 + st];
-      if (lane == 0) {
+      if (elect_one()) {
         const int32_t t0 = (int32_t)(s_beg + (int64_t)tm::C * c);
         const size_t sh = (size_t)(slot0 + c) * P.Hv + h;
         mbar_arrive_expect_tx(fb, L_::TX);
@@ -472,11 +506,13 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
     const uint32_t id_k = idesc_bf16(128, 64, 0, 0);             // A tensor memory, B K-major
     const uint32_t id_e = idesc_bf16(128, 64, 1, BACK ? 1 : 0);  // A smem MN-major
     const uint32_t id_u = idesc_bf16(128, 64, 0, BACK ? 1 : 0);  // T~^T forward, T~ backward
-    const uint32_t id_s = idesc_bf16(128, 128, 0, 1);            // B = K or Q, MN-major
-    const bool leader = lane == 0;
+    const uint32_t id_s = idesc_bf16(128, 128, 0, 1);            // B = K, MN-major
+    const uint32_t id_q = idesc_bf16(128, 128, 1, 1);            // A = dO^T, B = scale Gamma Q
+    auto live = [&]() { return __all_sync(0xffffffffu, !*abort_flag) != 0; };
     for (int i = 0; i < nch; ++i) {
       const int st = i % L_::STAGES;
       const uint32_t sp = sbase + st * L_::STAGE;
+      const uint32_t tm_u = tmem + u_col(i);
       const bool have = wait_full(i);
       const uint64_t dK = sdesc_sw128(sp + L_::K, 16, 1024);       // K as K-major B
       const uint64_t dKn = sdesc_sw128(sp + L_::K, 8192, 1024);    // K as MN-major B
@@ -486,85 +522,92 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
                                : sdesc_sw128(sp + L_::TP, 16, 1024);    // T~ as K-major B
       const uint64_t dP = sdesc_sw128(sp + L_::TP + 8192, 8192, 1024);  // P as MN-major B
       constexpr uint32_t t_step = BACK ? 2048 : 32;
-      if (have && leader && !*abort_flag) {
+      if (have && live()) {
         tc_fence_after();
-        // state-independent; its columns were read before the previous chunk's NB_U
+        // state-independent.  Backward: D2 was read before the previous chunk's NB_U.  Forward: these
+        // columns were read by the side group before the previous chunk's NB_S (two buffers).
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          if (BACK)
-            mma_bf16_ss(tmem + TM_D2, dadd(dXt, ks * 2048), dadd(dP, ks * 2048), id_e, ks > 0);
-          else
-            mma_bf16_ss(tmem + TM_U, dadd(dXt, ks * 2048), dadd(dT, ks * 32), id_e, ks > 0);
+          for (int ks = 0; ks < 4; ++ks) {
+            if (BACK)
+              mma_bf16_ss(tmem + TM_D2, dadd(dXt, ks * 2048), dadd(dP, ks * 2048), id_e, ks > 0);
+            else
+              mma_bf16_ss(tm_u, dadd(dXt, ks * 2048), dadd(dT, ks * 32), id_e, ks > 0);
+          }
         }
       }
       __syncwarp();
       named_bar(NB_S, NB_ALL);  // bf16 copy in place, U / dW of the previous chunk read
-      const bool go = have && !*abort_flag;
-      if (go && leader) {
+      const bool go = have && live();
+      if (go) {
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_bf16_ts(tmem + TM_D, tmem + TM_SB + 8 * ks,
-                      dadd(dK, (ks >> 2) * 8192 + (ks & 3) * 32), id_k, ks > 0);
-        mma_commit(&bars[B_K]);
+          for (int ks = 0; ks < 8; ++ks)
+            mma_bf16_ts(tmem + TM_D, tmem + TM_SB + 8 * ks,
+                        dadd(dK, (ks >> 2) * 8192 + (ks & 3) * 32), id_k, ks > 0);
+          mma_commit(&bars[B_K]);
+        }
       }
       __syncwarp();
-      named_bar(NB_X, NB_EI);  // X' written
-      if (go && leader && !*abort_flag) {
+      named_bar(NB_X, NB_CI);  // X' written
+      if (go && live()) {
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_bf16_ts(tmem + TM_U, tmem + TM_X + 8 * ks, dadd(dT, ks * t_step), id_u,
-                      !BACK || ks > 0);
-        mma_commit(&bars[B_U]);
+          for (int ks = 0; ks < 4; ++ks)
+            mma_bf16_ts(tm_u, tmem + TM_X + 8 * ks, dadd(dT, ks * t_step), id_u, !BACK || ks > 0);
+          mma_commit(&bars[B_U]);
+        }
       }
       __syncwarp();
       if (BACK) {
-        named_bar(NB_G, NB_EI);  // dS scaled, scale Gamma dO^T written
-        if (go && leader && !*abort_flag) {
+        named_bar(NB_G, NB_SI);  // dS scaled, scale Gamma Q written
+        if (go && live()) {
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ts(tmem + TM_S, tmem + TM_UT + 8 * ks, dadd(dQn, ks * 2048), id_s, 1);
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_ss(tmem + TM_S, dadd(dXt, ks * 2048), dadd(dQn, ks * 2048), id_q, 1);
+          }
         }
         __syncwarp();
       }
       named_bar(NB_U, NB_ALL);  // the update's operand written; matrix scaled
-      if (go && leader && !*abort_flag) {
+      if (go && live()) {
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_bf16_ts(tmem + TM_S, tmem + TM_UD + 8 * ks, dadd(dKn, ks * 2048), id_s, 1);
-        mma_commit(&bars[B_S]);
-        mma_commit(&bars[B_EMPTY0 + st]);
+          for (int ks = 0; ks < 4; ++ks)
+            mma_bf16_ts(tmem + TM_S, tmem + TM_UD + 8 * ks, dadd(dKn, ks * 2048), id_s, 1);
+          mma_commit(&bars[B_S]);
+          mma_commit(&bars[B_EMPTY0 + st]);
+        }
       }
       __syncwarp();
     }
-    if (lane == 0) {
-      // every MMA has completed before tensor memory is read back or released
+    // every MMA has completed before tensor memory is read back or released
+    if (elect_one()) {
       mma_commit(&bars[B_DRAIN]);
       if (!mbar_wait(&bars[B_DRAIN], 0)) fail(GDN_ERR_TIMEOUT);
     }
+    __syncwarp();
   }
 
   // the issuer's drain (and any abort) is visible to every thread after this barrier
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (BACK && warp < 4 && P.S_out && !*abort_flag) {
-    const int j = 32 * warp + lane;
-    const uint32_t lo = (uint32_t)(32 * warp) << 16;
-    float* dst = P.S_out + sidx + (size_t)j * tm::D;
+  if (BACK && warp < W_SIDE && P.S_out && __all_sync(0xffffffffu, !*abort_flag)) {
+    const int j = 32 * (warp & 3) + lane, half = warp >> 2;
+    float* dst = P.S_out + sidx + (size_t)j * tm::D + 64 * half;
+    float v[64];
+    ld64(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + TM_S + 64 * half, v);
+    tmem_ld_wait();
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      float v[64];
-      ld64(tmem + lo + TM_S + 64 * hh, v);
-      tmem_ld_wait();
-#pragma unroll
-      for (int q4 = 0; q4 < 16; ++q4)
-        reinterpret_cast<float4*>(dst + 64 * hh)[q4] =
-            make_float4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
-    }
+    for (int q4 = 0; q4 < 16; ++q4)
+      reinterpret_cast<float4*>(dst)[q4] =
+          make_float4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
   }
   tc_fence_before();
   __syncthreads();

@@ -106,7 +106,7 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc) {
 __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_q,
     const __grid_constant__ CUtensorMap map_do, const __grid_constant__ CUtensorMap map_dv,
-    const __grid_constant__ CUtensorMap map_ws, const GradParams P) {
+    const GradParams P) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -362,12 +362,11 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
     }
   } else if (warp == W_PROD) {
     // ------------------------------------------------------------------ TMA producer ---------
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tensormap(&map_k);
       prefetch_tensormap(&map_q);
       prefetch_tensormap(&map_do);
       prefetch_tensormap(&map_dv);
-      prefetch_tensormap(&map_ws);
     }
     uint32_t fix = 0;
     bool stop = false;
@@ -377,7 +376,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
     auto group = [&](int full, uint32_t bytes, int L, unsigned char* clear, int tiles, auto&& copy) {
       const bool part = L < tm::C;
       uint64_t* fb = &bars[part ? B_FIX : full];
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(fb, bytes);
         copy(fb);
       }
@@ -425,13 +424,9 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
               tma_load_3d(smem + SM_OW + 8192, &map_dv, fb, 0, h, t0);
               tma_load_3d(smem + SM_OW + 16384, &map_do, fb, 64, h, t0);
               tma_load_3d(smem + SM_OW + 24576, &map_dv, fb, 64, h, t0);
-              // rows of 64 columns counted from the start of S: then dS, then U
-              const int32_t n2 = (int32_t)((P.at.ds - P.at.s) / 128);
-              tma_load_2d(smem + SM_U, &map_ws, fb, 0, 2 * n2 + (int32_t)(sh * 128));
-              tma_load_2d(smem + SM_S, &map_ws, fb, 0, (int32_t)(sh * 256));
-              tma_load_2d(smem + SM_S + 16384, &map_ws, fb, 0, (int32_t)(sh * 256 + 128));
-              tma_load_2d(smem + SM_DS, &map_ws, fb, 0, n2 + (int32_t)(sh * 256));
-              tma_load_2d(smem + SM_DS + 16384, &map_ws, fb, 0, n2 + (int32_t)(sh * 256 + 128));
+              bulk_load(smem + SM_U, P.ws + P.at.u + sh * 16384, 16384, fb);
+              bulk_load(smem + SM_S, P.ws + P.at.s + sh * 32768, 32768, fb);
+              bulk_load(smem + SM_DS, P.ws + P.at.ds + sh * 32768, 32768, fb);
               bulk_load(smem + SM_GD + (x & 1) * GD_BYTES, P.ws + P.at.gd + sh * GD_BYTES, GD_BYTES,
                         fb);
             })) {
@@ -473,7 +468,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
     const uint64_t dNM = sdesc_sw128(sbase + SM_NM, 16, 1024);
     const uint64_t dNn = sdesc_sw128(sbase + SM_NM, 8192, 1024);
     const uint64_t dMn = sdesc_sw128(sbase + SM_NM + 8192, 8192, 1024);
-    const bool leader = lane == 0;
+    auto live = [&]() { return __all_sync(0xffffffffu, !*abort_flag) != 0; };
     for (int64_t it = blockIdx.x;; it += gridDim.x, ++y) {
       Chunk ch;
       int64_t slot;
@@ -481,52 +476,59 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
       if (!locate(it, ch, slot, hk)) break;
       for (int gi = 0; gi < G; ++gi, ++x) {
         const bool have = wait_w(B_H, x & 1);
-        if (have && leader && !*abort_flag) {
+        if (have && live()) {
           tc_fence_after();
           // D2 was read before the previous step's NB_NM
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_bf16_ss(tmem + TM_D2, dadd(dOW, (ks >> 2) * 16384 + (ks & 3) * 32),
-                        dadd(dU, ks * 2048), id_p, ks > 0);
-          mma_commit(&bars[B_P]);
+            for (int ks = 0; ks < 8; ++ks)
+              mma_bf16_ss(tmem + TM_D2, dadd(dOW, (ks >> 2) * 16384 + (ks & 3) * 32),
+                          dadd(dU, ks * 2048), id_p, ks > 0);
+            mma_commit(&bars[B_P]);
+          }
         }
         __syncwarp();
         if (x > 0) named_bar(NB_D, NB_ALL);  // the previous step's D1, D3, D4, D5 are read
-        if (have && leader && !*abort_flag) {
+        if (have && live()) {
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_bf16_ss(tmem + TM_D1, dadd(dSt, ks * 2048),
-                        dadd(dOW, (ks >> 2) * 16384 + (ks & 3) * 32), id_d1, ks > 0);
+            for (int ks = 0; ks < 8; ++ks)
+              mma_bf16_ss(tmem + TM_D1, dadd(dSt, ks * 2048),
+                          dadd(dOW, (ks >> 2) * 16384 + (ks & 3) * 32), id_d1, ks > 0);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_bf16_ss(tmem + TM_D3, dadd(dDSt, ks * 2048), dadd(dU, ks * 2048), id_d3, ks > 0);
-          mma_commit(&bars[B_HE]);
+            for (int ks = 0; ks < 8; ++ks)
+              mma_bf16_ss(tmem + TM_D3, dadd(dDSt, ks * 2048), dadd(dU, ks * 2048), id_d3, ks > 0);
+            mma_commit(&bars[B_HE]);
+          }
         }
         __syncwarp();
         const bool kq = wait_w(B_KQ, y & 1);
         named_bar(NB_NM, NB_ALL);  // [dN; dM] written
-        if (have && kq && leader && !*abort_flag) {
+        if (have && kq && live()) {
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ss(tmem + TM_D4, dadd(dKt, ks * 2048), dadd(dNM, ks * 32), id_d1, ks > 0);
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_ss(tmem + TM_D4, dadd(dKt, ks * 2048), dadd(dNM, ks * 32), id_d1, ks > 0);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ss(tmem + TM_D5, dadd(dQt, ks * 2048), dadd(dNn, ks * 2048), id_d3, ks > 0);
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_ss(tmem + TM_D5, dadd(dQt, ks * 2048), dadd(dNn, ks * 2048), id_d3, ks > 0);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ss(tmem + TM_D5, dadd(dKt, ks * 2048), dadd(dMn, ks * 2048), id_d3, 1);
-          mma_commit(&bars[B_N]);
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_ss(tmem + TM_D5, dadd(dKt, ks * 2048), dadd(dMn, ks * 2048), id_d3, 1);
+            mma_commit(&bars[B_N]);
+          }
         }
         __syncwarp();
       }
     }
     if (x > 0) named_bar(NB_D, NB_ALL);  // the last step's arrivals
-    if (lane == 0) {
+    if (elect_one()) {
       mma_commit(&bars[B_DRAIN]);
       if (!mbar_wait(&bars[B_DRAIN], 0)) fail(GDN_ERR_TIMEOUT);
     }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -558,13 +560,11 @@ cudaError_t launch_bwd_grads(const Args& a, cudaStream_t s) {
   p.N = a.N;
   p.Hk = a.Hk;
   p.Hv = a.Hv;
-  const int64_t rows = slots * a.Hv * (256 + 256 + 128);  // S, dS, U: rows of 64 columns
-  if (rows > 0x7fffffff || n_tok > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  CUtensorMap mk, mq, mo, mv, mw;
+  if (n_tok > 0x7fffffff) return cudaErrorInvalidConfiguration;  // TMA coordinates are 32-bit
+  CUtensorMap mk, mq, mo, mv;
   const int64_t hv = (int64_t)a.Hv * tm::D;
   if (!make_tok_map(&mk, a.k, a.Hk, n_tok, a.ts.k) || !make_tok_map(&mq, a.q, a.Hk, n_tok, a.ts.q) ||
-      !make_tok_map(&mo, a.dout, a.Hv, n_tok, hv) || !make_tok_map(&mv, a.dv_, a.Hv, n_tok, hv) ||
-      !make_rows64_map(&mw, ws + p.at.s, rows, 128))
+      !make_tok_map(&mo, a.dout, a.Hv, n_tok, hv) || !make_tok_map(&mv, a.dv_, a.Hv, n_tok, hv))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -573,7 +573,7 @@ cudaError_t launch_bwd_grads(const Args& a, cudaStream_t s) {
     e = cudaFuncSetAttribute(bwd_grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_BYTES);
   if (e != cudaSuccess) return e;
   const int64_t grid = p.items < sms ? p.items : sms;
-  bwd_grads_kernel<<<(unsigned)grid, THREADS, SM_BYTES, s>>>(mk, mq, mo, mv, mw, p);
+  bwd_grads_kernel<<<(unsigned)grid, THREADS, SM_BYTES, s>>>(mk, mq, mo, mv, p);
   return cudaGetLastError();
 }
 

@@ -19,6 +19,8 @@
 //   S  [n][2][128][64]  bf16: two 64-column halves of the state (rows: value index)
 //   DS [n][2][128][64]  bf16: the gradient of the state leaving the chunk
 //   U  [n][128][64]  bf16: U^T (rows: value index, columns: tokens of the chunk)
+// S, DS and U are kept as the 128-byte-swizzled images that the MMAs read (ptx::sw128), written and read by
+// plain bulk copies.
 #pragma once
 
 #include "bwd_internal.cuh"
