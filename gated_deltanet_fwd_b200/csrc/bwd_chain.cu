@@ -6,7 +6,7 @@
 // results are A operands from tensor memory and every B operand is a TMA-loaded tile:
 //   forward, chunk by chunk from the first (X' = -(S K^T) Gamma):
 //     D  = S_bf16 K^T          N 64,  K 128   critical
-//     E  = V^T T~^T            N 64,  K 64    early
+//     E  = V^T T~^T            N 64,  K 64    while X' is formed
 //     E += X' T~^T             N 64,  K 64    critical
 //     S  = Gamma_63 S + (beta d E) K      N 128, K 64   critical
 //   backward, from the last chunk (X = beta (scale D2 + d D)):
@@ -15,14 +15,14 @@
 //     W  = X T~                N 64,  K 64    critical: dW^T = dV^T
 //     dS = Gamma_63 dS + dO^T (scale Gamma Q) - (Gamma W) K     N 128, K 64 twice, the second critical
 // Warp roles (448 threads): warps 0-7 the critical epilogues (warps w and w + 4 share 32 lanes and split the
-// columns); warps 8-11 the side work (the carried matrix scaled by Gamma_63 and, in the same pass over
-// it, its bf16 copy to the workspace; scale Gamma Q in place; U or dv to memory); warp 12 the TMA
-// producer; warp 13 the MMA issuer.  What bounds it is the latency of the critical sequence of one
-// chunk, not traffic.  Three things that shorten it, by clock stamps of a 64-chunk run:
+// columns) and, while the first product of a chunk runs, the carried matrix scaled by Gamma_63 and its
+// bf16 copy on its way to the workspace; warps 8-11 U or dv to memory and scale Gamma Q in place; warp 12
+// the TMA producer; warp 13 the MMA issuer.  What bounds it is the latency of the critical sequence of
+// one chunk, not traffic.  Three things that shorten it, by clock stamps of a 64-chunk run:
 //   - MMAs are issued under elect.sync, which tells the compiler that one thread is active: 35 to 45
 //     cycles apart (A in tensor memory) against 134 under a plain lane test;
-//   - the bf16 copy leaves through shared memory and one bulk copy: stores of 32 bytes a lane, 256 bytes
-//     apart, held up every warp of the SM for 1300 of a chunk's 6300 cycles;
+//   - the bf16 copy, U and dv leave through shared memory and bulk copies: stores of 32 bytes a lane, 256
+//     bytes apart, held up every warp of the SM for 1300 of a chunk's 6300 cycles;
 //   - two warps per lane quarter halve each epilogue's columns.
 //
 // A chunk that ends inside a tile: rows of K, Q, V, dO behind the sequence end hold whatever follows in
@@ -51,19 +51,19 @@ struct Sm {
   static constexpr uint32_t TX = GD + GD_BYTES;  // bytes of a full stage
   static constexpr int STAGES = BACK ? 2 : 3;
   static constexpr uint32_t COPY = STAGES * STAGE;     // bf16 copy of the carried matrix on its way out
-  static constexpr uint32_t UOUT = COPY + 32768;       // forward: U^T on its way out
-  static constexpr uint32_t BAR = UOUT + (BACK ? 0 : 16384), BYTES = BAR + 256 + 1024;
+  static constexpr uint32_t OUT = COPY + 32768;        // U^T (forward) or dv (backward) on its way out
+  static constexpr uint32_t BAR = OUT + 16384, BYTES = BAR + 256 + 1024;
   static_assert(STAGE % 1024 == 0 && BYTES <= 232448, "stage layout");
 };
 
 enum { B_FULL0 = 0, B_EMPTY0 = 3, B_FIX = 6, B_K = 7, B_U = 8, B_S = 9, B_DRAIN = 10, B_N = 11 };
 
 // named barriers: hand-offs to the MMA issuer and between the two groups
-enum { NB_X = 1, NB_U = 2, NB_S = 3, NB_SR = 4, NB_G = 5, NB_SIDE = 6 };
+enum { NB_X = 1, NB_U = 2, NB_S = 3, NB_COPY = 4, NB_G = 5, NB_SIDE = 6 };
 constexpr int NB_ALL = 416;  // both groups + issuer warp
 constexpr int NB_CI = 288;   // critical group + issuer warp
 constexpr int NB_SI = 160;   // side group + issuer warp
-constexpr int NB_CS = 384;   // both groups
+constexpr int NB_CC = 288;   // critical group + the side warp that sends the copy
 
 // tensor-memory columns
 constexpr uint32_t TM_S = 0, TM_D = 128, TM_D2 = 192, TM_U = 256, TM_SB = 320, TM_X = 384,
@@ -103,7 +103,7 @@ template <bool BACK>
 __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_q,
     const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_tp,
-    const ChainParams P) {
+    const __grid_constant__ CUtensorMap map_dv, const ChainParams P) {
   using L_ = Sm<BACK>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -168,8 +168,6 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
   auto wait_full = [&](int i) {
     return wait_w(B_FULL0 + i % L_::STAGES, (uint32_t)(i / L_::STAGES) & 1);
   };
-  // forward: two buffers in turn, since the next chunk's V^T T~^T starts before this one's are read
-  auto u_col = [&](int i) { return !BACK && (i & 1) ? TM_D2 : TM_U; };
   auto record = [&](int i) {
     return reinterpret_cast<const float*>(smem + (i % L_::STAGES) * L_::STAGE + L_::GD);
   };
@@ -179,13 +177,43 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
     const int half = warp >> 2;
     const int j = 32 * (warp & 3) + lane;  // value row = tensor-memory lane
     const uint32_t lo = (uint32_t)(32 * (warp & 3)) << 16;
-    // bf16 copy of this thread's 64 columns of the carried matrix
-    auto copy_out = [&](const float* v) {
-      uint32_t pk[32];
+    // The carried matrix entering step i (this thread's 64 columns, in v): its bf16 copy is the next
+    // product's operand and, in the same rounding, what the parallel kernel reads -- as the swizzled
+    // image that its MMAs take: row j, 16-byte piece c at (c ^ j % 8).  Then it is scaled by Gamma_63.
+    auto enter = [&](int i, float* v, bool ok) {
+      if (ok) {
 #pragma unroll
-      for (int q = 0; q < 32; ++q) pk[q] = pack2(v[2 * q], v[2 * q + 1]);
-      tmem_st16u(tmem + lo + TM_SB + 32 * half, *reinterpret_cast<uint32_t(*)[16]>(pk));
-      tmem_st16u(tmem + lo + TM_SB + 32 * half + 16, *reinterpret_cast<uint32_t(*)[16]>(pk + 16));
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) pk[q] = pack2(v[32 * hh + 2 * q], v[32 * hh + 2 * q + 1]);
+          tmem_st16u(tmem + lo + TM_SB + 32 * half + 16 * hh, pk);
+        }
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      named_bar_arrive(NB_S, NB_ALL);
+      ok = wait_full(i) && ok;
+      if (ok) {
+        const float gl = record(i)[63];
+        // the previous copy has left (awaited before NB_U)
+        unsigned char* row = smem + L_::COPY + half * 16384 + j * 128;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float* x = v + 8 * q;
+          *reinterpret_cast<uint4*>(row + ((q ^ (j & 7)) << 4)) =
+              make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]),
+                         pack2(x[6], x[7]));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= gl;
+          if (q & 1)
+            tmem_st16(tmem + lo + TM_S + 64 * half + 8 * (q - 1),
+                      *reinterpret_cast<float(*)[16]>(v + 8 * (q - 1)));
+        }
+        fence_proxy_async_smem();
+        tmem_st_wait();
+      }
+      named_bar_arrive(NB_COPY, NB_CC);
     };
     {
       const float* src = P.S_in ? P.S_in + sidx + (size_t)j * tm::D + 64 * half : nullptr;
@@ -199,19 +227,11 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
         v[4 * q4 + 2] = f.z;
         v[4 * q4 + 3] = f.w;
       }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        tmem_st16(tmem + lo + TM_S + 64 * half + 16 * q, *reinterpret_cast<float(*)[16]>(v + 16 * q));
-      copy_out(v);
-      tmem_st_wait();
-      tc_fence_before();
-      named_bar_arrive(NB_SR, NB_CS);  // the side group may take the matrix over
-      named_bar(NB_S, NB_ALL);
+      enter(0, v, true);
     }
     for (int i = 0; i < nch; ++i) {
       const float* gd = record(i) + 32 * half;
-      const uint32_t tm_u = tmem + lo + u_col(i) + 32 * half;
-      wait_full(i);  // the chunk's record is visible to this thread
+      const uint32_t tm_u = tmem + lo + TM_U + 32 * half;
       // ---- X'
       if (wait_w(B_K, i & 1)) {
         tc_fence_after();
@@ -271,23 +291,16 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
       // a full barrier, not an arrival: the group then never runs a barrier instance ahead of the
       // issuer, even when an abort makes it skip its waits
       named_bar(NB_U, NB_ALL);
-      // ---- refresh of the bf16 copy (not after the last chunk)
+      // ---- the updated matrix (not after the last chunk)
       const bool s_ok = wait_w(B_S, i & 1);
       if (i + 1 < nch) {
+        float v[64];
         if (s_ok) {
           tc_fence_after();
-          float v[64];
           ld64(tmem + lo + TM_S + 64 * half, v);
           tmem_ld_wait();
-          tc_fence_before();
-          named_bar_arrive(NB_SR, NB_CS);  // the matrix is read: the side group may scale it
-          copy_out(v);
-          tmem_st_wait();
-        } else {
-          named_bar_arrive(NB_SR, NB_CS);
         }
-        tc_fence_before();
-        named_bar(NB_S, NB_ALL);
+        enter(i + 1, v, s_ok);
       }
     }
   } else if (warp < W_PROD) {
@@ -299,92 +312,63 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
     auto scale_q = [&](int i) {
       if (!wait_full(i)) return;
       const float* gd = record(i);
-      unsigned char* qt = smem + (i % L_::STAGES) * L_::STAGE + L_::Q;
+      uint4* qt = reinterpret_cast<uint4*>(smem + (i % L_::STAGES) * L_::STAGE + L_::Q) + t4;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {  // 16-byte pieces; piece / 8 is a row of one of the halves
-        const int piece = e * 128 + t4;
-        uint4* p = reinterpret_cast<uint4*>(qt) + piece;
-        const float f = P.scale * gd[(piece >> 3) & 63];
-        uint4 w = *p;
-        uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+      for (int b = 0; b < 2; ++b) {  // 16-byte pieces; piece / 8 is a row of one of the halves
+        uint4 w[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          x[q] = pack2(f * __uint_as_float(x[q] << 16), f * __uint_as_float(x[q] & 0xffff0000u));
-        *p = w;
+        for (int e = 0; e < 4; ++e) w[e] = qt[(4 * b + e) * 128];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f = P.scale * gd[(((4 * b + e) * 128 + t4) >> 3) & 63];
+          uint32_t* x = reinterpret_cast<uint32_t*>(&w[e]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            x[q] = pack2(f * __uint_as_float(x[q] << 16), f * __uint_as_float(x[q] & 0xffff0000u));
+          qt[(4 * b + e) * 128] = w[e];
+        }
       }
       fence_proxy_async_smem();
     };
-    // The carried matrix entering step i: its bf16 copy to the workspace, then scaled by Gamma_63 in
-    // tensor memory (after the critical group has read it).  The copy is the swizzled image that
-    // the MMAs of the parallel kernel read: row j, 16-byte piece c at (c ^ j % 8).
-    auto take = [&](int i) {
-      // the previous copy has left shared memory (forward: U may still be on its way)
-      if (t4 == 0) bulk_wait_read<BACK ? 0 : 1>();
-      named_bar(NB_SR, NB_CS);
-      tc_fence_after();
-      const bool ok = wait_full(i) && __all_sync(0xffffffffu, !*abort_flag);
-      if (ok) {
-        const float gl = record(i)[63];
-        unsigned char* row = smem + L_::COPY + j * 128;
-#pragma unroll
-        for (int hh = 0; hh < 4; ++hh) {
-          float v[32];
-          ld32(tmem + lo + TM_S + 32 * hh, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float* x = v + 8 * q;
-            *reinterpret_cast<uint4*>(row + (hh >> 1) * 16384 +
-                                      (((4 * (hh & 1) + q) ^ (j & 7)) << 4)) =
-                make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]),
-                           pack2(x[6], x[7]));
-          }
-#pragma unroll
-          for (int q = 0; q < 32; ++q) v[q] *= gl;
-          tmem_st16(tmem + lo + TM_S + 32 * hh, *reinterpret_cast<float(*)[16]>(v));
-          tmem_st16(tmem + lo + TM_S + 32 * hh + 16, *reinterpret_cast<float(*)[16]>(v + 16));
-        }
-        tmem_st_wait();
-        fence_proxy_async_smem();
-      }
-      return ok;
-    };
-    auto send = [&](int i, bool ok) {
-      named_bar(NB_SIDE, 128);
-      if (t4 == 0 && ok) {
+    // One warp sends the copy of the matrix entering step i.
+    auto send = [&](int i) {
+      if (warp != W_SIDE) return;
+      named_bar(NB_COPY, NB_CC);
+      if (t4 == 0 && !*abort_flag) {
         const size_t sh = (size_t)(slot0 + chunk_of(i)) * P.Hv + h;
         bulk_store(P.ws + (BACK ? P.at.ds : P.at.s) + sh * 32768, smem + L_::COPY, 32768);
         bulk_commit();
       }
+      __syncwarp();
     };
     named_bar_arrive(NB_S, NB_ALL);
-    if (BACK) scale_q(0);
-    {
-      const bool ok = take(0);
-      tc_fence_before();
-      if (BACK) named_bar_arrive(NB_G, NB_SI);
-      send(0, ok);
+    if (BACK) {
+      scale_q(0);
+      named_bar_arrive(NB_G, NB_SI);
     }
+    send(0);
     for (int i = 0; i < nch; ++i) {
-      if (!BACK && t4 == 0) bulk_wait_read<1>();  // the previous U has left shared memory
-      named_bar(NB_U, NB_ALL);  // matrix scaled; a full barrier (see the other group)
+      if (t4 == 0) bulk_wait_read<0>();  // everything sent so far has left shared memory
+      named_bar(NB_U, NB_ALL);           // a full barrier (see the other group)
       const int c = chunk_of(i);
       // E^T or dW^T: complete since the critical group has waited for it
       bool ok = wait_w(B_U, i & 1);
-      uint32_t ob[32];
+      if (!BACK) ok = wait_full(i) && ok;  // the record is visible to this thread
+      uint32_t ob[32];  // tokens 2q, 2q + 1 of value row j
       if (ok) {
         tc_fence_after();
         const float* be = record(i) + 128;
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           float t[32];
-          ld32(tmem + lo + u_col(i) + 32 * hh, t);
+          ld32(tmem + lo + TM_U + 32 * hh, t);
           tmem_ld_wait();
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
             if (!BACK) {
-              t[2 * q] *= be[32 * hh + 2 * q];
-              t[2 * q + 1] *= be[32 * hh + 2 * q + 1];
+              const float2 b2 = *reinterpret_cast<const float2*>(be + 32 * hh + 2 * q);
+              t[2 * q] *= b2.x;
+              t[2 * q + 1] *= b2.y;
             }
             ob[16 * hh + q] = pack2(t[2 * q], t[2 * q + 1]);
           }
@@ -392,50 +376,62 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
       }
       tc_fence_before();
       if (i + 1 < nch) named_bar_arrive(NB_S, NB_ALL);  // U / dW read
-      if (!BACK && ok) {
-        // U^T, the same kind of image
-        unsigned char* row = smem + L_::UOUT + j * 128;
+      const int L = rows_of(c);
+      if (ok && !BACK) {  // U^T, the same kind of image
+        unsigned char* row = smem + L_::OUT + j * 128;
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           *reinterpret_cast<uint4*>(row + ((q ^ (j & 7)) << 4)) =
               make_uint4(ob[4 * q], ob[4 * q + 1], ob[4 * q + 2], ob[4 * q + 3]);
-        fence_proxy_async_smem();
       }
-      if (!BACK) {
-        named_bar(NB_SIDE, 128);
-        if (t4 == 0) {
-          mbar_arrive(&bars[B_EMPTY0 + i % L_::STAGES]);
-          if (ok) {
-            const size_t sh = (size_t)(slot0 + c) * P.Hv + h;
-            bulk_store(P.ws + P.at.u + sh * 16384, smem + L_::UOUT, 16384);
-            bulk_commit();
+      if (ok && BACK) {
+        // dv, [token][channel], two bytes at a time: a warp's 32 channels are 64 consecutive bytes.  (Swapping
+        // halves between lanes for 4-byte stores took 3700 cycles a chunk against 400.)  A whole chunk
+        // goes out as the box of a tensor map, a partial one row by row.
+        if (L == tm::C) {
+          unsigned char* tile = smem + L_::OUT + (j >> 6) * 8192 + (j & 7) * 2;
+          const uint32_t c8 = (uint32_t)(j & 63) >> 3;
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            const uint32_t r = 2 * q;
+            *reinterpret_cast<uint16_t*>(tile + r * 128 + ((c8 ^ (r & 7)) << 4)) = (uint16_t)ob[q];
+            *reinterpret_cast<uint16_t*>(tile + (r + 1) * 128 + ((c8 ^ ((r + 1) & 7)) << 4)) =
+                (uint16_t)(ob[q] >> 16);
+          }
+        } else {
+          const int64_t rs = (int64_t)P.Hv * tm::D;
+          uint16_t* dst = reinterpret_cast<uint16_t*>(P.dv + (s_beg + (int64_t)tm::C * c) * rs +
+                                                      h * tm::D + j);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            if (2 * q < L) dst[(int64_t)(2 * q) * rs] = (uint16_t)ob[q];
+            if (2 * q + 1 < L) dst[(int64_t)(2 * q + 1) * rs] = (uint16_t)(ob[q] >> 16);
           }
         }
       }
-      if (i + 1 < nch) {
-        if (BACK) scale_q(i + 1);
-        const bool copied = take(i + 1);
-        tc_fence_before();
-        if (BACK) named_bar_arrive(NB_G, NB_SI);
-        send(i + 1, copied);
-      }
-      if (BACK && ok) {
-        // lanes j, j ^ 1 swap halves: an even lane stores row 2q at columns j, j + 1, an odd lane row
-        // 2q + 1 at columns j - 1, j -- each warp store two contiguous 64-byte row segments
-        const int64_t t0 = s_beg + (int64_t)tm::C * c;
-        const int L = rows_of(c);
-        const int odd = j & 1;
-        const int64_t rs = (int64_t)P.Hv * tm::D;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(P.dv + (t0 + odd) * rs + h * tm::D + (j & ~1));
-        const uint32_t sel = odd ? 0x7632u : 0x5410u;
-#pragma unroll 8
-        for (int q = 0; q < 32; ++q) {
-          const uint32_t mine = ob[q];
-          const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-          const uint32_t pair = odd ? __byte_perm(other, mine, sel) : __byte_perm(mine, other, sel);
-          if (2 * q + odd < L) *dst = pair;
-          dst += rs;  // two token rows of bf16, counted in 4-byte units
+      fence_proxy_async_smem();
+      named_bar(NB_SIDE, 128);
+      if (t4 == 0) {
+        if (!BACK) mbar_arrive(&bars[B_EMPTY0 + i % L_::STAGES]);
+        if (ok && !BACK) {
+          const size_t sh = (size_t)(slot0 + c) * P.Hv + h;
+          bulk_store(P.ws + P.at.u + sh * 16384, smem + L_::OUT, 16384);
+          bulk_commit();
         }
+        if (ok && BACK && L == tm::C) {
+          const int32_t t0 = (int32_t)(s_beg + (int64_t)tm::C * c);
+          tma_store_3d(&map_dv, smem + L_::OUT, 0, h, t0);
+          tma_store_3d(&map_dv, smem + L_::OUT + 8192, 64, h, t0);
+          bulk_commit();
+        }
+      }
+      __syncwarp();
+      if (i + 1 < nch) {
+        if (BACK) {
+          scale_q(i + 1);
+          named_bar_arrive(NB_G, NB_SI);
+        }
+        send(i + 1);
       }
     }
     if (t4 == 0) bulk_wait<0>();  // nothing on its way out of shared memory
@@ -512,7 +508,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
     for (int i = 0; i < nch; ++i) {
       const int st = i % L_::STAGES;
       const uint32_t sp = sbase + st * L_::STAGE;
-      const uint32_t tm_u = tmem + u_col(i);
+      const uint32_t tm_u = tmem + TM_U;
       const bool have = wait_full(i);
       const uint64_t dK = sdesc_sw128(sp + L_::K, 16, 1024);       // K as K-major B
       const uint64_t dKn = sdesc_sw128(sp + L_::K, 8192, 1024);    // K as MN-major B
@@ -522,18 +518,12 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
                                : sdesc_sw128(sp + L_::TP, 16, 1024);    // T~ as K-major B
       const uint64_t dP = sdesc_sw128(sp + L_::TP + 8192, 8192, 1024);  // P as MN-major B
       constexpr uint32_t t_step = BACK ? 2048 : 32;
-      if (have && live()) {
+      if (BACK && have && live()) {  // state-independent; D2 was read before the previous chunk's NB_U
         tc_fence_after();
-        // state-independent.  Backward: D2 was read before the previous chunk's NB_U.  Forward: these
-        // columns were read by the side group before the previous chunk's NB_S (two buffers).
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            if (BACK)
-              mma_bf16_ss(tmem + TM_D2, dadd(dXt, ks * 2048), dadd(dP, ks * 2048), id_e, ks > 0);
-            else
-              mma_bf16_ss(tm_u, dadd(dXt, ks * 2048), dadd(dT, ks * 32), id_e, ks > 0);
-          }
+          for (int ks = 0; ks < 4; ++ks)
+            mma_bf16_ss(tmem + TM_D2, dadd(dXt, ks * 2048), dadd(dP, ks * 2048), id_e, ks > 0);
         }
       }
       __syncwarp();
@@ -547,6 +537,11 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
             mma_bf16_ts(tmem + TM_D, tmem + TM_SB + 8 * ks,
                         dadd(dK, (ks >> 2) * 8192 + (ks & 3) * 32), id_k, ks > 0);
           mma_commit(&bars[B_K]);
+          if (!BACK) {  // state-independent, while X' is formed
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_ss(tm_u, dadd(dXt, ks * 2048), dadd(dT, ks * 32), id_e, ks > 0);
+          }
         }
       }
       __syncwarp();
@@ -638,17 +633,18 @@ cudaError_t launch_t(const Args& a, cudaStream_t s) {
   p.N = a.N;
   p.Hk = a.Hk;
   p.Hv = a.Hv;
-  CUtensorMap mk, mq, mx, mt;
+  CUtensorMap mk, mq, mx, mt, mv;
   if (!make_tok_map(&mk, a.k, a.Hk, n_tok, a.ts.k) || !make_tok_map(&mq, a.q, a.Hk, n_tok, a.ts.q) ||
       !make_tok_map(&mx, BACK ? a.dout : a.v, a.Hv, n_tok,
                     BACK ? (int64_t)a.Hv * tm::D : a.ts.v) ||
-      !make_rows64_map(&mt, ws + p.at.tp, slots * a.Hv * 128, BACK ? 128 : 64))
+      !make_rows64_map(&mt, ws + p.at.tp, slots * a.Hv * 128, BACK ? 128 : 64) ||
+      !make_tok_map(&mv, a.dv_, a.Hv, n_tok, (int64_t)a.Hv * tm::D))
     return cudaErrorInvalidValue;
   const cudaError_t e =
       cudaFuncSetAttribute(bwd_chain_kernel<BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Sm<BACK>::BYTES);
   if (e != cudaSuccess) return e;
-  bwd_chain_kernel<BACK><<<(unsigned)units, THREADS, Sm<BACK>::BYTES, s>>>(mk, mq, mx, mt, p);
+  bwd_chain_kernel<BACK><<<(unsigned)units, THREADS, Sm<BACK>::BYTES, s>>>(mk, mq, mx, mt, mv, p);
   return cudaGetLastError();
 }
 
