@@ -14,7 +14,7 @@
 //     D2 = dO^T P              N 64,  K 64    early
 //     W  = X T~                N 64,  K 64    critical: dW^T = dV^T
 //     dS = Gamma_63 dS + dO^T (scale Gamma Q) - (Gamma W) K     N 128, K 64 twice, the second critical
-// Warp roles (448 threads): warps 0-7 the critical epilogues (warps w and w + 4 share 32 lanes and split the
+// Warp roles (512 threads): warps 0-7 the critical epilogues (warps w and w + 4 share 32 lanes and split the
 // columns) and, while the first product of a chunk runs, the carried matrix scaled by Gamma_63 and its
 // bf16 copy on its way to the workspace; warps 8-11 U or dv to memory and scale Gamma Q in place; warp 12
 // the TMA producer; warp 13 the MMA issuer.  What bounds it is the latency of the critical sequence of
@@ -39,8 +39,12 @@ namespace {
 
 using namespace ptx;
 
-constexpr int THREADS = 448;
-constexpr int W_SIDE = 8, W_PROD = 12;  // warp 13 issues the MMAs
+// Four warpgroups: critical (two), side, and producer + issuer (two of its warps idle).  The launch gives
+// every thread 128 registers; the last group hands 48 of its own back and the critical groups take 24
+// each, which keeps them from spilling -- to an L1 that shared memory leaves almost nothing of.
+// 2 x 152 + 128 + 80 = 4 x 128.
+constexpr int THREADS = 512;
+constexpr int W_SIDE = 8, W_PROD = 12, W_MMA = 13;
 
 // shared memory, from a 1024-aligned base; a stage holds one chunk's tiles: K, [Q,] V or dO, T~ [and P],
 // the record.  64-row tiles are two 64-column halves 8192 bytes apart.
@@ -156,10 +160,18 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
     report(P.status, code);
     *abort_flag = 1;
   };
-  // a bounded wait, skipped once the CTA is aborting
+  // A bounded wait that gives up early once the CTA is aborting.  The flag is looked at only while the
+  // phase is incomplete: shared-memory reads queue behind the epilogues' traffic.
   auto wait = [&](int b, uint32_t parity) -> bool {
-    if (*abort_flag) return false;
-    if (mbar_wait(&bars[b], parity)) return true;
+    if (mbar_try_wait(&bars[b], parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t k = 0; k < kSpinLimit; ++k) {
+      if (mbar_try_wait(&bars[b], parity)) return true;
+      if ((k & 63) == 63) {
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+      }
+    }
     fail(GDN_ERR_TIMEOUT);
     return false;
   };
@@ -173,6 +185,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
   };
 
   if (warp < W_SIDE) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     // -------------------------------------------------------------- critical epilogues -------
     const int half = warp >> 2;
     const int j = 32 * (warp & 3) + lane;  // value row = tensor-memory lane
@@ -301,6 +314,15 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
           tmem_ld_wait();
         }
         enter(i + 1, v, s_ok);
+      } else if (BACK && P.S_out && s_ok) {  // the gradient of the initial state
+        tc_fence_after();
+        float v[64];
+        ld64(tmem + lo + TM_S + 64 * half, v);
+        tmem_ld_wait();
+        float4* dst = reinterpret_cast<float4*>(P.S_out + sidx + (size_t)j * tm::D + 64 * half);
+#pragma unroll
+        for (int q4 = 0; q4 < 16; ++q4)
+          dst[q4] = make_float4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
       }
     }
   } else if (warp < W_PROD) {
@@ -435,7 +457,9 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
       }
     }
     if (t4 == 0) bulk_wait<0>();  // nothing on its way out of shared memory
-  } else if (warp == W_PROD) {
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == W_PROD) {
     // -------------------------------------------------------------- TMA producer -------------
     if (elect_one()) {
       prefetch_tensormap(&map_k);
@@ -497,19 +521,20 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
       for (int i = issued > L_::STAGES ? issued - L_::STAGES : 0; i < issued; ++i)
         if (!mbar_wait(&bars[B_FULL0 + i % L_::STAGES], (uint32_t)(i / L_::STAGES) & 1))
           report(P.status, GDN_ERR_TIMEOUT);
-  } else {
+    } else if (warp == W_MMA) {
     // -------------------------------------------------------------- MMA issuer ---------------
     const uint32_t id_k = idesc_bf16(128, 64, 0, 0);             // A tensor memory, B K-major
     const uint32_t id_e = idesc_bf16(128, 64, 1, BACK ? 1 : 0);  // A smem MN-major
     const uint32_t id_u = idesc_bf16(128, 64, 0, BACK ? 1 : 0);  // T~^T forward, T~ backward
     const uint32_t id_s = idesc_bf16(128, 128, 0, 1);            // B = K, MN-major
     const uint32_t id_q = idesc_bf16(128, 128, 1, 1);            // A = dO^T, B = scale Gamma Q
-    auto live = [&]() { return __all_sync(0xffffffffu, !*abort_flag) != 0; };
     for (int i = 0; i < nch; ++i) {
       const int st = i % L_::STAGES;
       const uint32_t sp = sbase + st * L_::STAGE;
       const uint32_t tm_u = tmem + TM_U;
-      const bool have = wait_full(i);
+      // the chunk's tiles have landed and nothing failed so far; a failure later in the chunk leaves its
+      // MMAs to run on whatever is there, in bounds all the same
+      const bool go = wait_full(i) && __all_sync(0xffffffffu, !*abort_flag);
       const uint64_t dK = sdesc_sw128(sp + L_::K, 16, 1024);       // K as K-major B
       const uint64_t dKn = sdesc_sw128(sp + L_::K, 8192, 1024);    // K as MN-major B
       const uint64_t dQn = sdesc_sw128(sp + L_::Q, 8192, 1024);
@@ -518,7 +543,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
                                : sdesc_sw128(sp + L_::TP, 16, 1024);    // T~ as K-major B
       const uint64_t dP = sdesc_sw128(sp + L_::TP + 8192, 8192, 1024);  // P as MN-major B
       constexpr uint32_t t_step = BACK ? 2048 : 32;
-      if (BACK && have && live()) {  // state-independent; D2 was read before the previous chunk's NB_U
+      if (BACK && go) {  // state-independent; D2 was read before the previous chunk's NB_U
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -528,7 +553,6 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
       }
       __syncwarp();
       named_bar(NB_S, NB_ALL);  // bf16 copy in place, U / dW of the previous chunk read
-      const bool go = have && live();
       if (go) {
         tc_fence_after();
         if (elect_one()) {
@@ -546,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
       }
       __syncwarp();
       named_bar(NB_X, NB_CI);  // X' written
-      if (go && live()) {
+      if (go) {
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -558,7 +582,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
       __syncwarp();
       if (BACK) {
         named_bar(NB_G, NB_SI);  // dS scaled, scale Gamma Q written
-        if (go && live()) {
+        if (go) {
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -569,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
         __syncwarp();
       }
       named_bar(NB_U, NB_ALL);  // the update's operand written; matrix scaled
-      if (go && live()) {
+      if (go) {
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -587,23 +611,10 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
       if (!mbar_wait(&bars[B_DRAIN], 0)) fail(GDN_ERR_TIMEOUT);
     }
     __syncwarp();
+    }
   }
 
-  // the issuer's drain (and any abort) is visible to every thread after this barrier
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (BACK && warp < W_SIDE && P.S_out && __all_sync(0xffffffffu, !*abort_flag)) {
-    const int j = 32 * (warp & 3) + lane, half = warp >> 2;
-    float* dst = P.S_out + sidx + (size_t)j * tm::D + 64 * half;
-    float v[64];
-    ld64(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + TM_S + 64 * half, v);
-    tmem_ld_wait();
-#pragma unroll
-    for (int q4 = 0; q4 < 16; ++q4)
-      reinterpret_cast<float4*>(dst)[q4] =
-          make_float4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
-  }
+  // the issuer's drain is over for every thread after this barrier
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
