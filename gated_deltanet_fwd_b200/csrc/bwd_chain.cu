@@ -9,18 +9,18 @@
 //     E  = V^T T~^T            N 64,  K 64    while X' is formed
 //     E += X' T~^T             N 64,  K 64    critical
 //     S  = Gamma_63 S + (beta d E) K      N 128, K 64   critical
-//   backward, from the last chunk (X = beta (scale D2 + d D)):
+//   backward, from the last chunk (X = beta (D2 + d D)):
 //     D  = dS_bf16 K^T         N 64,  K 128   critical
-//     D2 = dO^T P              N 64,  K 64    early
+//     D2 = dO^T (scale P)              N 64,  K 64    early
 //     W  = X T~                N 64,  K 64    critical: dW^T = dV^T
 //     dS = Gamma_63 dS + dO^T (scale Gamma Q) - (Gamma W) K     N 128, K 64 twice, the second critical
 // Warp roles (512 threads): warps 0-7 the critical epilogues (warps w and w + 4 share 32 lanes and split the
-// columns) and, while the first product of a chunk runs, the carried matrix scaled by Gamma_63 and its
-// bf16 copy on its way to the workspace; warps 8-11 U or dv to memory and scale Gamma Q in place; warp 12
-// the TMA producer; warp 13 the MMA issuer.  What bounds it is the latency of the critical sequence of
+// columns) and, while the first product of a chunk runs, the carried matrix scaled by Gamma_63; warps 8-11
+// its bf16 copy, and U or dv, to memory; warp 12 the TMA producer; warp 13 the MMA issuer.  What bounds it is the latency of the critical sequence of
 // one chunk, not traffic.  Three things that shorten it, by clock stamps of a 64-chunk run:
-//   - MMAs are issued under elect.sync, which tells the compiler that one thread is active: 35 to 45
-//     cycles apart (A in tensor memory) against 134 under a plain lane test;
+//   - MMAs are issued under elect.sync, which tells the compiler that one thread is active, with
+//     descriptors that are loop-invariant but for constants (the stage is a template argument): about 10
+//     cycles apart, against 134 under a plain lane test and 45 with descriptors computed in the loop;
 //   - the bf16 copy, U and dv leave through shared memory and bulk copies: stores of 32 bytes a lane, 256
 //     bytes apart, held up every warp of the SM for 1300 of a chunk's 6300 cycles;
 //   - two warps per lane quarter halve each epilogue's columns.
@@ -30,6 +30,8 @@
 // publishes the stage.  Waits are bounded: one that runs out records GDN_ERR_TIMEOUT, and from
 // then on every role skips its work but keeps the barrier sequence, so the CTA leaves together with
 // nothing in flight.
+#include <type_traits>
+
 #include "bwd_tc.cuh"
 #include "ptx.cuh"
 
@@ -39,10 +41,10 @@ namespace {
 
 using namespace ptx;
 
-// Four warpgroups: critical (two), side, and producer + issuer (two of its warps idle).  The launch gives
-// every thread 128 registers; the last group hands 48 of its own back and the critical groups take 24
-// each, which keeps them from spilling -- to an L1 that shared memory leaves almost nothing of.
-// 2 x 152 + 128 + 80 = 4 x 128.
+// Four warpgroups: critical (two), side, and producer + issuer (two warps idle).  The launch gives
+// every thread 128 registers.  The backward walk's critical groups need more and take them from the other
+// two (2 x 144 + 120 + 104 = 4 x 128): spills cost twice here, since shared memory leaves almost no L1
+// (a backward chunk took 3.2 us with 140 spilled bytes against 2.6 us without).
 constexpr int THREADS = 512;
 constexpr int W_SIDE = 8, W_PROD = 12, W_MMA = 13;
 
@@ -54,8 +56,8 @@ struct Sm {
                             GD = TP + (BACK ? 16384 : 8192), STAGE = GD + 1024;
   static constexpr uint32_t TX = GD + GD_BYTES;  // bytes of a full stage
   static constexpr int STAGES = BACK ? 2 : 3;
-  static constexpr uint32_t COPY = STAGES * STAGE;     // bf16 copy of the carried matrix on its way out
-  static constexpr uint32_t OUT = COPY + 32768;        // U^T (forward) or dv (backward) on its way out
+  static constexpr uint32_t COPY = STAGES * STAGE;     // bf16 copies of the carried matrix on their way out
+  static constexpr uint32_t OUT = COPY + 2 * 32768;    // U^T (forward) or dv (backward) on its way out
   static constexpr uint32_t BAR = OUT + 16384, BYTES = BAR + 256 + 1024;
   static_assert(STAGE % 1024 == 0 && BYTES <= 232448, "stage layout");
 };
@@ -63,11 +65,10 @@ struct Sm {
 enum { B_FULL0 = 0, B_EMPTY0 = 3, B_FIX = 6, B_K = 7, B_U = 8, B_S = 9, B_DRAIN = 10, B_N = 11 };
 
 // named barriers: hand-offs to the MMA issuer and between the two groups
-enum { NB_X = 1, NB_U = 2, NB_S = 3, NB_COPY = 4, NB_G = 5, NB_SIDE = 6 };
-constexpr int NB_ALL = 416;  // both groups + issuer warp
-constexpr int NB_CI = 288;   // critical group + issuer warp
-constexpr int NB_SI = 160;   // side group + issuer warp
-constexpr int NB_CC = 288;   // critical group + the side warp that sends the copy
+enum { NB_X = 1, NB_U = 2, NB_S = 3, NB_COPY = 4, NB_SIDE = 5 };
+constexpr int NB_CSI = 416;   // both groups + issuer warp
+constexpr int NB_CI = 288;    // critical group + issuer warp
+constexpr int NB_CS = 384;    // both groups
 
 // tensor-memory columns
 constexpr uint32_t TM_S = 0, TM_D = 128, TM_D2 = 192, TM_U = 256, TM_SB = 320, TM_X = 384,
@@ -82,7 +83,6 @@ struct ChainParams {
   int* status;
   int64_t T;
   TcLayout at;
-  float scale;
   int N, Hk, Hv;
 };
 
@@ -105,8 +105,7 @@ __device__ __forceinline__ void ld64(uint32_t taddr, float* v) {
 
 template <bool BACK>
 __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
-    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_q,
-    const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_tp,
+    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_tp,
     const __grid_constant__ CUtensorMap map_dv, const ChainParams P) {
   using L_ = Sm<BACK>;
   extern __shared__ unsigned char smem_raw[];
@@ -185,15 +184,14 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
   };
 
   if (warp < W_SIDE) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    if (BACK) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     // -------------------------------------------------------------- critical epilogues -------
     const int half = warp >> 2;
     const int j = 32 * (warp & 3) + lane;  // value row = tensor-memory lane
     const uint32_t lo = (uint32_t)(32 * (warp & 3)) << 16;
     // The carried matrix entering step i (this thread's 64 columns, in v): its bf16 copy is the next
-    // product's operand and, in the same rounding, what the parallel kernel reads -- as the swizzled
-    // image that its MMAs take: row j, 16-byte piece c at (c ^ j % 8).  Then it is scaled by Gamma_63.
-    auto enter = [&](int i, float* v, bool ok) {
+    // product's operand; then, while that product runs, the matrix is scaled by Gamma_63.
+    auto enter = [&](float* v, float gl, bool ok) {
       if (ok) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -205,28 +203,18 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
         tmem_st_wait();
       }
       tc_fence_before();
-      named_bar_arrive(NB_S, NB_ALL);
-      ok = wait_full(i) && ok;
+      named_bar_arrive(NB_S, NB_CSI);
+      named_bar_arrive(NB_COPY, NB_CS);
       if (ok) {
-        const float gl = record(i)[63];
-        // the previous copy has left (awaited before NB_U)
-        unsigned char* row = smem + L_::COPY + half * 16384 + j * 128;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float* x = v + 8 * q;
-          *reinterpret_cast<uint4*>(row + ((q ^ (j & 7)) << 4)) =
-              make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]),
-                         pack2(x[6], x[7]));
+        for (int q = 0; q < 4; ++q) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= gl;
-          if (q & 1)
-            tmem_st16(tmem + lo + TM_S + 64 * half + 8 * (q - 1),
-                      *reinterpret_cast<float(*)[16]>(v + 8 * (q - 1)));
+          for (int e = 0; e < 16; ++e) v[16 * q + e] *= gl;
+          tmem_st16(tmem + lo + TM_S + 64 * half + 16 * q,
+                    *reinterpret_cast<float(*)[16]>(v + 16 * q));
         }
-        fence_proxy_async_smem();
         tmem_st_wait();
       }
-      named_bar_arrive(NB_COPY, NB_CC);
     };
     {
       const float* src = P.S_in ? P.S_in + sidx + (size_t)j * tm::D + 64 * half : nullptr;
@@ -240,34 +228,40 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
         v[4 * q4 + 2] = f.z;
         v[4 * q4 + 3] = f.w;
       }
-      enter(0, v, true);
+      const bool ok = wait_full(0);
+      enter(v, ok ? record(0)[63] : 0.0f, true);
     }
     for (int i = 0; i < nch; ++i) {
       const float* gd = record(i) + 32 * half;
       const uint32_t tm_u = tmem + lo + TM_U + 32 * half;
-      // ---- X'
+      // ---- X'.  The record's values are read before the waits, not after them, where registers allow.
+      float4 ra[8];
+#pragma unroll
+      for (int q4 = 0; q4 < 8; ++q4)  // d, or Gamma
+        ra[q4] = *reinterpret_cast<const float4*>(gd + (BACK ? 64 : 0) + 4 * q4);
       if (wait_w(B_K, i & 1)) {
         tc_fence_after();
-        float d[32], d2[32];
-        ld32(tmem + lo + TM_D + 32 * half, d);
-        if (BACK) ld32(tmem + lo + TM_D2 + 32 * half, d2);
-        tmem_ld_wait();
         uint32_t pk[16];
 #pragma unroll
-        for (int q4 = 0; q4 < 8; ++q4) {
-          const float* x = d + 4 * q4;
-          if (!BACK) {
-            const float4 gm = *reinterpret_cast<const float4*>(gd + 4 * q4);
-            pk[2 * q4] = pack2(-gm.x * x[0], -gm.y * x[1]);
-            pk[2 * q4 + 1] = pack2(-gm.z * x[2], -gm.w * x[3]);
-          } else {
-            const float* y = d2 + 4 * q4;
-            const float4 dd = *reinterpret_cast<const float4*>(gd + 64 + 4 * q4);
-            const float4 be = *reinterpret_cast<const float4*>(gd + 128 + 4 * q4);
-            pk[2 * q4] = pack2(be.x * fmaf(dd.x, x[0], P.scale * y[0]),
-                               be.y * fmaf(dd.y, x[1], P.scale * y[1]));
-            pk[2 * q4 + 1] = pack2(be.z * fmaf(dd.z, x[2], P.scale * y[2]),
-                                   be.w * fmaf(dd.w, x[3], P.scale * y[3]));
+        for (int hh = 0; hh < 2; ++hh) {
+          float d[16], d2[16];
+          tmem_ld16(tmem + lo + TM_D + 32 * half + 16 * hh, d);
+          if (BACK) tmem_ld16(tmem + lo + TM_D2 + 32 * half + 16 * hh, d2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const float* x = d + 4 * q4;
+            const float4 a = ra[4 * hh + q4];
+            uint32_t* o = pk + 8 * hh + 2 * q4;
+            if (!BACK) {
+              o[0] = pack2(-a.x * x[0], -a.y * x[1]);
+              o[1] = pack2(-a.z * x[2], -a.w * x[3]);
+            } else {
+              const float* y = d2 + 4 * q4;
+              const float4 be = *reinterpret_cast<const float4*>(gd + 128 + 16 * hh + 4 * q4);
+              o[0] = pack2(be.x * fmaf(a.x, x[0], y[0]), be.y * fmaf(a.y, x[1], y[1]));
+              o[1] = pack2(be.z * fmaf(a.z, x[2], y[2]), be.w * fmaf(a.w, x[3], y[3]));
+            }
           }
         }
         tmem_st16u(tmem + lo + TM_X + 16 * half, pk);
@@ -275,7 +269,18 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
       }
       tc_fence_before();
       named_bar_arrive(NB_X, NB_CI);
-      // ---- the update's operand
+      // ---- the update's operand: beta d E, or -Gamma dW
+#pragma unroll
+      for (int q4 = 0; q4 < 8; ++q4) {
+        if (!BACK) {
+          const float4 dd = *reinterpret_cast<const float4*>(gd + 64 + 4 * q4);
+          const float4 be = *reinterpret_cast<const float4*>(gd + 128 + 4 * q4);
+          ra[q4] = make_float4(be.x * dd.x, be.y * dd.y, be.z * dd.z, be.w * dd.w);
+        } else {
+          const float4 gm = *reinterpret_cast<const float4*>(gd + 4 * q4);
+          ra[q4] = make_float4(-gm.x, -gm.y, -gm.z, -gm.w);
+        }
+      }
       if (wait_w(B_U, i & 1)) {
         tc_fence_after();
         float u[32];
@@ -285,17 +290,8 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
 #pragma unroll
         for (int q4 = 0; q4 < 8; ++q4) {
           const float* x = u + 4 * q4;
-          float4 f;
-          if (!BACK) {
-            const float4 dd = *reinterpret_cast<const float4*>(gd + 64 + 4 * q4);
-            const float4 be = *reinterpret_cast<const float4*>(gd + 128 + 4 * q4);
-            f = make_float4(be.x * dd.x, be.y * dd.y, be.z * dd.z, be.w * dd.w);
-          } else {
-            const float4 gm = *reinterpret_cast<const float4*>(gd + 4 * q4);
-            f = make_float4(-gm.x, -gm.y, -gm.z, -gm.w);
-          }
-          pd[2 * q4] = pack2(f.x * x[0], f.y * x[1]);
-          pd[2 * q4 + 1] = pack2(f.z * x[2], f.w * x[3]);
+          pd[2 * q4] = pack2(ra[q4].x * x[0], ra[q4].y * x[1]);
+          pd[2 * q4 + 1] = pack2(ra[q4].z * x[2], ra[q4].w * x[3]);
         }
         tmem_st16u(tmem + lo + TM_UD + 16 * half, pd);
         tmem_st_wait();
@@ -303,8 +299,10 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
       tc_fence_before();
       // a full barrier, not an arrival: the group then never runs a barrier instance ahead of the
       // issuer, even when an abort makes it skip its waits
-      named_bar(NB_U, NB_ALL);
+      named_bar(NB_U, NB_CSI);
       // ---- the updated matrix (not after the last chunk)
+      float gl = 0.0f;
+      if (i + 1 < nch && wait_full(i + 1)) gl = record(i + 1)[63];
       const bool s_ok = wait_w(B_S, i & 1);
       if (i + 1 < nch) {
         float v[64];
@@ -313,7 +311,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
           ld64(tmem + lo + TM_S + 64 * half, v);
           tmem_ld_wait();
         }
-        enter(i + 1, v, s_ok);
+        enter(v, gl, s_ok);
       } else if (BACK && P.S_out && s_ok) {  // the gradient of the initial state
         tc_fence_after();
         float v[64];
@@ -327,51 +325,45 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
     }
   } else if (warp < W_PROD) {
     // -------------------------------------------------------------- side group (warps 8-11) --
+    if (BACK) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     const int quad = warp & 3, t4 = tid - 32 * W_SIDE;
     const int j = 32 * quad + lane;
     const uint32_t lo = (uint32_t)(32 * quad) << 16;
-    // Backward: Q of step i becomes scale Gamma Q, in place (the B operand of the dO term).
-    auto scale_q = [&](int i) {
-      if (!wait_full(i)) return;
-      const float* gd = record(i);
-      uint4* qt = reinterpret_cast<uint4*>(smem + (i % L_::STAGES) * L_::STAGE + L_::Q) + t4;
+    // The bf16 copy of the matrix entering step i, from tensor memory to shared memory: the swizzled image
+    // that the MMAs of the parallel kernel read (row j, 16-byte piece c at c ^ j % 8).
+    // Two buffers in turn: a copy takes most of a chunk's time to leave.
+    auto stage_copy = [&](int i) {
+      named_bar(NB_COPY, NB_CS);
+      tc_fence_after();
+      unsigned char* row = smem + L_::COPY + (i & 1) * 32768 + j * 128;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {  // 16-byte pieces; piece / 8 is a row of one of the halves
-        uint4 w[4];
+      for (int hh = 0; hh < 2; ++hh) {
+        float t[32];
+        ld32(tmem + lo + TM_SB + 32 * hh, t);
+        tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = qt[(4 * b + e) * 128];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float f = P.scale * gd[(((4 * b + e) * 128 + t4) >> 3) & 63];
-          uint32_t* x = reinterpret_cast<uint32_t*>(&w[e]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            x[q] = pack2(f * __uint_as_float(x[q] << 16), f * __uint_as_float(x[q] & 0xffff0000u));
-          qt[(4 * b + e) * 128] = w[e];
-        }
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<float4*>(row + hh * 16384 + ((q ^ (j & 7)) << 4)) =
+              make_float4(t[4 * q], t[4 * q + 1], t[4 * q + 2], t[4 * q + 3]);
       }
-      fence_proxy_async_smem();
+      tc_fence_before();
     };
-    // One warp sends the copy of the matrix entering step i.
-    auto send = [&](int i) {
-      if (warp != W_SIDE) return;
-      named_bar(NB_COPY, NB_CC);
-      if (t4 == 0 && !*abort_flag) {
-        const size_t sh = (size_t)(slot0 + chunk_of(i)) * P.Hv + h;
-        bulk_store(P.ws + (BACK ? P.at.ds : P.at.s) + sh * 32768, smem + L_::COPY, 32768);
-        bulk_commit();
-      }
-      __syncwarp();
+    auto send_copy = [&](int i) {
+      const size_t sh = (size_t)(slot0 + chunk_of(i)) * P.Hv + h;
+      bulk_store(P.ws + (BACK ? P.at.ds : P.at.s) + sh * 32768, smem + L_::COPY + (i & 1) * 32768, 32768);
+      bulk_commit();
     };
-    named_bar_arrive(NB_S, NB_ALL);
-    if (BACK) {
-      scale_q(0);
-      named_bar_arrive(NB_G, NB_SI);
-    }
-    send(0);
+    named_bar_arrive(NB_S, NB_CSI);
+    stage_copy(0);
+    fence_proxy_async_smem();
+    named_bar(NB_SIDE, 128);
+    if (t4 == 0) send_copy(0);
+    __syncwarp();
     for (int i = 0; i < nch; ++i) {
-      if (t4 == 0) bulk_wait_read<0>();  // everything sent so far has left shared memory
-      named_bar(NB_U, NB_ALL);           // a full barrier (see the other group)
+      // all that was sent has left shared memory, except perhaps the copy entering this step
+      if (t4 == 0) bulk_wait_read<1>();
+      __syncwarp();
+      named_bar(NB_U, NB_CSI);  // a full barrier (see the other group)
       const int c = chunk_of(i);
       // E^T or dW^T: complete since the critical group has waited for it
       bool ok = wait_w(B_U, i & 1);
@@ -397,7 +389,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
         }
       }
       tc_fence_before();
-      if (i + 1 < nch) named_bar_arrive(NB_S, NB_ALL);  // U / dW read
+      if (i + 1 < nch) named_bar_arrive(NB_S, NB_CSI);  // U / dW read
       const int L = rows_of(c);
       if (ok && !BACK) {  // U^T, the same kind of image
         unsigned char* row = smem + L_::OUT + j * 128;
@@ -431,6 +423,8 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
           }
         }
       }
+      const bool more = i + 1 < nch;
+      if (more) stage_copy(i + 1);
       fence_proxy_async_smem();
       named_bar(NB_SIDE, 128);
       if (t4 == 0) {
@@ -446,26 +440,19 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
           tma_store_3d(&map_dv, smem + L_::OUT + 8192, 64, h, t0);
           bulk_commit();
         }
+        if (more && !*abort_flag) send_copy(i + 1);
       }
       __syncwarp();
-      if (i + 1 < nch) {
-        if (BACK) {
-          scale_q(i + 1);
-          named_bar_arrive(NB_G, NB_SI);
-        }
-        send(i + 1);
-      }
     }
     if (t4 == 0) bulk_wait<0>();  // nothing on its way out of shared memory
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (BACK) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == W_PROD) {
     // -------------------------------------------------------------- TMA producer -------------
     if (elect_one()) {
       prefetch_tensormap(&map_k);
       prefetch_tensormap(&map_x);
       prefetch_tensormap(&map_tp);
-      if (BACK) prefetch_tensormap(&map_q);
     }
     int issued = 0;
     for (int i = 0; i < nch; ++i) {
@@ -487,8 +474,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
         tma_load_3d(sp + L_::K, &map_k, fb, 0, hk, t0);
         tma_load_3d(sp + L_::K + 8192, &map_k, fb, 64, hk, t0);
         if (BACK) {
-          tma_load_3d(sp + L_::Q, &map_q, fb, 0, hk, t0);
-          tma_load_3d(sp + L_::Q + 8192, &map_q, fb, 64, hk, t0);
+          bulk_load(sp + L_::Q, P.ws + P.at.qg + sh * 16384, 16384, fb);
         }
         tma_load_3d(sp + L_::X, &map_x, fb, 0, h, t0);
         tma_load_3d(sp + L_::X + 8192, &map_x, fb, 64, h, t0);
@@ -528,82 +514,82 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
     const uint32_t id_u = idesc_bf16(128, 64, 0, BACK ? 1 : 0);  // T~^T forward, T~ backward
     const uint32_t id_s = idesc_bf16(128, 128, 0, 1);            // B = K, MN-major
     const uint32_t id_q = idesc_bf16(128, 128, 1, 1);            // A = dO^T, B = scale Gamma Q
-    for (int i = 0; i < nch; ++i) {
-      const int st = i % L_::STAGES;
-      const uint32_t sp = sbase + st * L_::STAGE;
-      const uint32_t tm_u = tmem + TM_U;
+    const uint64_t dK0 = sdesc_sw128(sbase + L_::K, 16, 1024);       // K as K-major B
+    const uint64_t dKn0 = sdesc_sw128(sbase + L_::K, 8192, 1024);    // K as MN-major B
+    const uint64_t dQn0 = sdesc_sw128(sbase + L_::Q, 8192, 1024);    // scale Gamma Q as MN-major B
+    const uint64_t dXt0 = sdesc_sw128(sbase + L_::X, 8192, 1024);    // V^T / dO^T as MN-major A
+    const uint64_t dT0 = BACK ? sdesc_sw128(sbase + L_::TP, 8192, 1024)   // T~ as MN-major B
+                              : sdesc_sw128(sbase + L_::TP, 16, 1024);    // T~ as K-major B
+    const uint64_t dP0 = sdesc_sw128(sbase + L_::TP + 8192, 8192, 1024);  // P as MN-major B
+    constexpr uint32_t t_step = BACK ? 2048 : 32;
+    auto step = [&](auto stage, int i) {
+      constexpr uint32_t o = decltype(stage)::value * L_::STAGE;
       // the chunk's tiles have landed and nothing failed so far; a failure later in the chunk leaves its
       // MMAs to run on whatever is there, in bounds all the same
       const bool go = wait_full(i) && __all_sync(0xffffffffu, !*abort_flag);
-      const uint64_t dK = sdesc_sw128(sp + L_::K, 16, 1024);       // K as K-major B
-      const uint64_t dKn = sdesc_sw128(sp + L_::K, 8192, 1024);    // K as MN-major B
-      const uint64_t dQn = sdesc_sw128(sp + L_::Q, 8192, 1024);
-      const uint64_t dXt = sdesc_sw128(sp + L_::X, 8192, 1024);    // V^T / dO^T as MN-major A
-      const uint64_t dT = BACK ? sdesc_sw128(sp + L_::TP, 8192, 1024)   // T~ as MN-major B
-                               : sdesc_sw128(sp + L_::TP, 16, 1024);    // T~ as K-major B
-      const uint64_t dP = sdesc_sw128(sp + L_::TP + 8192, 8192, 1024);  // P as MN-major B
-      constexpr uint32_t t_step = BACK ? 2048 : 32;
       if (BACK && go) {  // state-independent; D2 was read before the previous chunk's NB_U
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ss(tmem + TM_D2, dadd(dXt, ks * 2048), dadd(dP, ks * 2048), id_e, ks > 0);
+            mma_bf16_ss(tmem + TM_D2, dadd(dXt0, o + ks * 2048), dadd(dP0, o + ks * 2048), id_e,
+                        ks > 0);
         }
       }
       __syncwarp();
-      named_bar(NB_S, NB_ALL);  // bf16 copy in place, U / dW of the previous chunk read
+      named_bar(NB_S, NB_CSI);  // bf16 copy in place, U / dW of the previous chunk read
       if (go) {
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
             mma_bf16_ts(tmem + TM_D, tmem + TM_SB + 8 * ks,
-                        dadd(dK, (ks >> 2) * 8192 + (ks & 3) * 32), id_k, ks > 0);
+                        dadd(dK0, o + (ks >> 2) * 8192 + (ks & 3) * 32), id_k, ks > 0);
           mma_commit(&bars[B_K]);
           if (!BACK) {  // state-independent, while X' is formed
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_bf16_ss(tm_u, dadd(dXt, ks * 2048), dadd(dT, ks * 32), id_e, ks > 0);
+              mma_bf16_ss(tmem + TM_U, dadd(dXt0, o + ks * 2048), dadd(dT0, o + ks * 32), id_e,
+                          ks > 0);
           }
         }
       }
       __syncwarp();
-      named_bar(NB_X, NB_CI);  // X' written
+      named_bar(NB_X, NB_CI);  // X' written, matrix scaled
       if (go) {
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ts(tm_u, tmem + TM_X + 8 * ks, dadd(dT, ks * t_step), id_u, !BACK || ks > 0);
+            mma_bf16_ts(tmem + TM_U, tmem + TM_X + 8 * ks, dadd(dT0, o + ks * t_step), id_u,
+                        !BACK || ks > 0);
           mma_commit(&bars[B_U]);
-        }
-      }
-      __syncwarp();
-      if (BACK) {
-        named_bar(NB_G, NB_SI);  // dS scaled, scale Gamma Q written
-        if (go) {
-          tc_fence_after();
-          if (elect_one()) {
+          if (BACK) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_bf16_ss(tmem + TM_S, dadd(dXt, ks * 2048), dadd(dQn, ks * 2048), id_q, 1);
+              mma_bf16_ss(tmem + TM_S, dadd(dXt0, o + ks * 2048), dadd(dQn0, o + ks * 2048), id_q,
+                          1);
           }
         }
-        __syncwarp();
       }
-      named_bar(NB_U, NB_ALL);  // the update's operand written; matrix scaled
+      __syncwarp();
+      named_bar(NB_U, NB_CSI);  // the update's operand written
       if (go) {
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ts(tmem + TM_S, tmem + TM_UD + 8 * ks, dadd(dKn, ks * 2048), id_s, 1);
+            mma_bf16_ts(tmem + TM_S, tmem + TM_UD + 8 * ks, dadd(dKn0, o + ks * 2048), id_s, 1);
           mma_commit(&bars[B_S]);
-          mma_commit(&bars[B_EMPTY0 + st]);
+          mma_commit(&bars[B_EMPTY0 + decltype(stage)::value]);
         }
       }
       __syncwarp();
+    };
+    for (int i = 0; i < nch; i += L_::STAGES) {
+      step(std::integral_constant<int, 0>(), i);
+      if (i + 1 < nch) step(std::integral_constant<int, 1>(), i + 1);
+      if (L_::STAGES > 2 && i + 2 < nch) step(std::integral_constant<int, L_::STAGES - 1>(), i + 2);
     }
     // every MMA has completed before tensor memory is read back or released
     if (elect_one()) {
@@ -640,12 +626,11 @@ cudaError_t launch_t(const Args& a, cudaStream_t s) {
   p.status = a.status;
   p.T = a.T;
   p.at = tc_layout(slots, a.Hv);
-  p.scale = a.scale;
   p.N = a.N;
   p.Hk = a.Hk;
   p.Hv = a.Hv;
-  CUtensorMap mk, mq, mx, mt, mv;
-  if (!make_tok_map(&mk, a.k, a.Hk, n_tok, a.ts.k) || !make_tok_map(&mq, a.q, a.Hk, n_tok, a.ts.q) ||
+  CUtensorMap mk, mx, mt, mv;
+  if (!make_tok_map(&mk, a.k, a.Hk, n_tok, a.ts.k) ||
       !make_tok_map(&mx, BACK ? a.dout : a.v, a.Hv, n_tok,
                     BACK ? (int64_t)a.Hv * tm::D : a.ts.v) ||
       !make_rows64_map(&mt, ws + p.at.tp, slots * a.Hv * 128, BACK ? 128 : 64) ||
@@ -655,7 +640,7 @@ cudaError_t launch_t(const Args& a, cudaStream_t s) {
       cudaFuncSetAttribute(bwd_chain_kernel<BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Sm<BACK>::BYTES);
   if (e != cudaSuccess) return e;
-  bwd_chain_kernel<BACK><<<(unsigned)units, THREADS, Sm<BACK>::BYTES, s>>>(mk, mq, mx, mt, mv, p);
+  bwd_chain_kernel<BACK><<<(unsigned)units, THREADS, Sm<BACK>::BYTES, s>>>(mk, mx, mt, mv, p);
   return cudaGetLastError();
 }
 

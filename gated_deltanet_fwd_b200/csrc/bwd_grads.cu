@@ -583,7 +583,10 @@ size_t tc_workspace_bytes(int N, int64_t n_tok, int Hv) {
 
 cudaError_t launch_tc(const Args& a, cudaStream_t s) {
   ChunkFusion f;
-  f.bwd_gd_off = tc_layout(max_slots(a.N, (int64_t)a.B * a.T, tm::C), a.Hv).gd;
+  const TcLayout at = tc_layout(max_slots(a.N, (int64_t)a.B * a.T, tm::C), a.Hv);
+  f.bwd_gd_off = at.gd;
+  f.bwd_qg_off = at.qg;
+  f.scale = a.scale;
   cudaError_t e = launch_chunk_prep(a.q, a.k, a.ts, a.g, a.beta, a.cu, a.N, a.B, a.T, a.Hk, a.Hv,
                                     a.ws, a.status, s, f);
   if (e == cudaSuccess) e = launch_bwd_chain(a, false, s);

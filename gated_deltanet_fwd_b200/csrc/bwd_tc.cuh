@@ -14,12 +14,13 @@
 //
 // Workspace from its 256-byte-aligned base (n = slots * Hv, a slot being a chunk's ordinal):
 //   [0, 1024)        status word, padding
-//   TP [n][128][64]  bf16: rows 0..63 T~, rows 64..127 P
+//   TP [n][128][64]  bf16: rows 0..63 T~, rows 64..127 scale P
 //   GD [n][4][64]    fp32: Gamma, d, beta (floored), gamma log2 e
 //   S  [n][2][128][64]  bf16: two 64-column halves of the state (rows: value index)
 //   DS [n][2][128][64]  bf16: the gradient of the state leaving the chunk
 //   U  [n][128][64]  bf16: U^T (rows: value index, columns: tokens of the chunk)
-// S, DS and U are kept as the 128-byte-swizzled images that the MMAs read (ptx::sw128), written and read by
+//   QG [n][2][64][64]   bf16: two 64-column halves of scale Gamma Q
+// S, DS, U and QG are kept as the 128-byte-swizzled images that the MMAs read (ptx::sw128), written and read by
 // plain bulk copies.
 #pragma once
 
@@ -30,7 +31,7 @@ namespace gdn {
 namespace bwd {
 
 struct TcLayout {
-  size_t tp, gd, s, ds, u, end;
+  size_t tp, gd, s, ds, u, qg, end;
 };
 
 __host__ __device__ inline TcLayout tc_layout(int64_t slots, int Hv) {
@@ -41,7 +42,8 @@ __host__ __device__ inline TcLayout tc_layout(int64_t slots, int Hv) {
   l.s = l.gd + n * GD_BYTES;
   l.ds = l.s + n * 32768;
   l.u = l.ds + n * 32768;
-  l.end = l.u + n * 16384;
+  l.qg = l.u + n * 16384;
+  l.end = l.qg + n * 16384;
   return l;
 }
 

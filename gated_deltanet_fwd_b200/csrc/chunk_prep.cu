@@ -25,7 +25,9 @@
 // For the backward pass (BWD; bwd_tc.cuh) the same inverse is written as T' = diag(beta) T~ with
 // T~ = (I + A~)^{-1}, A~[r,s] = e^{gamma_r - gamma_s} beta_s k_r.k_s: T~ has an exact unit diagonal, so
 // its bf16 copy loses only what the small off-diagonal entries lose, and beta is applied in fp32 by
-// whoever uses it.  The record then holds Gamma, d, beta and gamma log2 e.
+// whoever uses it.  The record then holds Gamma, d, beta and gamma log2 e, P carries the
+// output scale, and scale Gamma Q goes out next to it (operands of the backward chain, where scaling Q
+// cost 1400 cycles of a chunk).
 #include "bwd_internal.cuh"
 #include "chunk_tm.cuh"
 #include "gdn_internal.cuh"
@@ -84,6 +86,9 @@ struct PrepParams {
   const __nv_bfloat16* b;
   const float* A_log;
   const float* dt_bias;
+  // backward: byte offset of the scale Gamma Q tiles
+  int64_t qg_off;
+  float scale;
 };
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -362,6 +367,26 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
     tc_fence_before();
     if (!__syncthreads_and(ok)) break;
     tc_fence_after();
+    // scale Gamma Q of the pair as the swizzled image of two 64-column halves.  From global memory (L2):
+    // the shared-memory copy is about to be replaced.
+    if (BWD) {
+      for (int e = tid; e < npair * 1024; e += PP_THREADS) {
+        const int gi = e >> 10, r = (e >> 4) & 63, ch = e & 15;
+        const int h = hk * G + h0 + gi;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (r < L) {
+          w = *reinterpret_cast<const uint4*>(P.q + (t0 + r) * P.q_stride + hk * tm::D + ch * 8);
+          const float f = P.scale * ex2f(gl2_all[gi * 128 + r]);
+          uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            x[q] = pack_bf16x2(f * __uint_as_float(x[q] << 16),
+                               f * __uint_as_float(x[q] & 0xffff0000u));
+        }
+        *reinterpret_cast<uint4*>(P.ws + P.qg_off + ((size_t)slot * P.Hv + h) * 16384 +
+                                  (ch >> 3) * 8192 + sw128(r, (ch & 7) * 8)) = w;
+      }
+    }
     // the MMA has read [K; Q]: the next item's K and Q may land there while this one is worked on
     if (h0 == 0 && nst > 0) issue_loads(nxt);
     PP_TS(2);
@@ -388,7 +413,7 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
             for (int q = 16 * b16; q < 16 * b16 + 16; ++q) {
               const int s = cb + q;
               const bool keep = R < 64 ? (s < r) : (s <= r);
-              const float bs = BWD ? (R < 64 ? gl2[64 + s] : 1.0f) : br;
+              const float bs = BWD ? (R < 64 ? gl2[64 + s] : P.scale) : br;
               v[q] = keep ? bs * ex2f(gr - gl2[s]) * d[q] : 0.0f;
             }
           } else {  // the 16 columns lie above the diagonal
@@ -528,6 +553,8 @@ cudaError_t launch_chunk_prep(const void* q, const void* k, TokStrides ts, const
   p.b = fuse.b;
   p.A_log = fuse.A_log;
   p.dt_bias = fuse.dt_bias;
+  p.qg_off = (int64_t)fuse.bwd_qg_off;
+  p.scale = fuse.scale;
   return fuse.bwd_gd_off ? launch_prep_t<true>(p, slots, s) : launch_prep_t<false>(p, slots, s);
 }
 

@@ -224,7 +224,9 @@ struct ChunkFusion {
   const __nv_bfloat16* b = nullptr;
   const float* A_log = nullptr;
   const float* dt_bias = nullptr;
-  size_t bwd_gd_off = 0;  // set: the backward pass's operands, its records at this byte offset
+  // set: the backward pass's operands, its records and its scale Gamma Q tiles at these byte offsets
+  size_t bwd_gd_off = 0, bwd_qg_off = 0;
+  float scale = 0.0f;
 };
 
 // TMA tensor maps (tma_maps.cu), 128-byte swizzle, bf16:
