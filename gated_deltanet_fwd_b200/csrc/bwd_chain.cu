@@ -46,6 +46,7 @@ using namespace ptx;
 // two (2 x 144 + 120 + 104 = 4 x 128): spills cost twice here, since shared memory leaves almost no L1
 // (a backward chunk took 3.2 us with 140 spilled bytes against 2.6 us without).
 constexpr int THREADS = 512;
+constexpr int MAX_SORTED = 256;  // sequences that are put in order of length
 constexpr int W_SIDE = 8, W_PROD = 12, W_MMA = 13;
 
 // shared memory, from a 1024-aligned base; a stage holds one chunk's tiles: K, [Q,] V or dO, T~ [and P],
@@ -75,11 +76,12 @@ constexpr uint32_t TM_S = 0, TM_D = 128, TM_D2 = 192, TM_U = 256, TM_SB = 320, T
                    TM_UD = 416;
 
 struct ChainParams {
-  const float* S_in;   // initial state, or gradient of the final one; null: zero
-  float* S_out;        // gradient of the initial state (backward only); null: not wanted
+  const float* S0;     // initial state; null: zero
+  const float* dS_T;   // gradient of the final one; null: zero
+  float* dS0;          // gradient of the initial state; null: not wanted
   const int32_t* cu;
   unsigned char* ws;
-  __nv_bfloat16* dv;   // backward only
+  __nv_bfloat16* dv;
   int* status;
   int64_t T;
   TcLayout at;
@@ -103,21 +105,19 @@ __device__ __forceinline__ void ld64(uint32_t taddr, float* v) {
   ld32(taddr + 32, v + 32);
 }
 
+// One walk: sequence n, v-head h.  map_x: V forward, dO backward; map_tp: boxes of T~, backward of [T~; P].
 template <bool BACK>
-__global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
-    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_tp,
-    const __grid_constant__ CUtensorMap map_dv, const ChainParams P) {
+__device__ __forceinline__ void chain(const CUtensorMap* map_k, const CUtensorMap* map_x,
+                                      const CUtensorMap* map_tp, const CUtensorMap* map_dv,
+                                      const ChainParams& P, unsigned char* smem, int n, int h) {
   using L_ = Sm<BACK>;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const float* S_in = BACK ? P.dS_T : P.S0;
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L_::BAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L_::BAR + B_N * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::BAR + B_N * 8 + 4);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.x % P.Hv, n = blockIdx.x / P.Hv;
   const int hk = h / (P.Hv / P.Hk);
   int64_t s_beg, s_end, slot0;
   if (!seq_range(P.cu, P.T, n, tm::C, s_beg, s_end, slot0)) {
@@ -127,9 +127,9 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
   const size_t sidx = ((size_t)n * P.Hv + h) * tm::STATE_FLOATS;
   const int nch = (int)((s_end - s_beg + tm::C - 1) / tm::C);
   if (nch == 0) {  // empty sequence: the gradient passes through
-    if (BACK && P.S_out)
+    if (BACK && P.dS0)
       for (int e = tid; e < tm::D * tm::D; e += THREADS)
-        P.S_out[sidx + e] = P.S_in ? P.S_in[sidx + e] : 0.0f;
+        P.dS0[sidx + e] = S_in ? S_in[sidx + e] : 0.0f;
     return;
   }
   // step i works on chunk chunk_of(i)
@@ -159,16 +159,17 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
     report(P.status, code);
     *abort_flag = 1;
   };
-  // A bounded wait that gives up early once the CTA is aborting.  The flag is looked at only while the
-  // phase is incomplete: shared-memory reads queue behind the epilogues' traffic.
+  // A bounded wait that gives up early once the CTA is aborting.  The flag and the timer are looked at
+  // only in long waits: both take longer than the waits of a chunk.
   auto wait = [&](int b, uint32_t parity) -> bool {
-    if (mbar_try_wait(&bars[b], parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t k = 0; k < kSpinLimit; ++k) {
+    uint64_t t0 = 0;
+    for (uint32_t k = 1; k < kSpinLimit; ++k) {
       if (mbar_try_wait(&bars[b], parity)) return true;
-      if ((k & 63) == 63) {
+      if ((k & 255) == 0) {
         if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) break;
       }
     }
     fail(GDN_ERR_TIMEOUT);
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
       }
     };
     {
-      const float* src = P.S_in ? P.S_in + sidx + (size_t)j * tm::D + 64 * half : nullptr;
+      const float* src = S_in ? S_in + sidx + (size_t)j * tm::D + 64 * half : nullptr;
       float v[64];
 #pragma unroll
       for (int q4 = 0; q4 < 16; ++q4) {
@@ -312,12 +313,12 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
           tmem_ld_wait();
         }
         enter(v, gl, s_ok);
-      } else if (BACK && P.S_out && s_ok) {  // the gradient of the initial state
+      } else if (BACK && P.dS0 && s_ok) {  // the gradient of the initial state
         tc_fence_after();
         float v[64];
         ld64(tmem + lo + TM_S + 64 * half, v);
         tmem_ld_wait();
-        float4* dst = reinterpret_cast<float4*>(P.S_out + sidx + (size_t)j * tm::D + 64 * half);
+        float4* dst = reinterpret_cast<float4*>(P.dS0 + sidx + (size_t)j * tm::D + 64 * half);
 #pragma unroll
         for (int q4 = 0; q4 < 16; ++q4)
           dst[q4] = make_float4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
@@ -436,8 +437,8 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
         }
         if (ok && BACK && L == tm::C) {
           const int32_t t0 = (int32_t)(s_beg + (int64_t)tm::C * c);
-          tma_store_3d(&map_dv, smem + L_::OUT, 0, h, t0);
-          tma_store_3d(&map_dv, smem + L_::OUT + 8192, 64, h, t0);
+          tma_store_3d(map_dv, smem + L_::OUT, 0, h, t0);
+          tma_store_3d(map_dv, smem + L_::OUT + 8192, 64, h, t0);
           bulk_commit();
         }
         if (more && !*abort_flag) send_copy(i + 1);
@@ -450,9 +451,9 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
     if (warp == W_PROD) {
     // -------------------------------------------------------------- TMA producer -------------
     if (elect_one()) {
-      prefetch_tensormap(&map_k);
-      prefetch_tensormap(&map_x);
-      prefetch_tensormap(&map_tp);
+      prefetch_tensormap(map_k);
+      prefetch_tensormap(map_x);
+      prefetch_tensormap(map_tp);
     }
     int issued = 0;
     for (int i = 0; i < nch; ++i) {
@@ -471,14 +472,14 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
         const int32_t t0 = (int32_t)(s_beg + (int64_t)tm::C * c);
         const size_t sh = (size_t)(slot0 + c) * P.Hv + h;
         mbar_arrive_expect_tx(fb, L_::TX);
-        tma_load_3d(sp + L_::K, &map_k, fb, 0, hk, t0);
-        tma_load_3d(sp + L_::K + 8192, &map_k, fb, 64, hk, t0);
+        tma_load_3d(sp + L_::K, map_k, fb, 0, hk, t0);
+        tma_load_3d(sp + L_::K + 8192, map_k, fb, 64, hk, t0);
         if (BACK) {
           bulk_load(sp + L_::Q, P.ws + P.at.qg + sh * 16384, 16384, fb);
         }
-        tma_load_3d(sp + L_::X, &map_x, fb, 0, h, t0);
-        tma_load_3d(sp + L_::X + 8192, &map_x, fb, 64, h, t0);
-        tma_load_2d(sp + L_::TP, &map_tp, fb, 0, (int32_t)(sh * 128));
+        tma_load_3d(sp + L_::X, map_x, fb, 0, h, t0);
+        tma_load_3d(sp + L_::X + 8192, map_x, fb, 64, h, t0);
+        tma_load_2d(sp + L_::TP, map_tp, fb, 0, (int32_t)(sh * 128));
         bulk_load(sp + L_::GD, P.ws + P.at.gd + sh * GD_BYTES, GD_BYTES, fb);
       }
       if (part) {  // once per sequence: its last chunk
@@ -609,17 +610,55 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
   }
 }
 
-template <bool BACK>
-cudaError_t launch_t(const Args& a, cudaStream_t s) {
-  const int64_t n_tok = (int64_t)a.B * a.T, units = (int64_t)a.N * a.Hv;
+// The two walks of a (sequence, v-head) do not depend on one another, so all of both are units of one
+// launch, the longest sequences first: with 32 heads and sequences of 16384, 8192, 6144 and 2048 tokens the
+// walks one after the other took 475 + 535 us, half of it with most SMs idle, together 585 us.
+__global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
+    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+    const __grid_constant__ CUtensorMap map_do, const __grid_constant__ CUtensorMap map_t,
+    const __grid_constant__ CUtensorMap map_tp, const __grid_constant__ CUtensorMap map_dv,
+    const ChainParams P) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int h = blockIdx.x % P.Hv;
+  const bool back = (blockIdx.x / P.Hv) % 2 == 0;  // first: its chunks take longer
+  int n = blockIdx.x / (2 * P.Hv);
+  // the n-th longest sequence; many sequences balance without
+  if (P.cu && P.N > 1 && P.N <= MAX_SORTED) {
+    __shared__ int pick;
+    const int i = threadIdx.x;
+    if (i < P.N) {
+      const int len = P.cu[i + 1] - P.cu[i];
+      int rank = 0;
+      for (int m = 0; m < P.N; ++m) {
+        const int o = P.cu[m + 1] - P.cu[m];
+        rank += o > len || (o == len && m < i);
+      }
+      if (rank == n) pick = i;  // ranks are a permutation whatever cu_seqlens holds
+    }
+    __syncthreads();
+    n = pick;
+  }
+  if (back)
+    chain<true>(&map_k, &map_do, &map_tp, &map_dv, P, smem, n, h);
+  else
+    chain<false>(&map_k, &map_v, &map_t, &map_dv, P, smem, n, h);
+}
+
+}  // namespace
+
+cudaError_t launch_bwd_chain(const Args& a, cudaStream_t s) {
+  const int64_t n_tok = (int64_t)a.B * a.T, units = 2 * (int64_t)a.N * a.Hv;
   const int64_t slots = max_slots(a.N, n_tok, tm::C);
-  // TMA coordinates are 32-bit: rows of 64 columns of the state tiles are the largest
-  if (units > 0x7fffffff || n_tok > 0x7fffffff || slots * a.Hv > 0x7fffffff / 256)
+  // TMA coordinates are 32-bit
+  if (units > 0x7fffffff || n_tok > 0x7fffffff || slots * a.Hv > 0x7fffffff / 128)
     return cudaErrorInvalidConfiguration;
   ChainParams p;
   unsigned char* ws = reinterpret_cast<unsigned char*>(a.ws);
-  p.S_in = BACK ? a.dST : a.S0;
-  p.S_out = BACK ? a.dS0 : nullptr;
+  p.S0 = a.S0;
+  p.dS_T = a.dST;
+  p.dS0 = a.dS0;
   p.cu = a.cu;
   p.ws = ws;
   p.dv = reinterpret_cast<__nv_bfloat16*>(a.dv_);
@@ -629,25 +668,18 @@ cudaError_t launch_t(const Args& a, cudaStream_t s) {
   p.N = a.N;
   p.Hk = a.Hk;
   p.Hv = a.Hv;
-  CUtensorMap mk, mx, mt, mv;
-  if (!make_tok_map(&mk, a.k, a.Hk, n_tok, a.ts.k) ||
-      !make_tok_map(&mx, BACK ? a.dout : a.v, a.Hv, n_tok,
-                    BACK ? (int64_t)a.Hv * tm::D : a.ts.v) ||
-      !make_rows64_map(&mt, ws + p.at.tp, slots * a.Hv * 128, BACK ? 128 : 64) ||
-      !make_tok_map(&mv, a.dv_, a.Hv, n_tok, (int64_t)a.Hv * tm::D))
+  CUtensorMap mk, mv, mo, mt, mtp, mdv;
+  const int64_t hv = (int64_t)a.Hv * tm::D, rows = slots * a.Hv * 128;
+  if (!make_tok_map(&mk, a.k, a.Hk, n_tok, a.ts.k) || !make_tok_map(&mv, a.v, a.Hv, n_tok, a.ts.v) ||
+      !make_tok_map(&mo, a.dout, a.Hv, n_tok, hv) || !make_tok_map(&mdv, a.dv_, a.Hv, n_tok, hv) ||
+      !make_rows64_map(&mt, ws + p.at.tp, rows, 64) || !make_rows64_map(&mtp, ws + p.at.tp, rows, 128))
     return cudaErrorInvalidValue;
-  const cudaError_t e =
-      cudaFuncSetAttribute(bwd_chain_kernel<BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Sm<BACK>::BYTES);
+  constexpr uint32_t bytes = Sm<true>::BYTES > Sm<false>::BYTES ? Sm<true>::BYTES : Sm<false>::BYTES;
+  const cudaError_t e = cudaFuncSetAttribute(
+      bwd_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  bwd_chain_kernel<BACK><<<(unsigned)units, THREADS, Sm<BACK>::BYTES, s>>>(mk, mx, mt, mv, p);
+  bwd_chain_kernel<<<(unsigned)units, THREADS, bytes, s>>>(mk, mv, mo, mt, mtp, mdv, p);
   return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_bwd_chain(const Args& a, bool back, cudaStream_t s) {
-  return back ? launch_t<true>(a, s) : launch_t<false>(a, s);
 }
 
 }  // namespace bwd

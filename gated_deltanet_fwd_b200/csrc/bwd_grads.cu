@@ -589,8 +589,7 @@ cudaError_t launch_tc(const Args& a, cudaStream_t s) {
   f.scale = a.scale;
   cudaError_t e = launch_chunk_prep(a.q, a.k, a.ts, a.g, a.beta, a.cu, a.N, a.B, a.T, a.Hk, a.Hv,
                                     a.ws, a.status, s, f);
-  if (e == cudaSuccess) e = launch_bwd_chain(a, false, s);
-  if (e == cudaSuccess) e = launch_bwd_chain(a, true, s);
+  if (e == cudaSuccess) e = launch_bwd_chain(a, s);
   if (e == cudaSuccess) e = launch_bwd_grads(a, s);
   return e;
 }

@@ -1,10 +1,10 @@
 // bwd_tc.cuh -- layout of the tensor-core backward pass of the chunked rule (bf16, dk = dv = 128,
 // chunks of 64 tokens); the mathematics is in bwd_simt.cu.
 //
-// Four kernels, one after the other on the caller's stream:
-//   chunk_prep<BWD>   (chunk_prep.cu)  per (chunk, k-head): T~, P and the decay records
-//   bwd_chain<false>  (bwd_chain.cu)   per (sequence, v-head), forward: states S entering each chunk, and U
-//   bwd_chain<true>   (bwd_chain.cu)   per (sequence, v-head), backward: dS leaving each chunk, and dv
+// Three kernels, one after the other on the caller's stream:
+//   chunk_prep<BWD>   (chunk_prep.cu)  per (chunk, k-head): T~, P, scale Gamma Q and the decay records
+//   bwd_chain         (bwd_chain.cu)   per (sequence, v-head): a walk forward, which leaves the state S entering
+//                                      each chunk and U, and a walk backward: dS leaving each chunk, and dv
 //   bwd_grads         (bwd_grads.cu)   per (chunk, k-head): dq, dk, dg, dbeta
 // Only the two chains are serial; they carry the fp32 state (or its gradient) in tensor memory and leave
 // bf16 copies, the same roundings their own next product uses, so that everything else is parallel.
@@ -47,7 +47,7 @@ __host__ __device__ inline TcLayout tc_layout(int64_t slots, int Hv) {
   return l;
 }
 
-cudaError_t launch_bwd_chain(const Args& a, bool back, cudaStream_t s);
+cudaError_t launch_bwd_chain(const Args& a, cudaStream_t s);
 cudaError_t launch_bwd_grads(const Args& a, cudaStream_t s);
 
 }  // namespace bwd
