@@ -10,15 +10,19 @@
 //          D3 = dS^T U^T                M 128, N 64,  K 128        (raw dKw)
 //   MMA_n  D4 = K^T [dN; dM]^T          M 128, N 128, K 64
 //          D5 = Q^T dN + K^T dM         M 128, N 64,  K 64 twice
-// Epilogue A (token rows): decay masks on D2 -> [dN; dM] in shared memory as bf16; the diagonals are a
-// token's own pair p and dbeta; <S, dS> from shared memory.  Epilogue B (channel rows): Gamma and d applied
-// in fp32, dq and dk summed over the heads, dgamma = q.dq + k.(dKe - dKw) reduced over channels.
+// Epilogue A (token rows): decay masks on D2 -> [dN; dM] in shared memory as bf16 (with the diagonal of dN,
+// a token's own pair: its two contributions to dgamma are sums of the same rounded products and cancel
+// to fp32 rounding), and dbeta from the diagonal of dW U^T; <S, dS> from shared memory, by mma.sync on
+// 16-row diagonal blocks (32 warp instructions a warp; element by element it was 210).  Epilogue B
+// (channel rows): Gamma and d applied in fp32, dq and dk summed over the heads, dgamma = q.dq +
+// k.(dKe - dKw) reduced over channels; two tokens per instruction (fp32x2).
 // MMA_s does not wait for epilogue A, and a head's tiles are refilled as soon as MMA_s is done with them,
 // while MMA_n and epilogue B of that head still run.
 //
-// Warp roles (320 threads): warps 0-7 the epilogues (lane quarter warp % 4; columns, in epilogue B tokens,
+// Warp roles (384 threads): warps 0-7 the epilogues (lane quarter warp % 4; columns, in epilogue B tokens,
 // split in two by warp / 4), warp 8 the TMA producer, warp 9 the MMA issuer.  Bounds: 144 KB of tiles per
-// (chunk, v-head) at two v-heads a k-head against about 6 units of 64 x 128 x 128 products: HBM.
+// (chunk, v-head) at two v-heads a k-head against about 6 units of 64 x 128 x 128 products: HBM, with the
+// epilogues' instructions close behind (a step took 9400 cycles when they were written plainly).
 // Bounded waits and the abort protocol as in bwd_chain.cu.
 #include "bwd_tc.cuh"
 #include "ptx.cuh"
@@ -29,8 +33,10 @@ namespace {
 
 using namespace ptx;
 
-constexpr int THREADS = 320;
-constexpr int W_PROD = 8;  // warp 9 issues the MMAs
+// Three warpgroups: epilogues (two), and producer + issuer (two warps idle).  168 registers a thread at
+// launch; 2 x 184 + 136 = 3 x 168 (the issuer keeps its loop-invariant descriptors in registers).
+constexpr int THREADS = 384;
+constexpr int W_PROD = 8, W_MMA = 9;
 
 // shared memory, from a 1024-aligned base
 constexpr uint32_t SM_KQ = 0;               // [K; Q]: two 64-column halves x 128 rows x 128 B
@@ -40,15 +46,17 @@ constexpr uint32_t SM_S = SM_U + 16384;     // S: two halves x 128 rows x 128 B
 constexpr uint32_t SM_DS = SM_S + 32768;    // dS: the same
 constexpr uint32_t SM_NM = SM_DS + 32768;   // [dN; dM]: 128 rows x 128 B
 constexpr uint32_t SM_GD = SM_NM + 16384;   // two records
-constexpr uint32_t SM_RED = SM_GD + 2 * GD_BYTES;  // 2 x (dgamma parts [4][64], p [64], sums [8] + [8])
-constexpr uint32_t RED_FLOATS = 4 * 64 + 64 + 16;
+constexpr uint32_t SM_OUT = SM_GD + 2 * GD_BYTES;  // dq, dk on their way out: each two halves x 64 x 128 B
+constexpr uint32_t SM_RED = SM_OUT + 32768;        // 2 x (dgamma parts [4][64], sums [8] + [8])
+constexpr uint32_t RED_FLOATS = 4 * 64 + 16;
 constexpr uint32_t SM_BAR = SM_RED + 2 * RED_FLOATS * 4;
+static_assert(SM_OUT % 1024 == 0, "swizzled tiles");
 constexpr uint32_t SM_BYTES = SM_BAR + 128 + 1024;
 static_assert(SM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TX_KQ = 32768, TX_HEAD = 32768 + 16384 + 65536 + GD_BYTES;
 
 enum { B_KQ = 0, B_KQE = 1, B_H = 2, B_HE = 3, B_P = 4, B_N = 5, B_FIX = 6, B_DRAIN = 7, B_COUNT = 8 };
-enum { NB_NM = 1, NB_D = 2, NB_E = 3 };
+enum { NB_NM = 1, NB_D = 2, NB_E = 3, NB_O = 4 };
 constexpr int NB_ALL = 288;  // epilogue warps + issuer
 constexpr int NB_EPI = 256;
 
@@ -57,6 +65,7 @@ constexpr uint32_t TM_D2 = 0, TM_D1 = 64, TM_D4 = 192, TM_D3 = 320, TM_D5 = 384;
 
 struct GradParams {
   const float* beta;
+  const float* S0;  // only whether there is one
   const int32_t* cu;
   const unsigned char* ws;
   __nv_bfloat16 *dq, *dk, *dv, *dg, *dbeta;
@@ -89,23 +98,77 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ float bf_at(const unsigned char* p) {
-  return __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(p) << 16);
+// two fp32 values in a 64-bit register, and the arithmetic on them
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 two(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
-// sum of the products of eight bf16 pairs
-__device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc) {
-  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+__device__ __forceinline__ float2 parts(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// a pair of bf16 as fp32x2
+__device__ __forceinline__ f32x2 widen(uint32_t w) {
+  return two(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+// c (16 x 8) += a (16 x 16) b (16 x 8), bf16
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// This lane's part of the sum of X o Y over rows 16 w .. 16 w + 15 of two swizzled [2][128][64] images:
+// the diagonal of X Y^T on that block.
+__device__ __forceinline__ float dot_rows16(uint32_t x, uint32_t y, int w, int lane) {
+  float c0[4] = {}, c1[4] = {};
+  // ldmatrix: lanes 0-7 rows 0-7 of columns 0-7, lanes 8-15 rows 8-15, lanes 16-31 columns 8-15 -- as
+  // A (a0..a3); read the same way, registers 0, 2 are B of columns 0-7 and 1, 3 of columns 8-15
+  const int row = 16 * w + (lane & 15);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    acc = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), acc);
-    acc = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), acc);
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t off = (uint32_t)(k >> 2) * 16384 + sw128(row, 16 * (k & 3) + 8 * (lane >> 4));
+    uint32_t a[4], b[4];
+    ldmatrix4(a, x + off);
+    ldmatrix4(b, y + off);
+    mma_16816(c0, a, b[0], b[2]);
+    mma_16816(c1, a, b[1], b[3]);
   }
-  return acc;
+  // c0: (g, 2t), (g, 2t + 1) of the block's first 8 columns; c1[2..3]: rows g + 8 of its last 8
+  const int g = lane >> 2, t = 2 * (lane & 3);
+  return (g == t ? c0[0] + c1[2] : 0.0f) + (g == t + 1 ? c0[1] + c1[3] : 0.0f);
 }
 
 __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_q,
     const __grid_constant__ CUtensorMap map_do, const __grid_constant__ CUtensorMap map_dv,
+    const __grid_constant__ CUtensorMap map_dq, const __grid_constant__ CUtensorMap map_dk,
     const GradParams P) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -118,10 +181,11 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
   const int G = P.Hv / P.Hk;
 
   // item -> chunk and k-head; false past the last one or for a malformed cu_seqlens
+  ChunkCursor cursor;
   auto locate = [&](int64_t it, Chunk& ch, int64_t& slot, int& hk) {
     slot = it / P.Hk;
     hk = (int)(it - slot * P.Hk);
-    return it < P.items && find_chunk(P.cu, P.T, P.N, tm::C, slot, ch, P.status);
+    return it < P.items && cursor.find(P.cu, P.T, P.N, tm::C, slot, ch, P.status);
   };
   {
     Chunk ch;
@@ -130,7 +194,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
     if (!locate(blockIdx.x, ch, slot, hk)) return;  // nothing allocated yet
   }
   if (tid == 0) {
-    for (int i = 0; i < B_COUNT; ++i) mbar_init(&bars[i], i == B_KQE ? 8 : i == B_HE ? 9 : 1);
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(&bars[i], i == B_KQE || i == B_HE ? 9 : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -148,8 +212,16 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
     *abort_flag = 1;
   };
   auto wait = [&](int b, uint32_t parity) -> bool {
-    if (*abort_flag) return false;
-    if (mbar_wait(&bars[b], parity)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t k = 1; k < kSpinLimit; ++k) {
+      if (mbar_try_wait(&bars[b], parity)) return true;
+      if ((k & 255) == 0) {  // long waits only: the flag and the timer are slow to read
+        if (*abort_flag) return false;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) break;
+      }
+    }
     fail(GDN_ERR_TIMEOUT);
     return false;
   };
@@ -159,6 +231,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
   int x = 0, y = 0;
   if (warp < 8) {
     // ------------------------------------------------------------------ epilogues ------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int quad = warp & 3, half = warp >> 2;
     const int row = 32 * quad + lane;  // epilogue A: row of [dO; dW]; epilogue B: channel
     const uint32_t lo = (uint32_t)(32 * quad) << 16;
@@ -168,77 +241,100 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
       int hk;
       if (!locate(it, ch, slot, hk)) break;
       const int L = ch.L;
-      float aq[32], ak[32];  // dq, dk of channel `row`, tokens 32 half ..; summed over the heads
+      // tokens 32 half + 2 q, + 1 of channel `row`: dq, dk summed over the heads, and q, k
+      f32x2 aq[16], ak[16];
+      uint32_t qv[16], kv[16];
 #pragma unroll
-      for (int q = 0; q < 32; ++q) aq[q] = ak[q] = 0.0f;
+      for (int q = 0; q < 16; ++q) {
+        aq[q] = ak[q] = 0ull;
+        qv[q] = kv[q] = 0u;
+      }
       for (int gi = 0; gi < G; ++gi, ++x) {
         const int h = hk * G + gi;
         float* red = reinterpret_cast<float*>(smem + SM_RED) + (x & 1) * RED_FLOATS;
-        float* own = red + 256;
-        float* sums = own + 64;  // [8] <S, dS>, [8] k.dKw of the state part
+        float* sums = red + 256;  // [8] <S, dS>, [8] k.dKw of the state part
         const float* gd = reinterpret_cast<const float*>(smem + SM_GD + (x & 1) * GD_BYTES);
         const bool in = wait_w(B_H, x & 1);
         // ---- epilogue A
+        const int r = row & 63;
+        float diag = 0.0f;
         if (wait_w(B_P, x & 1) && in) {
           tc_fence_after();
           float d[32];
           tmem_ld32(tmem + lo + TM_D2 + 32 * half, d);
-          const int r = row & 63;
           const float gr = gd[192 + r], mul = row < 64 ? P.scale : -1.0f;
-          float diag = 0.0f;
           uint32_t pk[16];
+          if (half > (quad & 1)) {  // above the diagonal
 #pragma unroll
-          for (int q4 = 0; q4 < 8; ++q4) {
-            const float4 gs = *reinterpret_cast<const float4*>(gd + 192 + 32 * half + 4 * q4);
-            const float gv[4] = {gs.x, gs.y, gs.z, gs.w};
-            float v[4];
+            for (int q = 0; q < 16; ++q) pk[q] = 0u;
+          } else {
+            const bool tri = half == (quad & 1);  // the block on the diagonal
+            const int last = row < 64 ? lane : lane - 1;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int s = 32 * half + 4 * q4 + e;
-              const float w = d[4 * q4 + e];
-              if (s == r) diag = w;
-              v[e] = s < r ? mul * ex2(gr - gv[e]) * w : 0.0f;
+            for (int q4 = 0; q4 < 8; ++q4) {
+              const float4 gs = *reinterpret_cast<const float4*>(gd + 192 + 32 * half + 4 * q4);
+              float v[4] = {ex2(gr - gs.x), ex2(gr - gs.y), ex2(gr - gs.z), ex2(gr - gs.w)};
+              if (tri) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (4 * q4 + e > last) v[e] = 0.0f;
+              }
+              pk[2 * q4] = pack2(mul * v[0] * d[4 * q4], mul * v[1] * d[4 * q4 + 1]);
+              pk[2 * q4 + 1] = pack2(mul * v[2] * d[4 * q4 + 2], mul * v[3] * d[4 * q4 + 3]);
             }
-            pk[2 * q4] = pack2(v[0], v[1]);
-            pk[2 * q4 + 1] = pack2(v[2], v[3]);
+            if (tri && quad >= 2) {  // dW_r . U_r: column `lane` of this block, by halving
+#pragma unroll
+              for (int w = 16; w > 0; w >>= 1)
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                  if (q < w) d[q] = lane & w ? d[q + w] : d[q];
+              diag = d[0];
+            }
           }
           unsigned char* nm = smem + SM_NM;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             *reinterpret_cast<uint4*>(nm + sw128(row, 32 * half + 8 * q)) =
                 make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
-          if ((r >> 5) == half) {  // this thread held the diagonal of its row
-            if (row < 64) {
-              own[r] = P.scale * diag;
-            } else if (r < L) {
-              const float b = gd[128 + r], t = diag / b / b;
-              P.dbeta[(ch.t0 + r) * P.Hv + h] = __float2bfloat16_rn(t);
-            }
-          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        named_bar(NB_NM, NB_ALL);  // [dN; dM] written, D2 read; p visible to every epilogue warp
-        // ---- <S, dS>
+        named_bar(NB_NM, NB_ALL);  // [dN; dM] written, D2 read
+        // ---- <S, dS>, dbeta; q and k of the item
         float fr = 0.0f;
-        if (in) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint32_t o = (uint32_t)(q * 256 + tid) * 16;
-            fr = dot8(*reinterpret_cast<const uint4*>(smem + SM_S + o),
-                      *reinterpret_cast<const uint4*>(smem + SM_DS + o), fr);
-          }
-        }
+        if (in) fr = dot_rows16(sbase + SM_S, sbase + SM_DS, warp, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_HE]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) fr += __shfl_xor_sync(0xffffffffu, fr, o);
         if (lane == 0) sums[warp] = fr;
+        if (quad >= 2 && half == (quad & 1) && in && r < L) {
+          const float b = gd[128 + r], t = diag / b / b;
+          P.dbeta[(ch.t0 + r) * P.Hv + h] = __float2bfloat16_rn(t);
+        }
+        if (gi == 0) {
+          if (wait_w(B_KQ, y & 1)) {
+            // token t has t % 8 fixed per unrolled step: so is the swizzle of this thread's column
+            const unsigned char* kt = smem + SM_KQ + (row >> 6) * 16384 + half * 4096 + (row & 7) * 2;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const uint32_t c8 = ((uint32_t)row & 63) >> 3;
+              const unsigned char* p0 = kt + 2 * q * 128 + ((c8 ^ ((2 * q) & 7)) << 4);
+              const unsigned char* p1 = kt + (2 * q + 1) * 128 + ((c8 ^ ((2 * q + 1) & 7)) << 4);
+              kv[q] = *reinterpret_cast<const uint16_t*>(p0) |
+                      (uint32_t) * reinterpret_cast<const uint16_t*>(p1) << 16;
+              qv[q] = *reinterpret_cast<const uint16_t*>(p0 + 8192) |
+                      (uint32_t) * reinterpret_cast<const uint16_t*>(p1 + 8192) << 16;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_KQE]);  // this warp needs K and Q no more
+        }
         // ---- epilogue B
         if (wait_w(B_N, x & 1)) {
           tc_fence_after();
-          float kw = 0.0f, keep = 0.0f;
-          const unsigned char* kt = smem + SM_KQ + (row >> 6) * 16384;
+          f32x2 kw = 0ull;
+          float keep = 0.0f;
 #pragma unroll
           for (int b = 0; b < 4; ++b) {  // 8 tokens at a time
             const int t0 = 32 * half + 8 * b;
@@ -251,51 +347,53 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
             tmem_ld8(tmem + lo + TM_D5 + t0, d5);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int t = t0 + e;
-              // token t0 + e has t % 8 == e: the swizzle of this thread's column is fixed per e
-              const uint32_t off = (uint32_t)t * 128 + (((((uint32_t)row & 63) >> 3) ^ e) << 4) +
-                                   ((uint32_t)row & 7) * 2;
-              const float kv = bf_at(kt + off), qv = bf_at(kt + 8192 + off);
-              const float gm = gd[t], dd = gd[64 + t], p = own[t];
-              const float fq = fmaf(P.scale * gm, d1a[e], d4a[e]);
-              const float fe = fmaf(-gm, d1b[e], d4b[e]);
-              const float w1 = dd * d3[e], fw = w1 + d5[e];
-              v[e] = fmaf(qv, fq, kv * (fe - fw));
-              kw = fmaf(kv, w1, kw);
-              aq[8 * b + e] += fmaf(p, kv, fq);
-              ak[8 * b + e] += fmaf(p, qv, fe + fw);
+            for (int e = 0; e < 8; e += 2) {
+              const int p = 4 * b + e / 2;
+              const f32x2 k2 = widen(kv[p]), q2 = widen(qv[p]);
+              const float2 g1 = *reinterpret_cast<const float2*>(gd + t0 + e);
+              const float2 dd = *reinterpret_cast<const float2*>(gd + 64 + t0 + e);
+              const f32x2 g2 = two(g1.x, g1.y), neg = two(-1.0f, -1.0f);
+              const f32x2 fq = fma2(mul2(two(P.scale, P.scale), g2), two(d1a[e], d1a[e + 1]),
+                                    two(d4a[e], d4a[e + 1]));
+              const f32x2 fe = fma2(mul2(neg, g2), two(d1b[e], d1b[e + 1]),
+                                    two(d4b[e], d4b[e + 1]));
+              const f32x2 w1 = mul2(two(dd.x, dd.y), two(d3[e], d3[e + 1]));
+              const f32x2 fw = add2(w1, two(d5[e], d5[e + 1]));
+              const float2 vv = parts(fma2(q2, fq, mul2(k2, fma2(neg, fw, fe))));
+              v[e] = vv.x;
+              v[e + 1] = vv.y;
+              kw = fma2(k2, w1, kw);
+              aq[p] = add2(aq[p], fq);
+              ak[p] = add2(ak[p], add2(fe, fw));
             }
             // sum over the warp's 32 channels: halve the tokens a lane holds three times, then add the
             // four lanes that are left with the same token: token t0 + (lane >> 2)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const bool up = lane & 16;
-              const float give = up ? v[e] : v[e + 4], stay = up ? v[e + 4] : v[e];
-              v[e] = stay + __shfl_xor_sync(0xffffffffu, give, 16);
-            }
+            for (int w = 4; w > 0; w >>= 1) {
+              const bool up = lane & (4 * w);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const bool up = lane & 8;
-              const float give = up ? v[e] : v[e + 2], stay = up ? v[e + 2] : v[e];
-              v[e] = stay + __shfl_xor_sync(0xffffffffu, give, 8);
-            }
-            {
-              const bool up = lane & 4;
-              const float give = up ? v[0] : v[1], stay = up ? v[1] : v[0];
-              v[0] = stay + __shfl_xor_sync(0xffffffffu, give, 4);
+              for (int e = 0; e < 4; ++e) {
+                if (e < w) {
+                  const float give = up ? v[e] : v[e + w], stay = up ? v[e + w] : v[e];
+                  v[e] = stay + __shfl_xor_sync(0xffffffffu, give, 4 * w);
+                }
+              }
             }
             v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
             v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
             if ((lane & 3) == b) keep = v[0];  // lane 4 k + b ends up with token 8 b + k
           }
           red[quad * 64 + 32 * half + 8 * (lane & 3) + (lane >> 2)] = keep;
+          const float2 k2 = parts(kw);
+          float kws = k2.x + k2.y;
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) kw += __shfl_xor_sync(0xffffffffu, kw, o);
-          if (lane == 0) sums[8 + warp] = kw;
+          for (int o = 16; o > 0; o >>= 1) kws += __shfl_xor_sync(0xffffffffu, kws, o);
+          if (lane == 0) sums[8 + warp] = kws;
         }
         tc_fence_before();
         named_bar_arrive(NB_D, NB_ALL);  // D1, D3, D4, D5 read
+        if (tid == 0 && gi == G - 1) bulk_wait_read<0>();  // the previous item's dq and dk have left
+        __syncwarp();
         named_bar(NB_E, NB_EPI);         // dgamma parts and sums of all warps
         // ---- dg: suffix sums over the chunk, and what leaves through the state
         const bool live = __all_sync(0xffffffffu, !*abort_flag) != 0;
@@ -323,44 +421,71 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
             }
           }
           a0 += __shfl_sync(0xffffffffu, a1, 0);
+          // the first token's decay multiplies the initial state: without one its gradient is zero
+          const bool none = ch.first && !P.S0;
           __nv_bfloat16* dst = P.dg + ch.t0 * P.Hv + h;
-          if (lane < L) dst[(int64_t)lane * P.Hv] = __float2bfloat16_rn(a0 + f);
+          if (lane < L)
+            dst[(int64_t)lane * P.Hv] = __float2bfloat16_rn(lane == 0 && none ? 0.0f : a0 + f);
           if (32 + lane < L) dst[(int64_t)(32 + lane) * P.Hv] = __float2bfloat16_rn(a1 + f);
         }
         // ---- dv rows whose beta was floored: T' used the floored value
-        if (tid < L && live) {
+        if (tid < L && live && fabsf(gd[128 + tid]) == kBetaFloor) {
           const int64_t at = (ch.t0 + tid) * P.Hv + h;
-          const float b = P.beta[at], bf = gd[128 + tid];
-          if (b != bf) {
-            __nv_bfloat16* dv = P.dv + at * tm::D;
-            for (int e = 0; e < tm::D; ++e)
-              dv[e] = __float2bfloat16_rn(__bfloat162float(dv[e]) * (b / bf));
-          }
+          const float ratio = P.beta[at] / gd[128 + tid];
+          __nv_bfloat16* dv = P.dv + at * tm::D;
+          for (int e = 0; e < tm::D; ++e)
+            dv[e] = __float2bfloat16_rn(__bfloat162float(dv[e]) * ratio);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[B_KQE]);  // K and Q of this item read
-      // ---- dq, dk: lanes row, row ^ 1 swap, so that a store is a pair of channels
-      if (__all_sync(0xffffffffu, !*abort_flag)) {
-        const int odd = row & 1;
-        const int64_t rs = (int64_t)P.Hk * tm::D;
-        const int64_t base = (ch.t0 + 32 * half + odd) * rs + hk * tm::D + (row & ~1);
-        uint32_t* oq = reinterpret_cast<uint32_t*>(P.dq + base);
-        uint32_t* ok = reinterpret_cast<uint32_t*>(P.dk + base);
-        const uint32_t sel = odd ? 0x7632u : 0x5410u;
+      // ---- dq, dk: two bytes at a time into shared memory (a warp's 32 channels are 64 consecutive
+      // bytes), out as boxes of tensor maps; a partial chunk row by row
+      if (L == tm::C) {
+        unsigned char* tile = smem + SM_OUT + (row >> 6) * 8192 + half * 4096 + (row & 7) * 2;
+        const uint32_t c8 = ((uint32_t)row & 63) >> 3;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
-          const uint32_t mq = pack2(aq[2 * q], aq[2 * q + 1]), mk = pack2(ak[2 * q], ak[2 * q + 1]);
-          const uint32_t nq = __shfl_xor_sync(0xffffffffu, mq, 1);
-          const uint32_t nk = __shfl_xor_sync(0xffffffffu, mk, 1);
-          if (32 * half + 2 * q + odd < L) {
-            oq[(int64_t)q * rs] = odd ? __byte_perm(nq, mq, sel) : __byte_perm(mq, nq, sel);
-            ok[(int64_t)q * rs] = odd ? __byte_perm(nk, mk, sel) : __byte_perm(mk, nk, sel);
+          const float2 fq = parts(aq[q]), fk = parts(ak[q]);
+          const uint32_t wq = pack2(fq.x, fq.y), wk = pack2(fk.x, fk.y);
+          unsigned char* p0 = tile + 2 * q * 128 + ((c8 ^ ((2 * q) & 7)) << 4);
+          unsigned char* p1 = tile + (2 * q + 1) * 128 + ((c8 ^ ((2 * q + 1) & 7)) << 4);
+          *reinterpret_cast<uint16_t*>(p0) = (uint16_t)wq;
+          *reinterpret_cast<uint16_t*>(p1) = (uint16_t)(wq >> 16);
+          *reinterpret_cast<uint16_t*>(p0 + 16384) = (uint16_t)wk;
+          *reinterpret_cast<uint16_t*>(p1 + 16384) = (uint16_t)(wk >> 16);
+        }
+        fence_proxy_async_smem();
+      } else if (__all_sync(0xffffffffu, !*abort_flag)) {
+        const int64_t rs = (int64_t)P.Hk * tm::D;
+        const int64_t base = (ch.t0 + 32 * half) * rs + hk * tm::D + row;
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const float2 fq = parts(aq[q]), fk = parts(ak[q]);
+          const int t = 32 * half + 2 * q;
+          if (t < L) {
+            P.dq[base + 2 * q * rs] = __float2bfloat16_rn(fq.x);
+            P.dk[base + 2 * q * rs] = __float2bfloat16_rn(fk.x);
+          }
+          if (t + 1 < L) {
+            P.dq[base + (2 * q + 1) * rs] = __float2bfloat16_rn(fq.y);
+            P.dk[base + (2 * q + 1) * rs] = __float2bfloat16_rn(fk.y);
           }
         }
       }
+      named_bar(NB_O, NB_EPI);
+      if (tid == 0 && L == tm::C && !*abort_flag) {
+        const int32_t t0 = (int32_t)ch.t0;
+        tma_store_3d(&map_dq, smem + SM_OUT, 0, hk, t0);
+        tma_store_3d(&map_dq, smem + SM_OUT + 8192, 64, hk, t0);
+        tma_store_3d(&map_dk, smem + SM_OUT + 16384, 0, hk, t0);
+        tma_store_3d(&map_dk, smem + SM_OUT + 24576, 64, hk, t0);
+        bulk_commit();
+      }
+      __syncwarp();
     }
-  } else if (warp == W_PROD) {
+    if (tid == 0) bulk_wait<0>();  // nothing on its way out of shared memory
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
+    if (warp == W_PROD) {
     // ------------------------------------------------------------------ TMA producer ---------
     if (elect_one()) {
       prefetch_tensormap(&map_k);
@@ -454,7 +579,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
       if (x > 0 && !mbar_wait(&bars[B_H], (uint32_t)(x - 1) & 1)) report(P.status, GDN_ERR_TIMEOUT);
       if (y > 0 && !mbar_wait(&bars[B_KQ], (uint32_t)(y - 1) & 1)) report(P.status, GDN_ERR_TIMEOUT);
     }
-  } else {
+    } else if (warp == W_MMA) {
     // ------------------------------------------------------------------ MMA issuer -----------
     const uint32_t id_p = idesc_bf16(128, 64, 0, 1);    // A = [dO; dW] K-major, B = U^T MN-major
     const uint32_t id_d1 = idesc_bf16(128, 128, 1, 0);  // A = S^T MN-major, B = [dO; dW] K-major
@@ -518,6 +643,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
             for (int ks = 0; ks < 4; ++ks)
               mma_bf16_ss(tmem + TM_D5, dadd(dKt, ks * 2048), dadd(dMn, ks * 2048), id_d3, 1);
             mma_commit(&bars[B_N]);
+            if (gi == G - 1) mma_commit(&bars[B_KQE]);
           }
         }
         __syncwarp();
@@ -529,6 +655,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
       if (!mbar_wait(&bars[B_DRAIN], 0)) fail(GDN_ERR_TIMEOUT);
     }
     __syncwarp();
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -545,6 +672,7 @@ cudaError_t launch_bwd_grads(const Args& a, cudaStream_t s) {
   unsigned char* ws = reinterpret_cast<unsigned char*>(a.ws);
   GradParams p;
   p.beta = a.beta;
+  p.S0 = a.S0;
   p.cu = a.cu;
   p.ws = ws;
   p.dq = (__nv_bfloat16*)a.dq;
@@ -561,10 +689,12 @@ cudaError_t launch_bwd_grads(const Args& a, cudaStream_t s) {
   p.Hk = a.Hk;
   p.Hv = a.Hv;
   if (n_tok > 0x7fffffff) return cudaErrorInvalidConfiguration;  // TMA coordinates are 32-bit
-  CUtensorMap mk, mq, mo, mv;
+  CUtensorMap mk, mq, mo, mv, mdq, mdk;
   const int64_t hv = (int64_t)a.Hv * tm::D;
   if (!make_tok_map(&mk, a.k, a.Hk, n_tok, a.ts.k) || !make_tok_map(&mq, a.q, a.Hk, n_tok, a.ts.q) ||
-      !make_tok_map(&mo, a.dout, a.Hv, n_tok, hv) || !make_tok_map(&mv, a.dv_, a.Hv, n_tok, hv))
+      !make_tok_map(&mo, a.dout, a.Hv, n_tok, hv) || !make_tok_map(&mv, a.dv_, a.Hv, n_tok, hv) ||
+      !make_tok_map(&mdq, a.dq, a.Hk, n_tok, (int64_t)a.Hk * tm::D) ||
+      !make_tok_map(&mdk, a.dk_, a.Hk, n_tok, (int64_t)a.Hk * tm::D))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -573,7 +703,7 @@ cudaError_t launch_bwd_grads(const Args& a, cudaStream_t s) {
     e = cudaFuncSetAttribute(bwd_grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_BYTES);
   if (e != cudaSuccess) return e;
   const int64_t grid = p.items < sms ? p.items : sms;
-  bwd_grads_kernel<<<(unsigned)grid, THREADS, SM_BYTES, s>>>(mk, mq, mo, mv, p);
+  bwd_grads_kernel<<<(unsigned)grid, THREADS, SM_BYTES, s>>>(mk, mq, mo, mv, mdq, mdk, p);
   return cudaGetLastError();
 }
 

@@ -42,8 +42,9 @@ __host__ __device__ inline int64_t max_slots(int N, int64_t n_tok, int C) {
 }
 
 // The smallest magnitude of beta used in T' (see bwd_simt.cu): 2^-30.
+constexpr float kBetaFloor = 1.0f / (1 << 30);
 __device__ __forceinline__ float floor_beta(float b) {
-  return fabsf(b) < 9.313225746e-10f ? copysignf(9.313225746e-10f, b) : b;
+  return fabsf(b) < kBetaFloor ? copysignf(kBetaFloor, b) : b;
 }
 
 // Sequence n's tokens and the slot of its first chunk; false for a malformed cu_seqlens met up to n
@@ -71,6 +72,7 @@ __device__ __forceinline__ bool seq_range(const int32_t* cu, int64_t T, int n, i
 struct Chunk {
   int n, L;
   int64_t t0;
+  bool first;  // of its sequence
 };
 
 // The chunk of a slot; false past the last one or for a malformed cu_seqlens (reported).
@@ -82,6 +84,7 @@ __device__ __forceinline__ bool find_chunk(const int32_t* cu, int64_t T, int N, 
     ch.n = (int)(slot / per);
     const int64_t c = slot - (int64_t)ch.n * per;
     ch.t0 = (int64_t)ch.n * T + c * C;
+    ch.first = c == 0;
     ch.L = (int)(T - c * C < C ? T - c * C : C);
     return true;
   }
@@ -96,6 +99,7 @@ __device__ __forceinline__ bool find_chunk(const int32_t* cu, int64_t T, int N, 
     if (slot < base + nch) {
       ch.n = m;
       ch.t0 = a + (slot - base) * C;
+      ch.first = slot == base;
       ch.L = (int)(b - ch.t0 < C ? b - ch.t0 : C);
       return true;
     }
@@ -103,6 +107,38 @@ __device__ __forceinline__ bool find_chunk(const int32_t* cu, int64_t T, int N, 
   }
   return false;
 }
+
+// find_chunk for slots that never decrease: the search goes on from the sequence found last, so a
+// persistent block reads each entry of cu_seqlens about once.
+struct ChunkCursor {
+  int m = 0;
+  int64_t base = 0, a = -1, b = -1;  // sequence m: slot of its first chunk, its tokens (a < 0: not read yet)
+  __device__ __forceinline__ bool find(const int32_t* cu, int64_t T, int N, int C, int64_t slot,
+                                       Chunk& ch, int* status) {
+    if (!cu) return find_chunk(cu, T, N, C, slot, ch, status);
+    for (; m < N; ++m, a = -1) {
+      if (a < 0) {
+        a = cu[m];
+        b = cu[m + 1];
+        if (a < 0 || b < a || b > T) {
+          if (threadIdx.x == 0) report(status, GDN_ERR_DEVICE_ARG);
+          a = -1;
+          return false;
+        }
+      }
+      const int64_t nch = (b - a + C - 1) / C;
+      if (slot < base + nch) {
+        ch.n = m;
+        ch.t0 = a + (slot - base) * C;
+        ch.L = (int)(b - ch.t0 < C ? b - ch.t0 : C);
+        ch.first = slot == base;
+        return true;
+      }
+      base += nch;
+    }
+    return false;
+  }
+};
 
 }  // namespace bwd
 }  // namespace gdn
