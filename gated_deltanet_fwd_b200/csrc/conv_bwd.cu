@@ -8,20 +8,31 @@
 // An input in front of its sequence is conv_state_in; its gradient is the same sum at a negative place.
 // conv_state_out is a copy of the last K-1 of (history, inputs), so dconv_state_out is added there.
 //
-// HBM-bound: dy and x in, dx out, once each (and K-1 tokens of halo at the ends of a token range).
+// HBM-bound: dy and x in, dx out, once each (and K-1 tokens of halo at the ends of a token range), with
+// the instructions per element close behind, so the arithmetic is packed (two channels an instruction).
 // A thread holds 4 channels and streams a range of tokens forward: x[t-KT+1 .. t] and
 // dpre[t-KT+1 .. t] are register windows, so each token is loaded and each dpre computed once; dx is
-// stored KT-1 tokens late.  A warp spans 128 channels, so the norm's sums for groups up to 128 are
-// shuffles; a group of 256 spans the block's two warps, which exchange their sums through shared memory.
+// stored KT-1 tokens late.  Whole batches of tokens inside a range and a sequence run unrolled without
+// conditions, their inputs copied up to three batches ahead into a private ring in shared memory
+// (registers are taken by the windows and sums); the ends run token by token.
+// A warp spans 128 channels, so the norm's sums for groups up to 128 are shuffles -- for 128 itself both
+// sums share them: a lane half keeps one sum each, 6 shuffles instead of 10.  A group of 256 spans the
+// block's two warps, which exchange their sums through shared memory.
 // dw and dbias are summed in registers over the range; each range writes one partial row, added in
 // order by a second kernel.  Kernels exist for 2, 4 and 8 taps; a smaller K has leading zero taps.
 #include "act8.cuh"
+#include "f32x2.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int CB_THREADS = 64;
 constexpr int CB_CH = 4;  // channels per thread
+
+struct Four {  // 4 channels as two packed pairs
+  f32x2 a, b;
+};
+__device__ __forceinline__ Four zero4() { return {0ull, 0ull}; }
 
 template <typename T>
 struct Raw4;
@@ -31,12 +42,7 @@ struct Raw4<__nv_bfloat16> {
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     u = __ldg(reinterpret_cast<const uint2*>(p));
   }
-  __device__ __forceinline__ void to_float(float (&f)[4]) const {
-    f[0] = __uint_as_float(u.x << 16);
-    f[1] = __uint_as_float(u.x & 0xffff0000u);
-    f[2] = __uint_as_float(u.y << 16);
-    f[3] = __uint_as_float(u.y & 0xffff0000u);
-  }
+  __device__ __forceinline__ Four get() const { return {widen(u.x), widen(u.y)}; }
 };
 template <>
 struct Raw4<float> {
@@ -44,44 +50,78 @@ struct Raw4<float> {
   __device__ __forceinline__ void load(const float* p) {
     u = __ldg(reinterpret_cast<const float4*>(p));
   }
-  __device__ __forceinline__ void to_float(float (&f)[4]) const {
-    f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
-  }
+  __device__ __forceinline__ Four get() const { return {two(u.x, u.y), two(u.z, u.w)}; }
 };
 
-__device__ __forceinline__ void put4(__nv_bfloat16* p, const float (&f)[4]) {
-  __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+__device__ __forceinline__ void put4(__nv_bfloat16* p, const Four& f) {
+  const float2 x = parts(f.a), y = parts(f.b);
+  __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(y.x, y.y);
   *reinterpret_cast<uint2*>(p) =
       make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
-__device__ __forceinline__ void put4(float* p, const float (&f)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+__device__ __forceinline__ void put4(float* p, const Four& f) {
+  const float2 x = parts(f.a), y = parts(f.b);
+  *reinterpret_cast<float4*>(p) = make_float4(x.x, x.y, y.x, y.y);
 }
 
-// 4 channels of the conv's input: as they are, or codes and their group's scale
+// asynchronous copy of N bytes into this thread's own shared memory
+template <int N>
+__device__ __forceinline__ void ring_copy(unsigned char* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(N) : "memory");
+}
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ring_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 4 channels of the conv's input: as they are, or codes and their group's scale.  `at` = t * C + c.
 template <typename T, bool CK>
 struct XIn {
   Raw4<T> r;
-  __device__ __forceinline__ void load(const ConvBwdArgs& P, int64_t t, int c) {
-    r.load((const T*)P.x + t * P.C + c);
+  static constexpr int SLOT = 4 * sizeof(T);  // bytes of a ring entry
+  __device__ __forceinline__ void load(const ConvBwdArgs& P, int64_t at, int64_t t, int) {
+    r.load((const T*)P.x + at);
   }
-  __device__ __forceinline__ void to_float(float (&f)[4]) const { r.to_float(f); }
+  __device__ __forceinline__ Four get() const { return r.get(); }
+  static __device__ __forceinline__ void copy(unsigned char* slot, const ConvBwdArgs& P, int64_t at,
+                                              int64_t, int) {
+    ring_copy<SLOT>(slot, (const T*)P.x + at);
+  }
 };
 template <typename T>
 struct XIn<T, true> {
   uint32_t u;
   float sc;
-  __device__ __forceinline__ void load(const ConvBwdArgs& P, int64_t t, int c) {
-    u = __ldg(reinterpret_cast<const uint32_t*>((const int8_t*)P.x + t * P.C + c));
-    sc = __ldg(P.xs + t * (P.C / P.xgroup) + c / P.xgroup);
+  static constexpr int SLOT = 8;
+  static __device__ __forceinline__ void copy(unsigned char* slot, const ConvBwdArgs& P, int64_t at,
+                                              int64_t t, int group) {
+    ring_copy<4>(slot, (const int8_t*)P.x + at);
+    ring_copy<4>(slot + 4, P.xs + t * (P.C / P.xgroup) + group);
   }
-  __device__ __forceinline__ void to_float(float (&f)[4]) const { act8::unpack4(u, sc, f); }
+  __device__ __forceinline__ void load(const ConvBwdArgs& P, int64_t at, int64_t t, int group) {
+    u = __ldg(reinterpret_cast<const uint32_t*>((const int8_t*)P.x + at));
+    sc = __ldg(P.xs + t * (P.C / P.xgroup) + group);
+  }
+  __device__ __forceinline__ Four get() const {
+    float f[4];
+    act8::unpack4(u, sc, f);
+    return {two(f[0], f[1]), two(f[2], f[3])};
+  }
 };
 
-template <typename T, int KT, bool CK>
-__global__ void __launch_bounds__(CB_THREADS) conv_bwd_kernel(const ConvBwdArgs P) {
+// G128: the normalised groups are 128 channels, one warp each
+template <typename T, int KT, bool CK, bool G128>
+__global__ void __launch_bounds__(CB_THREADS, KT == 8 ? 4 : 8) conv_bwd_kernel(const ConvBwdArgs P) {
   constexpr int D = KT - 1;                // tokens that dx lags behind
-  constexpr int PF = KT == 8 ? 4 : 8;      // tokens loaded ahead
+  constexpr int PF = 4, AHEAD = 3;         // tokens of a batch, batches copied ahead
+  constexpr int XS = XIn<T, CK>::SLOT, YS = 4 * sizeof(T), RING = PF * (AHEAD + 1);
+  __shared__ __align__(16) unsigned char ring_x[RING * CB_THREADS * XS];
+  __shared__ __align__(16) unsigned char ring_y[RING * CB_THREADS * YS];
   __shared__ float2 ex[2][2];              // sums of a 256-channel group, two tokens in turn
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = blockIdx.x * (CB_THREADS * CB_CH) + tid * CB_CH;
@@ -92,17 +132,25 @@ __global__ void __launch_bounds__(CB_THREADS) conv_bwd_kernel(const ConvBwdArgs 
   const bool norm = on && c < P.n_l2;
   const int gl = P.group / CB_CH;  // lanes of a group
   const bool any = P.n_l2 > (P.group > 128 ? blockIdx.x * (CB_THREADS * CB_CH) : c - lane * CB_CH);
+  const int xg = CK && on ? c / P.xgroup : 0;
 
-  float w[KT][4], bias[4] = {}, dw[KT][4] = {}, db[4] = {};
+  Four w[KT], bias = zero4(), dw[KT], db = zero4();
 #pragma unroll
-  for (int i = 0; i < KT; ++i)
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      w[i][q] = on && i >= pad ? __ldg(P.w + (int64_t)(c + q) * K + i - pad) : 0.0f;
-  if (on && P.bias)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) bias[q] = __ldg(P.bias + c + q);
-
+  for (int i = 0; i < KT; ++i) {
+    const float* p = P.w + (int64_t)c * K + i - pad;
+    const bool has = on && i >= pad;
+    w[i].a = two(has ? __ldg(p) : 0.0f, has ? __ldg(p + K) : 0.0f);
+    w[i].b = two(has ? __ldg(p + 2 * K) : 0.0f, has ? __ldg(p + 3 * K) : 0.0f);
+    dw[i] = zero4();
+  }
+  if (on && P.bias) {
+    bias.a = two(__ldg(P.bias + c), __ldg(P.bias + c + 1));
+    bias.b = two(__ldg(P.bias + c + 2), __ldg(P.bias + c + 3));
+  }
+  // a history place of this thread's channels (K - 1 apart)
+  auto hist = [&](const float* p) -> Four {
+    return {two(__ldg(p), __ldg(p + K - 1)), two(__ldg(p + 2 * (K - 1)), __ldg(p + 3 * (K - 1)))};
+  };
   auto bound = [&](int m, int64_t& b, int64_t& e) {  // sequence m's tokens, clamped to the tensor
     b = P.cu ? P.cu[m] : (int64_t)m * P.T;
     e = P.cu ? P.cu[m + 1] : b + P.T;
@@ -119,6 +167,85 @@ __global__ void __launch_bounds__(CB_THREADS) conv_bwd_kernel(const ConvBwdArgs 
     }
   }
   if (r0 < r1) {
+    const f32x2 one = two(1.0f, 1.0f), minus = two(-1.0f, -1.0f);
+    Four xw[KT], dp[KT];  // x[t - d], dpre[t - d]
+    // one token: its input and output gradient in; the windows move on, dp[0] is its dpre
+    auto token = [&](const Four& x, Four dy, int64_t t) {
+#pragma unroll
+      for (int d = KT - 1; d > 0; --d) {
+        xw[d] = xw[d - 1];
+        dp[d] = dp[d - 1];
+      }
+      xw[0] = x;
+      Four pre = bias;
+#pragma unroll
+      for (int d = 0; d < KT; ++d) {
+        pre.a = fma2(w[KT - 1 - d].a, xw[d].a, pre.a);
+        pre.b = fma2(w[KT - 1 - d].b, xw[d].b, pre.b);
+      }
+      auto sig = [](f32x2 v) {
+        const float2 f = parts(v);
+        return two(__fdividef(1.0f, 1.0f + __expf(-f.x)), __fdividef(1.0f, 1.0f + __expf(-f.y)));
+      };
+      const f32x2 sa = sig(pre.a), sb = sig(pre.b);
+      const f32x2 aa = mul2(pre.a, sa), ab = mul2(pre.b, sb);  // the activation
+      // sigma (1 + pre (1 - sigma)), as a product: it is 0, not infinity - infinity, far to the left
+      const f32x2 la = mul2(sa, fma2(pre.a, fma2(sa, minus, one), one));
+      const f32x2 lb = mul2(sb, fma2(pre.b, fma2(sb, minus, one), one));
+      if (any) {
+        const float2 s2 = parts(fma2(aa, aa, mul2(ab, ab)));
+        const float2 d2 = parts(fma2(aa, dy.a, mul2(ab, dy.b)));
+        float ss = s2.x + s2.y, ad = d2.x + d2.y;
+        if (G128) {
+          const bool up = lane & 16;
+          float v = (up ? ad : ss) + __shfl_xor_sync(0xffffffffu, up ? ss : ad, 16);
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          const float o = __shfl_xor_sync(0xffffffffu, v, 16);
+          ss = up ? o : v;
+          ad = up ? v : o;
+        } else {
+          for (int o = min(gl, 32) >> 1; o > 0; o >>= 1) {
+            ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            ad += __shfl_xor_sync(0xffffffffu, ad, o);
+          }
+          if (gl == 64) {
+            const int par = (int)(t & 1);
+            if (lane == 0) ex[par][warp] = make_float2(ss, ad);
+            __syncthreads();
+            const float2 e0 = ex[par][0], e1 = ex[par][1];
+            ss = e0.x + e1.x;
+            ad = e0.y + e1.y;
+          }
+        }
+        if (norm) {
+          const float rn = rsqrtf(ss + P.eps), f = -rn * rn * ad;
+          const f32x2 f2 = two(f, f), r2 = two(rn, rn);
+          dy.a = mul2(r2, fma2(aa, f2, dy.a));
+          dy.b = mul2(r2, fma2(ab, f2, dy.b));
+        }
+      }
+      dp[0].a = mul2(dy.a, la);
+      dp[0].b = mul2(dy.b, lb);
+    };
+    auto count = [&]() {  // the token belongs to this range: its part of dw and dbias
+      db.a = add2(db.a, dp[0].a);
+      db.b = add2(db.b, dp[0].b);
+#pragma unroll
+      for (int d = 0; d < KT; ++d) {
+        dw[KT - 1 - d].a = fma2(dp[0].a, xw[d].a, dw[KT - 1 - d].a);
+        dw[KT - 1 - d].b = fma2(dp[0].b, xw[d].b, dw[KT - 1 - d].b);
+      }
+    };
+    auto back = [&]() {  // the gradient of the input D places before dp[0]
+      Four v = {mul2(w[0].a, dp[0].a), mul2(w[0].b, dp[0].b)};
+#pragma unroll
+      for (int i = 1; i < KT; ++i) {
+        v.a = fma2(w[i].a, dp[i].a, v.a);
+        v.b = fma2(w[i].b, dp[i].b, v.b);
+      }
+      return v;
+    };
     int n = seq_of_token(P.cu, P.N, P.T, r0);
     for (; n < P.N; ++n) {
       int64_t s_beg, s_end;
@@ -128,138 +255,107 @@ __global__ void __launch_bounds__(CB_THREADS) conv_bwd_kernel(const ConvBwdArgs 
       if (a >= e) continue;
       const int64_t te = min(e + D, s_end);
       const int64_t cs = ((int64_t)n * P.C + c) * (K - 1);
-      float xw[KT][4], dp[KT][4] = {};  // x[t - d], dpre[t - d]
 #pragma unroll
-      for (int d = 1; d < KT; ++d) {
+      for (int d = 0; d < KT; ++d) {
+        xw[d] = zero4();
+        dp[d] = zero4();
+      }
+#pragma unroll
+      for (int d = 1; d < KT; ++d) {  // the inputs before the first token
         const int64_t p = a - d;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) xw[d - 1][q] = 0.0f;
         if (on && d < K) {
           if (p >= s_beg) {
             XIn<T, CK> xi;
-            xi.load(P, p, c);
-            xi.to_float(xw[d - 1]);
+            xi.load(P, p * P.C + c, p, xg);
+            xw[d - 1] = xi.get();
           } else if (P.cs_in) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              xw[d - 1][q] = __ldg(P.cs_in + cs + (int64_t)q * (K - 1) + (K - 1) + (p - s_beg));
+            xw[d - 1] = hist(P.cs_in + cs + (K - 1) + (p - s_beg));
           }
         }
       }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) xw[KT - 1][q] = 0.0f;
-      // the gradient of the input at place p (a token, or a place of the history) once dp[0] is dpre[p + D]
+      // place p: a token of this range, or one of the history if the sequence starts here
       auto emit = [&](int64_t p) {
         if (!on) return;
-        float v[4] = {};
-#pragma unroll
-        for (int i = 0; i < KT; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = fmaf(w[i][q], dp[i][q], v[q]);
+        Four v = back();
         const int64_t jo = p - (s_end - (K - 1));  // place in the history left behind
-        if (P.dcs_out && jo >= 0 && jo < K - 1)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] += __ldg(P.dcs_out + cs + (int64_t)q * (K - 1) + jo);
+        if (P.dcs_out && jo >= 0 && jo < K - 1) {
+          const Four o = hist(P.dcs_out + cs + jo);
+          v.a = add2(v.a, o.a);
+          v.b = add2(v.b, o.b);
+        }
         if (p >= a) {
           if (p < e) put4((T*)P.dx + p * P.C + c, v);
         } else if (p < s_beg && a == s_beg && P.dcs_in) {
           const int64_t j = p - s_beg + (K - 1);
-          if (j >= 0)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) P.dcs_in[cs + (int64_t)q * (K - 1) + j] = v[q];
+          if (j >= 0) {
+            float* o = P.dcs_in + cs + j;
+            const float2 x = parts(v.a), y = parts(v.b);
+            o[0] = x.x;
+            o[K - 1] = x.y;
+            o[2 * (K - 1)] = y.x;
+            o[3 * (K - 1)] = y.y;
+          }
         }
       };
-      auto shift = [&]() {
-#pragma unroll
-        for (int d = KT - 1; d > 0; --d)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) dp[d][q] = dp[d - 1][q];
-      };
-      XIn<T, CK> xn[PF];
-      Raw4<T> yn[PF];
-      auto fetch = [&](int64_t t) {
-#pragma unroll
-        for (int u = 0; u < PF; ++u)
-          if (on && t + u < te) {
-            xn[u].load(P, t + u, c);
-            yn[u].load((const T*)P.dy + (t + u) * P.C + c);
-          }
-      };
-      fetch(a);
-      for (int64_t tb = a; tb < te; tb += PF) {
-        XIn<T, CK> xc[PF];
-        Raw4<T> yc[PF];
-#pragma unroll
-        for (int u = 0; u < PF; ++u) {
-          xc[u] = xn[u];
-          yc[u] = yn[u];
+      auto single = [&](int64_t t) {
+        XIn<T, CK> xi;
+        Raw4<T> yi;
+        Four x = zero4(), dy = zero4();
+        if (on) {
+          xi.load(P, t * P.C + c, t, xg);
+          yi.load((const T*)P.dy + t * P.C + c);
+          x = xi.get();
+          dy = yi.get();
         }
-        fetch(tb + PF);
+        token(x, dy, t);
+        if (t < e) count();
+        emit(t - D);
+      };
+      int64_t t = a;
+#pragma unroll 1
+      for (; t < te && t < a + D; ++t) single(t);  // nothing to store yet, or history
+      if (t + PF <= e) {
+        unsigned char* rx = ring_x + tid * XS;
+        unsigned char* ry = ring_y + tid * YS;
+        auto fetch = [&](int64_t u0, int slot) {  // a batch, if it is whole and inside the range
+          if (on && u0 + PF <= e) {
+            const int64_t at = u0 * P.C + c;
 #pragma unroll
-        for (int u = 0; u < PF; ++u) {
-          const int64_t t = tb + u;
-          if (t >= te) break;
-#pragma unroll
-          for (int d = KT - 1; d > 0; --d)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) xw[d][q] = xw[d - 1][q];
-          shift();
-          float dyv[4] = {};
-          if (on) {
-            xc[u].to_float(xw[0]);
-            yc[u].to_float(dyv);
-          }
-          float act[4], slope[4], ss = 0.0f, ad = 0.0f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float pre = bias[q];
-#pragma unroll
-            for (int d = 0; d < KT; ++d) pre = fmaf(w[KT - 1 - d][q], xw[d][q], pre);
-            const float sg = __fdividef(1.0f, 1.0f + __expf(-pre));
-            act[q] = pre * sg;
-            slope[q] = sg * fmaf(pre, 1.0f - sg, 1.0f);
-            ss = fmaf(act[q], act[q], ss);
-            ad = fmaf(act[q], dyv[q], ad);
-          }
-          if (any) {
-            for (int o = min(gl, 32) >> 1; o > 0; o >>= 1) {
-              ss += __shfl_xor_sync(0xffffffffu, ss, o);
-              ad += __shfl_xor_sync(0xffffffffu, ad, o);
-            }
-            if (gl == 64) {
-              const int par = (int)(t & 1);
-              if (lane == 0) ex[par][warp] = make_float2(ss, ad);
-              __syncthreads();
-              const float2 e0 = ex[par][0], e1 = ex[par][1];
-              ss = e0.x + e1.x;
-              ad = e0.y + e1.y;
-            }
-            if (norm) {
-              const float rn = rsqrtf(ss + P.eps), f = rn * rn * ad;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) dyv[q] = rn * fmaf(-act[q], f, dyv[q]);
+            for (int u = 0; u < PF; ++u) {
+              XIn<T, CK>::copy(rx + (slot + u) * CB_THREADS * XS, P, at + (int64_t)u * P.C, u0 + u, xg);
+              ring_copy<YS>(ry + (slot + u) * CB_THREADS * YS, (const T*)P.dy + at + (int64_t)u * P.C);
             }
           }
+          ring_commit();
+        };
 #pragma unroll
-          for (int q = 0; q < 4; ++q) dp[0][q] = dyv[q] * slope[q];
-          if (t < e) {
+        for (int k = 0; k < AHEAD; ++k) fetch(t + k * PF, k * PF);
+        int slot = 0;
+#pragma unroll 1
+        for (; t + PF <= e; t += PF) {
+          fetch(t + AHEAD * PF, (slot + AHEAD * PF) % RING);
+          ring_wait<AHEAD>();
+          T* out = (T*)P.dx + (t - D) * P.C + c;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              db[q] += dp[0][q];
-#pragma unroll
-              for (int d = 0; d < KT; ++d)
-                dw[KT - 1 - d][q] = fmaf(dp[0][q], xw[d][q], dw[KT - 1 - d][q]);
-            }
+          for (int u = 0; u < PF; ++u) {
+            XIn<T, CK> xi = *reinterpret_cast<const XIn<T, CK>*>(rx + (slot + u) * CB_THREADS * XS);
+            Raw4<T> yi = *reinterpret_cast<const Raw4<T>*>(ry + (slot + u) * CB_THREADS * YS);
+            token(on ? xi.get() : zero4(), on ? yi.get() : zero4(), t + u);
+            count();
+            if (on) put4(out + (int64_t)u * P.C, back());
           }
-          emit(t - D);
+          slot = (slot + PF) % RING;
         }
+        ring_wait<0>();
       }
+#pragma unroll 1
+      for (; t < te; ++t) single(t);
       if (te == s_end) {  // nothing follows the sequence
 #pragma unroll 1
         for (int m = 1; m <= D; ++m) {
-          shift();
 #pragma unroll
-          for (int q = 0; q < 4; ++q) dp[0][q] = 0.0f;
+          for (int d = KT - 1; d > 0; --d) dp[d] = dp[d - 1];
+          dp[0] = zero4();
           emit(s_end - 1 + m - D);
         }
       }
@@ -269,45 +365,56 @@ __global__ void __launch_bounds__(CB_THREADS) conv_bwd_kernel(const ConvBwdArgs 
   if (on) {
     float* row = P.part + (int64_t)blockIdx.y * P.C * (K + 1);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-#pragma unroll
-      for (int i = 0; i < KT; ++i)
-        if (i >= pad) row[(int64_t)(c + q) * K + i - pad] = dw[i][q];
-      row[(int64_t)P.C * K + c + q] = db[q];
-    }
+    for (int i = 0; i < KT; ++i)
+      if (i >= pad) {
+        const float2 x = parts(dw[i].a), y = parts(dw[i].b);
+        float* o = row + (int64_t)c * K + i - pad;
+        o[0] = x.x;
+        o[K] = x.y;
+        o[2 * K] = y.x;
+        o[3 * K] = y.y;
+      }
+    const float2 x = parts(db.a), y = parts(db.b);
+    *reinterpret_cast<float4*>(row + (int64_t)P.C * K + c) = make_float4(x.x, x.y, y.x, y.y);
   }
 }
 
-template <typename T, int KT, bool CK>
+template <typename T, int KT, bool CK, bool G128>
 cudaError_t run(ConvBwdArgs a, cudaStream_t s) {
   int dev = 0, sms = 148, per_sm = 1;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, conv_bwd_kernel<T, KT, CK>, CB_THREADS, 0);
+  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, conv_bwd_kernel<T, KT, CK, G128>, CB_THREADS, 0);
   const int64_t tiles = (a.C + CB_THREADS * CB_CH - 1) / (CB_THREADS * CB_CH);
   // one wave of blocks, with at least 16 tokens in a range (the halo costs up to KT - 1)
   int64_t ranges = (int64_t)sms * (per_sm > 0 ? per_sm : 1) / tiles;
   if (ranges > (a.n_tok + 15) / 16) ranges = (a.n_tok + 15) / 16;
   if (ranges > a.max_parts) ranges = a.max_parts;
   if (ranges < 1) ranges = 1;
-  conv_bwd_kernel<T, KT, CK><<<dim3((unsigned)tiles, (unsigned)ranges), CB_THREADS, 0, s>>>(a);
+  conv_bwd_kernel<T, KT, CK, G128><<<dim3((unsigned)tiles, (unsigned)ranges), CB_THREADS, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t wk = (int64_t)a.C * a.K;
   return launch_sum_parts(a.part, ranges, a.dbias ? wk + a.C : wk, wk, a.dw, a.dbias, wk + a.C, s);
 }
 
-template <typename T, bool CK>
+template <typename T, bool CK, bool G128>
 cudaError_t taps(const ConvBwdArgs& a, cudaStream_t s) {
-  return a.K <= 2 ? run<T, 2, CK>(a, s) : a.K <= 4 ? run<T, 4, CK>(a, s) : run<T, 8, CK>(a, s);
+  return a.K <= 2   ? run<T, 2, CK, G128>(a, s)
+         : a.K <= 4 ? run<T, 4, CK, G128>(a, s)
+                    : run<T, 8, CK, G128>(a, s);
+}
+template <typename T, bool CK>
+cudaError_t group(const ConvBwdArgs& a, cudaStream_t s) {
+  return a.group == 128 ? taps<T, CK, true>(a, s) : taps<T, CK, false>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_conv_bwd(const ConvBwdArgs& a, gdn_dtype dt, cudaStream_t s) {
   if (dt == GDN_BF16)
-    return a.xs ? taps<__nv_bfloat16, true>(a, s) : taps<__nv_bfloat16, false>(a, s);
-  return a.xs ? taps<float, true>(a, s) : taps<float, false>(a, s);
+    return a.xs ? group<__nv_bfloat16, true>(a, s) : group<__nv_bfloat16, false>(a, s);
+  return a.xs ? group<float, true>(a, s) : group<float, false>(a, s);
 }
 
 }  // namespace gdn
