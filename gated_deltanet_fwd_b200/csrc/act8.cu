@@ -31,13 +31,12 @@ __global__ void __launch_bounds__(256) act_pack8_kernel(const T* __restrict__ x,
 #pragma unroll
     for (int u = 0; u < ACT_U; ++u) {
       const int64_t g = gb + u * stride + gsub;
-      float f[8];
-      raw[u].to_float(f);
-      uint32_t m = act8::amax8(f);
+      uint32_t m = act8::amax8(raw[u]);
 #pragma unroll
       for (int o = TPG / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (g < groups) {
-        float sc, inv;
+        float f[8], sc, inv;
+        raw[u].to_float(f);
         act8::scale_of(m, sc, inv);
         *reinterpret_cast<uint2*>(codes + g * GROUP + sub * 8) = act8::pack8(f, inv);
         if (sub == 0) scales[g] = sc;

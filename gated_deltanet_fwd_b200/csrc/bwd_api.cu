@@ -52,15 +52,15 @@ inline bool ws_ok(const void* ws, size_t have, size_t need) {
   return ws && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 && have >= need;
 }
 
-// Partial rows of the sums over tokens that a call's workspace has room for: enough for one wave of
-// blocks on any B200, fewer for short inputs.
+// Partial rows of the sums over tokens that a call's workspace has room for: enough for the blocks
+// of a launch on a B200, fewer for short inputs.
 int64_t gates_parts(int64_t n_tok) { return n_tok < 512 ? n_tok : 512; }
 int64_t norm_parts(int64_t rows, int dim) {
   const int64_t per = 2 * (256 / (dim / 8)), need = (rows + per - 1) / per;
   return need < 1184 ? need : 1184;
 }
 int64_t conv_parts(int64_t n_tok, int C) {
-  const int64_t tiles = (C + 255) / 256, most = 2368 / tiles > 1 ? 2368 / tiles : 1;
+  const int64_t tiles = (C + 255) / 256, most = 4736 / tiles > 1 ? 4736 / tiles : 1;
   const int64_t need = (n_tok + 15) / 16;
   return need < 1 ? 1 : need < most ? need : most;
 }

@@ -15,9 +15,9 @@
 // stored KT-1 tokens late.  Whole batches of tokens inside a range and a sequence run unrolled without
 // conditions, their inputs copied up to three batches ahead into a private ring in shared memory
 // (registers are taken by the windows and sums); the ends run token by token.
-// A warp spans 128 channels, so the norm's sums for groups up to 128 are shuffles -- for 128 itself both
-// sums share them: a lane half keeps one sum each, 6 shuffles instead of 10.  A group of 256 spans the
-// block's two warps, which exchange their sums through shared memory.
+// A warp spans 128 channels, so the norm's sums for groups up to 128 are shuffles -- for 128 itself two
+// tokens' four sums share them.  A group of 256 spans the block's two warps, which exchange their sums
+// through shared memory.
 // dw and dbias are summed in registers over the range; each range writes one partial row, added in
 // order by a second kernel.  Kernels exist for 2, 4 and 8 taps; a smaller K has leading zero taps.
 #include "act8.cuh"
@@ -169,13 +169,15 @@ __global__ void __launch_bounds__(CB_THREADS, KT == 8 ? 4 : 8) conv_bwd_kernel(c
   if (r0 < r1) {
     const f32x2 one = two(1.0f, 1.0f), minus = two(-1.0f, -1.0f);
     Four xw[KT], dp[KT];  // x[t - d], dpre[t - d]
-    // one token: its input and output gradient in; the windows move on, dp[0] is its dpre
-    auto token = [&](const Four& x, Four dy, int64_t t) {
+    auto sig = [](f32x2 v) {
+      const float2 f = parts(v);
+      return two(__fdividef(1.0f, 1.0f + __expf(-f.x)), __fdividef(1.0f, 1.0f + __expf(-f.y)));
+    };
+    // the activation of the token whose input came last, and its slope sigma (1 + pre (1 - sigma)) -- as a
+    // product: it is 0, not infinity - infinity, far to the left
+    auto activate = [&](const Four& x, Four& act, Four& slope) {
 #pragma unroll
-      for (int d = KT - 1; d > 0; --d) {
-        xw[d] = xw[d - 1];
-        dp[d] = dp[d - 1];
-      }
+      for (int d = KT - 1; d > 0; --d) xw[d] = xw[d - 1];
       xw[0] = x;
       Four pre = bias;
 #pragma unroll
@@ -183,50 +185,50 @@ __global__ void __launch_bounds__(CB_THREADS, KT == 8 ? 4 : 8) conv_bwd_kernel(c
         pre.a = fma2(w[KT - 1 - d].a, xw[d].a, pre.a);
         pre.b = fma2(w[KT - 1 - d].b, xw[d].b, pre.b);
       }
-      auto sig = [](f32x2 v) {
-        const float2 f = parts(v);
-        return two(__fdividef(1.0f, 1.0f + __expf(-f.x)), __fdividef(1.0f, 1.0f + __expf(-f.y)));
-      };
       const f32x2 sa = sig(pre.a), sb = sig(pre.b);
-      const f32x2 aa = mul2(pre.a, sa), ab = mul2(pre.b, sb);  // the activation
-      // sigma (1 + pre (1 - sigma)), as a product: it is 0, not infinity - infinity, far to the left
-      const f32x2 la = mul2(sa, fma2(pre.a, fma2(sa, minus, one), one));
-      const f32x2 lb = mul2(sb, fma2(pre.b, fma2(sb, minus, one), one));
-      if (any) {
-        const float2 s2 = parts(fma2(aa, aa, mul2(ab, ab)));
-        const float2 d2 = parts(fma2(aa, dy.a, mul2(ab, dy.b)));
-        float ss = s2.x + s2.y, ad = d2.x + d2.y;
-        if (G128) {
-          const bool up = lane & 16;
-          float v = (up ? ad : ss) + __shfl_xor_sync(0xffffffffu, up ? ss : ad, 16);
+      act = {mul2(pre.a, sa), mul2(pre.b, sb)};
+      slope.a = mul2(sa, fma2(pre.a, fma2(sa, minus, one), one));
+      slope.b = mul2(sb, fma2(pre.b, fma2(sb, minus, one), one));
+    };
+    auto dot = [](const Four& u, const Four& v) {
+      const float2 s = parts(fma2(u.a, v.a, mul2(u.b, v.b)));
+      return s.x + s.y;
+    };
+    // dy <- rn (dy - act rn^2 ad), f = -rn^2 ad
+    auto through_norm = [](Four& dy, const Four& act, float rn, float f) {
+      const f32x2 f2 = two(f, f), r2 = two(rn, rn);
+      dy.a = mul2(r2, fma2(act.a, f2, dy.a));
+      dy.b = mul2(r2, fma2(act.b, f2, dy.b));
+    };
+    auto enter = [&](const Four& dy, const Four& slope) {  // a token's dpre
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          const float o = __shfl_xor_sync(0xffffffffu, v, 16);
-          ss = up ? o : v;
-          ad = up ? v : o;
-        } else {
-          for (int o = min(gl, 32) >> 1; o > 0; o >>= 1) {
-            ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            ad += __shfl_xor_sync(0xffffffffu, ad, o);
-          }
-          if (gl == 64) {
-            const int par = (int)(t & 1);
-            if (lane == 0) ex[par][warp] = make_float2(ss, ad);
-            __syncthreads();
-            const float2 e0 = ex[par][0], e1 = ex[par][1];
-            ss = e0.x + e1.x;
-            ad = e0.y + e1.y;
-          }
+      for (int d = KT - 1; d > 0; --d) dp[d] = dp[d - 1];
+      dp[0] = {mul2(dy.a, slope.a), mul2(dy.b, slope.b)};
+    };
+    // one token: its input and output gradient in; the windows move on, dp[0] is its dpre
+    auto token = [&](const Four& x, Four dy, int64_t t) {
+      Four act, slope;
+      activate(x, act, slope);
+      if (any) {
+        float ss = dot(act, act), ad = dot(act, dy);
+        for (int o = min(gl, 32) >> 1; o > 0; o >>= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          ad += __shfl_xor_sync(0xffffffffu, ad, o);
+        }
+        if (gl == 64) {
+          const int par = (int)(t & 1);
+          if (lane == 0) ex[par][warp] = make_float2(ss, ad);
+          __syncthreads();
+          const float2 e0 = ex[par][0], e1 = ex[par][1];
+          ss = e0.x + e1.x;
+          ad = e0.y + e1.y;
         }
         if (norm) {
-          const float rn = rsqrtf(ss + P.eps), f = -rn * rn * ad;
-          const f32x2 f2 = two(f, f), r2 = two(rn, rn);
-          dy.a = mul2(r2, fma2(aa, f2, dy.a));
-          dy.b = mul2(r2, fma2(ab, f2, dy.b));
+          const float rn = rsqrtf(ss + P.eps);
+          through_norm(dy, act, rn, -rn * rn * ad);
         }
       }
-      dp[0].a = mul2(dy.a, la);
-      dp[0].b = mul2(dy.b, lb);
+      enter(dy, slope);
     };
     auto count = [&]() {  // the token belongs to this range: its part of dw and dbias
       db.a = add2(db.a, dp[0].a);
@@ -297,59 +299,98 @@ __global__ void __launch_bounds__(CB_THREADS, KT == 8 ? 4 : 8) conv_bwd_kernel(c
           }
         }
       };
-      auto single = [&](int64_t t) {
-        XIn<T, CK> xi;
-        Raw4<T> yi;
-        Four x = zero4(), dy = zero4();
+      unsigned char* rx = ring_x + tid * XS;
+      unsigned char* ry = ring_y + tid * YS;
+      auto fetch = [&](int64_t u0, int slot) {  // a batch, as far as it is needed
         if (on) {
-          xi.load(P, t * P.C + c, t, xg);
-          yi.load((const T*)P.dy + t * P.C + c);
-          x = xi.get();
-          dy = yi.get();
-        }
-        token(x, dy, t);
-        if (t < e) count();
-        emit(t - D);
-      };
-      int64_t t = a;
-#pragma unroll 1
-      for (; t < te && t < a + D; ++t) single(t);  // nothing to store yet, or history
-      if (t + PF <= e) {
-        unsigned char* rx = ring_x + tid * XS;
-        unsigned char* ry = ring_y + tid * YS;
-        auto fetch = [&](int64_t u0, int slot) {  // a batch, if it is whole and inside the range
-          if (on && u0 + PF <= e) {
-            const int64_t at = u0 * P.C + c;
+          const int64_t at = u0 * P.C + c;
 #pragma unroll
-            for (int u = 0; u < PF; ++u) {
+          for (int u = 0; u < PF; ++u)
+            if (u0 + u < te) {
               XIn<T, CK>::copy(rx + (slot + u) * CB_THREADS * XS, P, at + (int64_t)u * P.C, u0 + u, xg);
               ring_copy<YS>(ry + (slot + u) * CB_THREADS * YS, (const T*)P.dy + at + (int64_t)u * P.C);
             }
-          }
-          ring_commit();
-        };
+        }
+        ring_commit();
+      };
+      auto x_at = [&](int k) {
+        return on ? reinterpret_cast<const XIn<T, CK>*>(rx + k * CB_THREADS * XS)->get() : zero4();
+      };
+      auto y_at = [&](int k) {
+        return on ? reinterpret_cast<const Raw4<T>*>(ry + k * CB_THREADS * YS)->get() : zero4();
+      };
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) fetch(t + k * PF, k * PF);
-        int slot = 0;
+      for (int k = 0; k < AHEAD; ++k) fetch(a + k * PF, k * PF);
+      int slot = 0;
 #pragma unroll 1
-        for (; t + PF <= e; t += PF) {
-          fetch(t + AHEAD * PF, (slot + AHEAD * PF) % RING);
-          ring_wait<AHEAD>();
+      for (int64_t t = a; t < te; t += PF) {
+        fetch(t + AHEAD * PF, (slot + AHEAD * PF) % RING);
+        ring_wait<AHEAD>();
+        if (t >= a + D && t + PF <= e) {
           T* out = (T*)P.dx + (t - D) * P.C + c;
 #pragma unroll
-          for (int u = 0; u < PF; ++u) {
-            XIn<T, CK> xi = *reinterpret_cast<const XIn<T, CK>*>(rx + (slot + u) * CB_THREADS * XS);
-            Raw4<T> yi = *reinterpret_cast<const Raw4<T>*>(ry + (slot + u) * CB_THREADS * YS);
-            token(on ? xi.get() : zero4(), on ? yi.get() : zero4(), t + u);
-            count();
-            if (on) put4(out + (int64_t)u * P.C, back());
+          for (int u = 0; u < PF; u += 2) {
+            if (G128) {
+              // two tokens at once: lane halves take a token each, quarters a sum each, and the norm's
+              // factors are computed for both in one go: 9 shuffles for what took 20
+              Four act0, act1, sl0, sl1, dy0 = y_at(slot + u), dy1 = y_at(slot + u + 1);
+              activate(x_at(slot + u), act0, sl0);
+              const Four x3 = xw[KT - 1];  // leaves the window, but token t + u still needs it
+              activate(x_at(slot + u + 1), act1, sl1);
+              if (any) {
+                const bool up = lane & 16, second = lane & 8;
+                const float s0 = dot(act0, act0), s1 = dot(act1, act1);
+                const float a0 = dot(act0, dy0), a1 = dot(act1, dy1);
+                const float s = (up ? s1 : s0) + __shfl_xor_sync(0xffffffffu, up ? s0 : s1, 16);
+                const float q = (up ? a1 : a0) + __shfl_xor_sync(0xffffffffu, up ? a0 : a1, 16);
+                float v = (second ? q : s) + __shfl_xor_sync(0xffffffffu, second ? s : q, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                const float o = __shfl_xor_sync(0xffffffffu, v, 8);
+                const float rn = rsqrtf((second ? o : v) + P.eps);
+                const float f = -rn * rn * (second ? v : o);
+                const float rno = __shfl_xor_sync(0xffffffffu, rn, 16);
+                const float fo = __shfl_xor_sync(0xffffffffu, f, 16);
+                if (norm) {
+                  through_norm(dy0, act0, up ? rno : rn, up ? fo : f);
+                  through_norm(dy1, act1, up ? rn : rno, up ? f : fo);
+                }
+              }
+              enter(dy0, sl0);
+              // xw is a token further than dp here
+              db.a = add2(db.a, dp[0].a);
+              db.b = add2(db.b, dp[0].b);
+#pragma unroll
+              for (int d = 0; d < KT; ++d) {
+                const Four& x = d + 1 < KT ? xw[d + 1] : x3;
+                dw[KT - 1 - d].a = fma2(dp[0].a, x.a, dw[KT - 1 - d].a);
+                dw[KT - 1 - d].b = fma2(dp[0].b, x.b, dw[KT - 1 - d].b);
+              }
+              if (on) put4(out + (int64_t)u * P.C, back());
+              enter(dy1, sl1);
+              count();
+              if (on) put4(out + (int64_t)(u + 1) * P.C, back());
+            } else {
+#pragma unroll
+              for (int k = u; k < u + 2; ++k) {
+                token(x_at(slot + k), y_at(slot + k), t + k);
+                count();
+                if (on) put4(out + (int64_t)k * P.C, back());
+              }
+            }
           }
-          slot = (slot + PF) % RING;
-        }
-        ring_wait<0>();
-      }
+        } else {
 #pragma unroll 1
-      for (; t < te; ++t) single(t);
+          for (int u = 0; u < PF && t + u < te; ++u) {
+            token(x_at(slot + u), y_at(slot + u), t + u);
+            if (t + u < e) count();
+            emit(t + u - D);
+          }
+        }
+        slot = (slot + PF) % RING;
+      }
+      ring_wait<0>();
       if (te == s_end) {  // nothing follows the sequence
 #pragma unroll 1
         for (int m = 1; m <= D; ++m) {
@@ -386,8 +427,9 @@ cudaError_t run(ConvBwdArgs a, cudaStream_t s) {
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, conv_bwd_kernel<T, KT, CK, G128>, CB_THREADS, 0);
   const int64_t tiles = (a.C + CB_THREADS * CB_CH - 1) / (CB_THREADS * CB_CH);
-  // one wave of blocks, with at least 16 tokens in a range (the halo costs up to KT - 1)
-  int64_t ranges = (int64_t)sms * (per_sm > 0 ? per_sm : 1) / tiles;
+  // four waves of blocks: the channels without a norm take less time, and the hardware's dispatch evens
+  // that out; at least 16 tokens in a range (the halo costs up to KT - 1)
+  int64_t ranges = 4 * (int64_t)sms * (per_sm > 0 ? per_sm : 1) / tiles;
   if (ranges > (a.n_tok + 15) / 16) ranges = (a.n_tok + 15) / 16;
   if (ranges > a.max_parts) ranges = a.max_parts;
   if (ranges < 1) ranges = 1;

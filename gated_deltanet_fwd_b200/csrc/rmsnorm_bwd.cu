@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(256) rmsnorm_ckpt8_kernel(
       zr[u].to_float(zv);
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(xv[i], xv[i], ss);
-      uint32_t mx = act8::amax8(xv), mz = act8::amax8(zv);
+      uint32_t mx = act8::amax8(xr[u]), mz = act8::amax8(zr[u]);
 #pragma unroll
       for (int o = TPR / 2; o > 0; o >>= 1) {
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
