@@ -169,9 +169,17 @@ __global__ void __launch_bounds__(CB_THREADS, KT == 8 ? 4 : 8) conv_bwd_kernel(c
   if (r0 < r1) {
     const f32x2 one = two(1.0f, 1.0f), minus = two(-1.0f, -1.0f);
     Four xw[KT], dp[KT];  // x[t - d], dpre[t - d]
-    auto sig = [](f32x2 v) {
-      const float2 f = parts(v);
-      return two(__fdividef(1.0f, 1.0f + __expf(-f.x)), __fdividef(1.0f, 1.0f + __expf(-f.y)));
+    // 1 / (1 + 2^(-v log2 e)); the approximate reciprocal of an overflowed sum is 0
+    const f32x2 neg_log2e = two(-1.4426950408889634f, -1.4426950408889634f);
+    auto sig = [&](f32x2 v) {
+      const float2 f = parts(mul2(v, neg_log2e));
+      float2 e;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(f.x));
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(f.y));
+      e = parts(add2(two(e.x, e.y), one));
+      asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+      asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+      return two(e.x, e.y);
     };
     // the activation of the token whose input came last, and its slope sigma (1 + pre (1 - sigma)) -- as a
     // product: it is 0, not infinity - infinity, far to the left
@@ -301,14 +309,18 @@ __global__ void __launch_bounds__(CB_THREADS, KT == 8 ? 4 : 8) conv_bwd_kernel(c
       };
       unsigned char* rx = ring_x + tid * XS;
       unsigned char* ry = ring_y + tid * YS;
-      auto fetch = [&](int64_t u0, int slot) {  // a batch, as far as it is needed
-        if (on) {
-          const int64_t at = u0 * P.C + c;
+      // copies of the batch whose first element is `at`, as far as its tokens are needed
+      const int64_t row = P.C;
+      auto fetch = [&](int64_t u0, int slot) {
+        const int64_t left = te - u0;
+        if (on && left > 0) {
+          const int64_t at = u0 * row + c;
+          const int m = left < PF ? (int)left : PF;
 #pragma unroll
           for (int u = 0; u < PF; ++u)
-            if (u0 + u < te) {
-              XIn<T, CK>::copy(rx + (slot + u) * CB_THREADS * XS, P, at + (int64_t)u * P.C, u0 + u, xg);
-              ring_copy<YS>(ry + (slot + u) * CB_THREADS * YS, (const T*)P.dy + at + (int64_t)u * P.C);
+            if (u < m) {
+              XIn<T, CK>::copy(rx + (slot + u) * CB_THREADS * XS, P, at + u * row, u0 + u, xg);
+              ring_copy<YS>(ry + (slot + u) * CB_THREADS * YS, (const T*)P.dy + at + u * row);
             }
         }
         ring_commit();
@@ -322,11 +334,27 @@ __global__ void __launch_bounds__(CB_THREADS, KT == 8 ? 4 : 8) conv_bwd_kernel(c
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) fetch(a + k * PF, k * PF);
       int slot = 0;
-#pragma unroll 1
-      for (int64_t t = a; t < te; t += PF) {
+      int64_t t = a;
+      auto slowly = [&]() {  // one batch with every condition
         fetch(t + AHEAD * PF, (slot + AHEAD * PF) % RING);
         ring_wait<AHEAD>();
-        if (t >= a + D && t + PF <= e) {
+#pragma unroll 1
+        for (int u = 0; u < PF && t + u < te; ++u) {
+          token(x_at(slot + u), y_at(slot + u), t + u);
+          if (t + u < e) count();
+          emit(t + u - D);
+        }
+        slot = (slot + PF) % RING;
+        t += PF;
+      };
+      slowly();  // its tokens have nothing to store yet, or history
+      static_assert(D <= PF || KT == 8, "the first batch covers the lag");
+      if (D > PF && t < te) slowly();
+#pragma unroll 1
+      for (; t + PF <= e; t += PF) {
+        fetch(t + AHEAD * PF, (slot + AHEAD * PF) % RING);
+        ring_wait<AHEAD>();
+        {
           T* out = (T*)P.dx + (t - D) * P.C + c;
 #pragma unroll
           for (int u = 0; u < PF; u += 2) {
@@ -380,16 +408,11 @@ __global__ void __launch_bounds__(CB_THREADS, KT == 8 ? 4 : 8) conv_bwd_kernel(c
               }
             }
           }
-        } else {
-#pragma unroll 1
-          for (int u = 0; u < PF && t + u < te; ++u) {
-            token(x_at(slot + u), y_at(slot + u), t + u);
-            if (t + u < e) count();
-            emit(t + u - D);
-          }
         }
         slot = (slot + PF) % RING;
       }
+#pragma unroll 1
+      while (t < te) slowly();
       ring_wait<0>();
       if (te == s_end) {  // nothing follows the sequence
 #pragma unroll 1
