@@ -248,6 +248,7 @@ gdn_status gdn_causal_conv1d_silu_bwd(const void* dy, const void* x, const float
   a.x = x;
   a.xs = x_scales;
   a.xgroup = x_group;
+  a.xgroups = x_scales ? C / x_group : 0;
   a.w = w;
   a.bias = bias;
   a.n_tok = n_tok;

@@ -101,11 +101,11 @@ struct XIn<T, true> {
   static __device__ __forceinline__ void copy(unsigned char* slot, const ConvBwdArgs& P, int64_t at,
                                               int64_t t, int group) {
     ring_copy<4>(slot, (const int8_t*)P.x + at);
-    ring_copy<4>(slot + 4, P.xs + t * (P.C / P.xgroup) + group);
+    ring_copy<4>(slot + 4, P.xs + t * P.xgroups + group);
   }
   __device__ __forceinline__ void load(const ConvBwdArgs& P, int64_t at, int64_t t, int group) {
     u = __ldg(reinterpret_cast<const uint32_t*>((const int8_t*)P.x + at));
-    sc = __ldg(P.xs + t * (P.C / P.xgroup) + group);
+    sc = __ldg(P.xs + t * P.xgroups + group);
   }
   __device__ __forceinline__ Four get() const {
     float f[4];
@@ -151,19 +151,33 @@ __global__ void __launch_bounds__(CB_THREADS, KT == 8 ? 4 : 8) conv_bwd_kernel(c
   auto hist = [&](const float* p) -> Four {
     return {two(__ldg(p), __ldg(p + K - 1)), two(__ldg(p + 2 * (K - 1)), __ldg(p + 3 * (K - 1)))};
   };
+  // up to 32 entries of cu_seqlens are held by the lanes, one each: one load instead of a search
+  const bool held = P.cu && P.N < 32;
+  const int mine = held && lane <= P.N ? P.cu[lane] : 0x7fffffff;
   auto bound = [&](int m, int64_t& b, int64_t& e) {  // sequence m's tokens, clamped to the tensor
-    b = P.cu ? P.cu[m] : (int64_t)m * P.T;
-    e = P.cu ? P.cu[m + 1] : b + P.T;
+    if (held) {
+      b = __shfl_sync(0xffffffffu, mine, m);
+      e = __shfl_sync(0xffffffffu, mine, m + 1);
+    } else {
+      b = P.cu ? P.cu[m] : (int64_t)m * P.T;
+      e = P.cu ? P.cu[m + 1] : b + P.T;
+    }
     b = max((int64_t)0, min(b, P.n_tok));
     e = max(b, min(e, P.n_tok));
   };
-  if (blockIdx.y == 0 && P.dcs_in && on) {  // empty sequences: the history passes through
+  if (blockIdx.y == gridDim.y - 1 && P.dcs_in) {  // empty sequences: the history passes through
     for (int m = 0; m < P.N; ++m) {
       int64_t b, e;
       bound(m, b, e);
-      if (e > b) continue;
+      if (e > b || !on) continue;
       const int64_t at = ((int64_t)m * P.C + c) * (K - 1);
-      for (int q = 0; q < 4 * (K - 1); ++q) P.dcs_in[at + q] = P.dcs_out ? P.dcs_out[at + q] : 0.0f;
+      float v[4 * D];
+#pragma unroll
+      for (int q = 0; q < 4 * D; ++q)
+        v[q] = P.dcs_out && q < 4 * (K - 1) ? __ldg(P.dcs_out + at + q) : 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4 * D; ++q)
+        if (q < 4 * (K - 1)) P.dcs_in[at + q] = v[q];
     }
   }
   if (r0 < r1) {
@@ -256,7 +270,9 @@ __global__ void __launch_bounds__(CB_THREADS, KT == 8 ? 4 : 8) conv_bwd_kernel(c
       }
       return v;
     };
-    int n = seq_of_token(P.cu, P.N, P.T, r0);
+    int n = held ? min(__popc(__ballot_sync(0xffffffffu, (int64_t)mine <= r0)) - 1, P.N - 1)
+                 : seq_of_token(P.cu, P.N, P.T, r0);
+    if (n < 0) n = 0;
     for (; n < P.N; ++n) {
       int64_t s_beg, s_end;
       bound(n, s_beg, s_end);
@@ -451,9 +467,9 @@ cudaError_t run(ConvBwdArgs a, cudaStream_t s) {
   cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, conv_bwd_kernel<T, KT, CK, G128>, CB_THREADS, 0);
   const int64_t tiles = (a.C + CB_THREADS * CB_CH - 1) / (CB_THREADS * CB_CH);
   // four waves of blocks: the channels without a norm take less time, and the hardware's dispatch evens
-  // that out; at least 16 tokens in a range (the halo costs up to KT - 1)
+  // that out; at least 32 tokens in a range (its ends cost about 8 more; 16 and 64 are slower)
   int64_t ranges = 4 * (int64_t)sms * (per_sm > 0 ? per_sm : 1) / tiles;
-  if (ranges > (a.n_tok + 15) / 16) ranges = (a.n_tok + 15) / 16;
+  if (ranges > (a.n_tok + 31) / 32) ranges = (a.n_tok + 31) / 32;
   if (ranges > a.max_parts) ranges = a.max_parts;
   if (ranges < 1) ranges = 1;
   conv_bwd_kernel<T, KT, CK, G128><<<dim3((unsigned)tiles, (unsigned)ranges), CB_THREADS, 0, s>>>(a);

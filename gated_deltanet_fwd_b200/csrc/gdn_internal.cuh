@@ -179,7 +179,7 @@ struct ConvBwdArgs {
   const void* dy;
   const void* x;        // of dtype, or int8 codes when xs is set
   const float* xs;      // [tokens, C / xgroup] or null
-  int xgroup;
+  int xgroup, xgroups;  // channels of a scale, scales of a token
   const float *w, *bias;
   int64_t n_tok, T;
   int C, K, N, n_l2, group;
