@@ -307,26 +307,42 @@ def _kept(x):
 
 def _run(name, device, *args):
     """Calls the entry point on `device` and on torch's current stream there (the last argument)."""
-    with torch.cuda.device(device):
-        stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        _check(name, getattr(load(), name)(*args, stream))
+    if device.index == torch.cuda.current_device():
+        _check(name, getattr(_lib, name)(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(name, getattr(_lib, name)(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _all_cuda(*ts):
     """Contiguous CUDA tensors of one device (None is skipped)."""
-    _cuda(*ts)
-    if len({t.device for t in ts if t is not None}) > 1:
-        raise ValueError("tensors must be on one device")
+    load()
+    dev = -1
+    for t in ts:
+        if t is not None:
+            d = t.get_device() if t.is_cuda else -1
+            if d < 0 or not t.is_contiguous():
+                raise ValueError("tensors must be contiguous CUDA tensors")
+            if d != dev:
+                if dev >= 0:
+                    raise ValueError("tensors must be on one device")
+                dev = d
 
 
 def _same(dtype, *ts):
-    if any(t is not None and t.dtype != dtype for t in ts):
-        raise TypeError(f"expected tensors of {dtype}")
+    for t in ts:
+        if t is not None and t.dtype != dtype:
+            raise TypeError(f"expected tensors of {dtype}")
 
 
 def _shape(shape, *ts):
-    if any(t is not None and tuple(t.shape) != tuple(shape) for t in ts):
-        raise ValueError(f"expected tensors of shape {tuple(shape)}")
+    for t in ts:
+        if t is not None and t.shape != shape:
+            raise ValueError(f"expected tensors of shape {tuple(shape)}")
 
 
 def chunk_bwd_workspace_size(dtype, N, B, T, Hk, Hv, dk, dv, chunk=64):
@@ -369,14 +385,14 @@ def gdn_chunk_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, cu_seq
         output_dinitial_state = initial_state is not None
     if dinitial_state is None and output_dinitial_state:
         dinitial_state = torch.empty((N, Hv, d_v, d_k), dtype=torch.float32, device=q.device)
-    lib, dt = load(), _dt(q)
+    lib, dt = _lib, _dt(q)
     ws, ws_b = _ws(lib.gdn_chunk_bwd_workspace_size(dt, N, B, T, Hk, Hv, d_k, d_v, chunk),
                    workspace, q.device)
     _run("gdn_chunk_bwd", q.device,
-        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(g), _ptr(beta), _ptr(dout), dt,
-        float(d_k ** -0.5 if scale is None else scale), _ptr(initial_state), _ptr(dfinal_state),
-        _ptr(cu_seqlens), N, B, T, Hk, Hv, d_k, d_v, chunk, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
-        _ptr(dbeta), _ptr(dinitial_state), _ptr(ws), ws_b)
+        _adr(q), qs, _adr(k), ks, _adr(v), vs, _adr(g), _adr(beta), _adr(dout), dt,
+        float(d_k ** -0.5 if scale is None else scale), _adr(initial_state), _adr(dfinal_state),
+        _adr(cu_seqlens), N, B, T, Hk, Hv, d_k, d_v, chunk, _adr(dq), _adr(dk), _adr(dv), _adr(dg),
+        _adr(dbeta), _adr(dinitial_state), _adr(ws), ws_b)
     return dq, dk, dv, dg, dbeta, dinitial_state
 
 
@@ -395,11 +411,11 @@ def gdn_gates_bwd(a, b, A_log, dt_bias, dg, dbeta, da=None, db=None, dA_log=None
     db = torch.empty_like(b) if db is None else db
     dA_log = torch.empty_like(A_log) if dA_log is None else dA_log
     ddt_bias = torch.empty_like(dt_bias) if ddt_bias is None else ddt_bias
-    n_tok, lib = a.numel() // Hv, load()
+    n_tok, lib = a.numel() // Hv, _lib
     ws, ws_b = _ws(lib.gdn_gates_bwd_workspace_size(n_tok, Hv), workspace, a.device)
     _run("gdn_gates_bwd", a.device,
-        _ptr(a), _ptr(b), _dt(a), _ptr(A_log), _ptr(dt_bias), _ptr(dg), _ptr(dbeta), n_tok, Hv,
-        _ptr(da), _ptr(db), _ptr(dA_log), _ptr(ddt_bias), _ptr(ws), ws_b)
+        _adr(a), _adr(b), _dt(a), _adr(A_log), _adr(dt_bias), _adr(dg), _adr(dbeta), n_tok, Hv,
+        _adr(da), _adr(db), _adr(dA_log), _adr(ddt_bias), _adr(ws), ws_b)
     return da, db, dA_log, ddt_bias
 
 
@@ -424,11 +440,11 @@ def gdn_gated_rmsnorm_bwd(dy, x, z, w, eps=1e-6, dx=None, dz=None, dw=None, work
     dx = torch.empty_like(dy) if dx is None else dx
     dz = torch.empty_like(dy) if dz is None else dz
     dw = torch.empty_like(w) if dw is None else dw
-    lib = load()
+    lib = _lib
     ws, ws_b = _ws(lib.gdn_gated_rmsnorm_bwd_workspace_size(n_rows, dim), workspace, dy.device)
     _run("gdn_gated_rmsnorm_bwd", dy.device,
-        _ptr(dy), _ptr(x), _ptr(xs), _ptr(z), _ptr(zs), _dt(dy), _ptr(w), float(eps), n_rows, dim,
-        _ptr(dx), _ptr(dz), _ptr(dw), _ptr(ws), ws_b)
+        _adr(dy), _adr(x), _adr(xs), _adr(z), _adr(zs), _dt(dy), _adr(w), float(eps), n_rows, dim,
+        _adr(dx), _adr(dz), _adr(dw), _adr(ws), ws_b)
     return dx, dz, dw
 
 
@@ -464,12 +480,12 @@ def gdn_causal_conv1d_silu_bwd(dy, x, w, bias=None, cu_seqlens=None, n_l2norm_ch
     dbias = torch.empty_like(bias) if dbias is None and bias is not None else dbias
     if dconv_state_in is None and conv_state_in is not None:
         dconv_state_in = torch.empty_like(conv_state_in)
-    lib = load()
+    lib = _lib
     ws, ws_b = _ws(lib.gdn_causal_conv1d_silu_bwd_workspace_size(B, T, C, K), workspace, dy.device)
     _run("gdn_causal_conv1d_silu_bwd", dy.device,
-        _ptr(dy), _ptr(x), _ptr(xs), group, _dt(dy), _ptr(w), _ptr(bias), B, T, C, K,
-        _ptr(cu_seqlens), N, n_l2norm_ch, l2norm_group, float(l2_eps), _ptr(conv_state_in),
-        _ptr(dconv_state_out), _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dconv_state_in), _ptr(ws),
+        _adr(dy), _adr(x), _adr(xs), group, _dt(dy), _adr(w), _adr(bias), B, T, C, K,
+        _adr(cu_seqlens), N, n_l2norm_ch, l2norm_group, float(l2_eps), _adr(conv_state_in),
+        _adr(dconv_state_out), _adr(dx), _adr(dw), _adr(dbias), _adr(dconv_state_in), _adr(ws),
         ws_b)
     return dx, dw, dbias, dconv_state_in
 
@@ -489,8 +505,8 @@ def gdn_act_pack8(x, group=128, codes=None, scales=None):
     _shape((*x.shape[:-1], dim // group), scales)
     _same(torch.int8, codes)
     _same(torch.float32, scales)
-    _run("gdn_act_pack8", x.device, _ptr(x), _dt(x), x.numel() // dim, dim, group, _ptr(codes),
-         _ptr(scales))
+    _run("gdn_act_pack8", x.device, _adr(x), _dt(x), x.numel() // dim, dim, group, _adr(codes),
+         _adr(scales))
     return codes, scales
 
 
@@ -505,8 +521,8 @@ def gdn_act_unpack8(codes, scales, dtype=torch.bfloat16, x=None):
     x = torch.empty(codes.shape, dtype=dtype, device=codes.device) if x is None else x
     _shape(codes.shape, x)
     _run("gdn_act_unpack8", codes.device,
-        _ptr(codes), _ptr(scales), _dt(x), codes.numel() // dim, dim, dim // scales.shape[-1],
-        _ptr(x))
+        _adr(codes), _adr(scales), _dt(x), codes.numel() // dim, dim, dim // scales.shape[-1],
+        _adr(x))
     return x
 
 
@@ -526,6 +542,6 @@ def gdn_gated_rmsnorm_ckpt8(x, z, w, eps=1e-6, y=None):
     xc, zc = new(x.shape, torch.int8), new(x.shape, torch.int8)
     xs, zs = new((*x.shape[:-1], 1), torch.float32), new((*x.shape[:-1], 1), torch.float32)
     _run("gdn_gated_rmsnorm_ckpt8", x.device,
-        _ptr(x), _ptr(z), _dt(x), _ptr(w), float(eps), x.numel() // dim, dim, _ptr(y), _ptr(xc),
-        _ptr(xs), _ptr(zc), _ptr(zs))
+        _adr(x), _adr(z), _dt(x), _adr(w), float(eps), x.numel() // dim, dim, _adr(y), _adr(xc),
+        _adr(xs), _adr(zc), _adr(zs))
     return y, (xc, xs), (zc, zs)
