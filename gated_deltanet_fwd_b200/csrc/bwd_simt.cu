@@ -21,13 +21,14 @@
 // below 2^-30 is replaced by +-2^-30 in T' so that the quotient exists (U, dW and all that follows
 // move by less than 2^-30 of a beta = 1 token; dV is rescaled, so it is exactly 0 for beta = 0).
 //
-// Four kernels.  gprep, parallel over (chunk, k-head): T' and P to the workspace.  gfwd, one block per
-// (sequence, v-head, 16 value rows), walks the chunks forward: entering states S0 and U.  gbwd walks
-// them backward: dS and dW.  (Value rows are independent in both walks, so the serial part is split over
-// them.)  ggrad, parallel over (chunk, k-head): everything else; the v-heads that share the k-head are
-// summed in registers in head order, so dq and dk do not depend on scheduling.  Cumulative log-decays
-// are kept in 64 bits: their differences lose half the digits of an fp32 sum once |gamma| is in the
-// hundreds.
+// Three kernels.  gprep, parallel over (chunk, k-head): T', P and the decay factors to the workspace.
+// gwalk, one block per (sequence, v-head, 16 value rows) and direction: forward it leaves the entering
+// states S0 and U, backward dS and dW.  (Neither walk needs the other, and value rows are independent in
+// both, so the serial part is split over them.)  ggrad, parallel over (chunk, k-head): everything else; the
+// v-heads that share the k-head are summed in registers in head order, so dq and dk do not depend on
+// scheduling.  Cumulative log-decays are kept in 64 bits: their differences lose half the digits of an
+// fp32 sum once |gamma| is in the hundreds.  The walks are bound by the latency of a chunk's few small
+// products and barriers.
 #include "bwd_internal.cuh"
 
 namespace gdn {
@@ -44,6 +45,7 @@ struct SimtWs {
   float* dS;   // [dv][dk] gradient of the state leaving it
   float* U;    // [C][dv]
   float* dW;   // [C][dv]
+  float* rec;  // [5][C]: Gamma, d, beta (floored), gamma (64-bit, two places)
 };
 
 __host__ __device__ inline SimtWs simt_ws(void* ws, int64_t slots, int Hv, int dk, int dv, int C) {
@@ -54,6 +56,7 @@ __host__ __device__ inline SimtWs simt_ws(void* ws, int64_t slots, int Hv, int d
   w.dS = w.S + n * dv * dk;
   w.U = w.dS + n * dv * dk;
   w.dW = w.U + n * C * dv;
+  w.rec = w.dW + n * C * dv;
   return w;
 }
 
@@ -71,18 +74,33 @@ struct SimtArgs {
   int* status;
 };
 
-// this chunk's gates of one v-head: gam (64-bit cumulative log-decay), bet (as used in T')
-__device__ __forceinline__ void load_gates(const SimtArgs& P, int64_t t0, int L, int h, double* gam,
-                                           float* bet) {
-  if (threadIdx.x == 0) {
-    double acc = 0.0;
-    for (int r = 0; r < P.C; ++r) {
-      if (r < L) acc += (double)P.g[(t0 + r) * P.Hv + h];
-      gam[r] = acc;  // constant behind the end
+// This chunk's gates of one v-head, by one warp per call site: gam (64-bit cumulative log-decay, constant
+// behind the end) and bet (as used in T').  C <= 64: lanes hold tokens lane and 32 + lane.
+__device__ __forceinline__ void scan_gates(const SimtArgs& P, int64_t t0, int L, int h, int lane,
+                                           double* gam, float* bet) {
+  double x[2];
+  float b[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 32 * i + lane;
+    x[i] = r < L ? (double)P.g[(t0 + r) * P.Hv + h] : 0.0;
+    b[i] = r < L ? floor_beta(P.beta[(t0 + r) * P.Hv + h]) : 0.0f;
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y0 = __shfl_up_sync(0xffffffffu, x[0], o), y1 = __shfl_up_sync(0xffffffffu, x[1], o);
+    if (lane >= o) {
+      x[0] += y0;
+      x[1] += y1;
     }
   }
-  for (int r = threadIdx.x; r < P.C; r += THREADS)
-    bet[r] = r < L ? floor_beta(P.beta[(t0 + r) * P.Hv + h]) : 0.0f;
+  x[1] += __shfl_sync(0xffffffffu, x[0], 31);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (32 * i + lane < P.C) {
+      gam[32 * i + lane] = x[i];
+      bet[32 * i + lane] = b[i];
+    }
 }
 
 // rows [t0, t0 + L) of a token tensor into smem [C][ld], zeros behind
@@ -153,9 +171,16 @@ __global__ void __launch_bounds__(THREADS) gprep_kernel(const SimtArgs P) {
   for (int gi = 0; gi < G; ++gi) {
     const int h = hk * G + gi;
     __syncthreads();
-    load_gates(P, ch.t0, ch.L, h, gam, bet);
+    if (tid < 32) scan_gates(P, ch.t0, ch.L, h, tid, gam, bet);
     __syncthreads();
     float* tp = w.tp + (slot * P.Hv + h) * 2 * C * C;
+    float* rec = w.rec + (slot * P.Hv + h) * 5 * C;
+    if (tid < C) {
+      rec[tid] = expf((float)gam[tid]);
+      rec[C + tid] = expf((float)(gam[C - 1] - gam[tid]));
+      rec[2 * C + tid] = bet[tid];
+      reinterpret_cast<double*>(rec + 3 * C)[tid] = gam[tid];
+    }
     for (int e = tid; e < C * C; e += THREADS) {
       const int r = e / C, s = e - r * C;
       const float ex = s <= r ? expf((float)(gam[r] - gam[s])) : 0.0f;
@@ -191,18 +216,18 @@ __global__ void __launch_bounds__(THREADS) gprep_kernel(const SimtArgs P) {
   }
 }
 
-// ------------------------------------------------------------------------ gfwd / gbwd ------
-// Block = (sequence, v-head, 16 value rows).
+// ------------------------------------------------------------------------------- gwalk -----
+// Block = (sequence, v-head, 16 value rows, direction).
 struct Walk {
   int n, h, hk, j0;
   int64_t s_beg, s_end, slot0, nch;
 };
 
 __device__ __forceinline__ bool walk_of(const SimtArgs& P, Walk& W) {
-  const int slices = P.dv / DVS;
-  W.j0 = (blockIdx.x % slices) * DVS;
-  W.h = (blockIdx.x / slices) % P.Hv;
-  W.n = blockIdx.x / (slices * P.Hv);
+  const int slices = P.dv / DVS, unit = blockIdx.x >> 1;
+  W.j0 = (unit % slices) * DVS;
+  W.h = (unit / slices) % P.Hv;
+  W.n = unit / (slices * P.Hv);
   W.hk = W.h / (P.Hv / P.Hk);
   if (!seq_range(P.cu, P.T, W.n, P.C, W.s_beg, W.s_end, W.slot0)) {
     if (threadIdx.x == 0) report(P.status, GDN_ERR_DEVICE_ARG);
@@ -213,8 +238,7 @@ __device__ __forceinline__ bool walk_of(const SimtArgs& P, Walk& W) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(THREADS) gfwd_kernel(const SimtArgs P) {
-  extern __shared__ __align__(16) float sm[];
+__device__ __forceinline__ void walk_forward(const SimtArgs& P, const Walk& W, float* sm) {
   const int C = P.C, ldk = P.dk + 4, ldc = C + 4, tid = threadIdx.x;
   float* Ss = sm;                 // [DVS][ldk]
   float* Ks = Ss + DVS * ldk;     // [C][ldk]
@@ -223,10 +247,6 @@ __global__ void __launch_bounds__(THREADS) gfwd_kernel(const SimtArgs P) {
   float* Us = Ws + C * DVS;       // [C][DVS]
   float* Gm = Us + C * DVS;
   float* dd = Gm + C;
-  float* bet = dd + C;
-  double* gam = reinterpret_cast<double*>(bet + C);
-  Walk W;
-  if (!walk_of(P, W)) return;
   const SimtWs w = simt_ws(P.ws, P.slots, P.Hv, P.dk, P.dv, C);
   const int64_t sbase = ((int64_t)W.n * P.Hv + W.h) * P.dv * P.dk + (int64_t)W.j0 * P.dk;
   for (int e = tid; e < DVS * P.dk; e += THREADS)
@@ -236,17 +256,12 @@ __global__ void __launch_bounds__(THREADS) gfwd_kernel(const SimtArgs P) {
     const int64_t t0 = W.s_beg + c * C, sh = (W.slot0 + c) * P.Hv + W.h;
     const int L = (int)min((int64_t)C, W.s_end - t0);
     __syncthreads();
-    load_gates(P, t0, L, W.h, gam, bet);
+    if (tid < 2 * C) Gm[tid] = w.rec[sh * 5 * C + tid];  // Gamma, d
     load_rows((const T*)P.k + W.hk * P.dk, P.ts.k, t0, L, C, P.dk, Ks, ldk);
     load_rows_f(w.tp + sh * 2 * C * C, C, C, Ts, ldc);
     load_rows((const T*)P.v + W.h * P.dv + W.j0, P.ts.v, t0, L, C, DVS, Ws, DVS);
     float* So = w.S + sh * P.dv * P.dk + W.j0 * P.dk;
     for (int e = tid; e < DVS * P.dk; e += THREADS) So[e] = Ss[(e / P.dk) * ldk + e % P.dk];
-    __syncthreads();
-    if (tid < C) {
-      Gm[tid] = expf((float)gam[tid]);
-      dd[tid] = expf((float)(gam[C - 1] - gam[tid]));
-    }
     __syncthreads();
     const int j = tid % DVS;
     for (int r = tid / DVS; r < C; r += THREADS / DVS) {  // W = V - Gamma K S^T
@@ -283,8 +298,7 @@ __global__ void __launch_bounds__(THREADS) gfwd_kernel(const SimtArgs P) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(THREADS) gbwd_kernel(const SimtArgs P) {
-  extern __shared__ __align__(16) float sm[];
+__device__ __forceinline__ void walk_backward(const SimtArgs& P, const Walk& W, float* sm) {
   const int C = P.C, ldk = P.dk + 4, ldc = C + 4, tid = threadIdx.x;
   float* Ss = sm;              // [DVS][ldk] dS
   float* Ks = Ss + DVS * ldk;  // [C][ldk]
@@ -296,10 +310,6 @@ __global__ void __launch_bounds__(THREADS) gbwd_kernel(const SimtArgs P) {
   float* Ws = Us + C * DVS;    // [C][DVS] Gamma dW
   float* Gm = Ws + C * DVS;
   float* dd = Gm + C;
-  float* bet = dd + C;
-  double* gam = reinterpret_cast<double*>(bet + C);
-  Walk W;
-  if (!walk_of(P, W)) return;
   const SimtWs w = simt_ws(P.ws, P.slots, P.Hv, P.dk, P.dv, C);
   const int64_t sbase = ((int64_t)W.n * P.Hv + W.h) * P.dv * P.dk + (int64_t)W.j0 * P.dk;
   for (int e = tid; e < DVS * P.dk; e += THREADS)
@@ -309,7 +319,7 @@ __global__ void __launch_bounds__(THREADS) gbwd_kernel(const SimtArgs P) {
     const int64_t t0 = W.s_beg + c * C, sh = (W.slot0 + c) * P.Hv + W.h;
     const int L = (int)min((int64_t)C, W.s_end - t0);
     __syncthreads();
-    load_gates(P, t0, L, W.h, gam, bet);
+    if (tid < 2 * C) Gm[tid] = w.rec[sh * 5 * C + tid];  // Gamma, d
     load_rows((const T*)P.k + W.hk * P.dk, P.ts.k, t0, L, C, P.dk, Ks, ldk);
     load_rows((const T*)P.q + W.hk * P.dk, P.ts.q, t0, L, C, P.dk, Qs, ldk);
     load_rows_f(w.tp + sh * 2 * C * C, C, C, Ts, ldc);
@@ -318,11 +328,6 @@ __global__ void __launch_bounds__(THREADS) gbwd_kernel(const SimtArgs P) {
               P.scale);
     float* So = w.dS + sh * P.dv * P.dk + W.j0 * P.dk;
     for (int e = tid; e < DVS * P.dk; e += THREADS) So[e] = Ss[(e / P.dk) * ldk + e % P.dk];
-    __syncthreads();
-    if (tid < C) {
-      Gm[tid] = expf((float)gam[tid]);
-      dd[tid] = expf((float)(gam[C - 1] - gam[tid]));
-    }
     __syncthreads();
     const int j = tid % DVS;
     for (int s = tid / DVS; s < C; s += THREADS / DVS) {  // dU = P^T dO' + d K dS^T
@@ -341,9 +346,10 @@ __global__ void __launch_bounds__(THREADS) gbwd_kernel(const SimtArgs P) {
       Ws[s * DVS + j] = Gm[s] * acc;
       w.dW[sh * C * P.dv + s * P.dv + W.j0 + j] = acc;
       if (s < L) {
-        const float b = P.beta[(t0 + s) * P.Hv + W.h];
-        ((T*)P.dv_)[((t0 + s) * P.Hv + W.h) * P.dv + W.j0 + j] =
-            from_f<T>(b == bet[s] ? acc : acc * (b / bet[s]));
+        const float bf = w.rec[sh * 5 * C + 2 * C + s];
+        float out = acc;
+        if (fabsf(bf) == kBetaFloor) out *= P.beta[(t0 + s) * P.Hv + W.h] / bf;  // T' used the floor
+        ((T*)P.dv_)[((t0 + s) * P.Hv + W.h) * P.dv + W.j0 + j] = from_f<T>(out);
       }
     }
     __syncthreads();
@@ -368,6 +374,17 @@ __global__ void __launch_bounds__(THREADS) gbwd_kernel(const SimtArgs P) {
   if (P.dS0)
     for (int e = tid; e < DVS * P.dk; e += THREADS)
       P.dS0[sbase + e] = Ss[(e / P.dk) * ldk + e % P.dk];
+}
+
+template <typename T>
+__global__ void __launch_bounds__(THREADS) gwalk_kernel(const SimtArgs P) {
+  extern __shared__ __align__(16) float sm[];
+  Walk W;
+  if (!walk_of(P, W)) return;
+  if (blockIdx.x & 1)
+    walk_forward<T>(P, W, sm);
+  else
+    walk_backward<T>(P, W, sm);
 }
 
 // ------------------------------------------------------------------------------- ggrad -----
@@ -410,15 +427,12 @@ __global__ void __launch_bounds__(THREADS) ggrad_kernel(const SimtArgs P) {
     const float* S = w.S + sh * P.dv * P.dk;
     const float* dS = w.dS + sh * P.dv * P.dk;
     __syncthreads();
-    load_gates(P, t0, L, h, gam, bet);
+    for (int e = tid; e < 3 * C; e += THREADS) Gm[e] = w.rec[sh * 5 * C + e];  // Gamma, d, beta
+    if (tid < C) gam[tid] = reinterpret_cast<const double*>(w.rec + sh * 5 * C + 3 * C)[tid];
     load_rows_f(w.U + sh * C * P.dv, C, P.dv, Us, ldv);
     load_rows_f(w.dW + sh * C * P.dv, C, P.dv, Ws, ldv);
     load_rows((const T*)P.dout + h * P.dv, (int64_t)P.Hv * P.dv, t0, L, C, P.dv, Os, ldv, P.scale);
     __syncthreads();
-    if (tid < C) {
-      Gm[tid] = expf((float)gam[tid]);
-      dd[tid] = expf((float)(gam[C - 1] - gam[tid]));
-    }
     float frob = 0.0f;
     for (int e = tid; e < P.dv * P.dk; e += THREADS) frob = fmaf(S[e], dS[e], frob);
 #pragma unroll
@@ -573,26 +587,21 @@ cudaError_t launch_t(const SimtArgs& P, cudaStream_t s) {
   const int C = P.C, ldk = P.dk + 4, ldv = P.dv + 4, ldc = C + 4;
   const size_t f = sizeof(float);
   const size_t sm_prep = (2 * (size_t)C * ldk + 4 * C * ldc + C) * f + C * 8;
-  const size_t sm_fwd = ((size_t)(DVS + C) * ldk + C * ldc + 2 * C * DVS + 3 * C) * f + C * 8;
-  const size_t sm_bwd =
-      ((size_t)(DVS + 2 * C) * ldk + 2 * C * ldc + 3 * C * DVS + 3 * C) * f + C * 8;
+  const size_t sm_walk =  // the backward walk's; the forward one needs less
+      ((size_t)(DVS + 2 * C) * ldk + 2 * C * ldc + 3 * C * DVS + 2 * C) * f;
   const size_t sm_grad =
       (2 * (size_t)C * ldk + 3 * C * ldv + 2 * C * ldc + 6 * C + 8) * f + C * 8;
   auto set = [](auto kern, size_t bytes) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   };
   cudaError_t e = set(gprep_kernel<T>, sm_prep);
-  if (e == cudaSuccess) e = set(gfwd_kernel<T>, sm_fwd);
-  if (e == cudaSuccess) e = set(gbwd_kernel<T>, sm_bwd);
+  if (e == cudaSuccess) e = set(gwalk_kernel<T>, sm_walk);
   if (e == cudaSuccess) e = set(ggrad_kernel<T>, sm_grad);
   if (e != cudaSuccess) return e;
-  const int64_t par = P.slots * P.Hk, walks = (int64_t)P.N * P.Hv * (P.dv / DVS);
+  const int64_t par = P.slots * P.Hk, walks = 2 * (int64_t)P.N * P.Hv * (P.dv / DVS);
   if (par > 0x7fffffff || walks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if (par > 0) {
-    gprep_kernel<T><<<(unsigned)par, THREADS, sm_prep, s>>>(P);
-    gfwd_kernel<T><<<(unsigned)walks, THREADS, sm_fwd, s>>>(P);
-  }
-  if (walks > 0) gbwd_kernel<T><<<(unsigned)walks, THREADS, sm_bwd, s>>>(P);
+  if (par > 0) gprep_kernel<T><<<(unsigned)par, THREADS, sm_prep, s>>>(P);
+  if (walks > 0) gwalk_kernel<T><<<(unsigned)walks, THREADS, sm_walk, s>>>(P);
   if (par > 0) ggrad_kernel<T><<<(unsigned)par, THREADS, sm_grad, s>>>(P);
   return cudaGetLastError();
 }
@@ -601,7 +610,8 @@ cudaError_t launch_t(const SimtArgs& P, cudaStream_t s) {
 
 size_t simt_workspace_bytes(int N, int64_t n_tok, int Hv, int dk, int dv, int C) {
   const size_t n = (size_t)max_slots(N, n_tok, C) * Hv;
-  return HEADER + n * (2 * (size_t)C * C + 2 * (size_t)dv * dk + 2 * (size_t)C * dv) * sizeof(float);
+  return HEADER +
+         n * (2 * (size_t)C * C + 2 * (size_t)dv * dk + 2 * (size_t)C * dv + 5 * (size_t)C) * sizeof(float);
 }
 
 cudaError_t launch_simt(const Args& a, cudaStream_t s) {
