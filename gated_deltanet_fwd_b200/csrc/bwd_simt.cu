@@ -126,17 +126,19 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float acc) {
 }
 
 // ------------------------------------------------------------------------------- gprep -----
-template <typename T>
+// Thread tile of the C x C products: TS x TS entries, 16 x 16 threads.
+template <typename T, int C>
 __global__ void __launch_bounds__(THREADS) gprep_kernel(const SimtArgs P) {
   extern __shared__ __align__(16) float sm[];
-  const int C = P.C, ldk = P.dk + 4, ldc = C + 4;
+  constexpr int ldc = C + 4, TS = C / 16, RG = C / 4;
+  const int ldk = P.dk + 4;
   float* Ks = sm;
   float* Qs = Ks + C * ldk;
   float* KK = Qs + C * ldk;
   float* QK = KK + C * ldc;
-  float* A = QK + C * ldc;
-  float* Ti = A + C * ldc;
-  float* bet = Ti + C * ldc;
+  float* At = QK + C * ldc;      // A transposed
+  float* line = At + C * ldc;    // [2][C]
+  float* bet = line + 2 * C;
   double* gam = reinterpret_cast<double*>(bet + C);
   Chunk ch;
   const int64_t slot = blockIdx.x / P.Hk;
@@ -147,24 +149,32 @@ __global__ void __launch_bounds__(THREADS) gprep_kernel(const SimtArgs P) {
   load_rows((const T*)P.q + hk * P.dk, P.ts.q, ch.t0, ch.L, C, P.dk, Qs, ldk);
   __syncthreads();
   const int tid = threadIdx.x;
-  for (int e = tid; e < C * C / 4; e += THREADS) {  // 1 row x 4 columns
-    const int r = e / (C / 4), s = 4 * (e % (C / 4));
-    if (s > r) continue;
-    float a[4] = {}, b[4] = {};
-    for (int i = 0; i < P.dk; i += 4) {
-      const float4 kr = *reinterpret_cast<const float4*>(Ks + r * ldk + i);
-      const float4 qr = *reinterpret_cast<const float4*>(Qs + r * ldk + i);
+  {
+    const int rb = TS * (tid / 16), sb = TS * (tid % 16);
+    if (sb <= rb) {
+      float a[TS][TS] = {}, b[TS][TS] = {};
+      for (int i = 0; i < P.dk; i += 4) {
+        float4 ks[TS];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float4 ks = *reinterpret_cast<const float4*>(Ks + (s + x) * ldk + i);
-        a[x] = dot4(kr, ks, a[x]);
-        b[x] = dot4(qr, ks, b[x]);
+        for (int y = 0; y < TS; ++y) ks[y] = *reinterpret_cast<const float4*>(Ks + (sb + y) * ldk + i);
+#pragma unroll
+        for (int x = 0; x < TS; ++x) {
+          const float4 kr = *reinterpret_cast<const float4*>(Ks + (rb + x) * ldk + i);
+          const float4 qr = *reinterpret_cast<const float4*>(Qs + (rb + x) * ldk + i);
+#pragma unroll
+          for (int y = 0; y < TS; ++y) {
+            a[x][y] = dot4(kr, ks[y], a[x][y]);
+            b[x][y] = dot4(qr, ks[y], b[x][y]);
+          }
+        }
       }
-    }
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      KK[r * ldc + s + x] = a[x];
-      QK[r * ldc + s + x] = b[x];
+      for (int x = 0; x < TS; ++x)
+#pragma unroll
+        for (int y = 0; y < TS; ++y) {
+          KK[(rb + x) * ldc + sb + y] = a[x][y];
+          QK[(rb + x) * ldc + sb + y] = b[x][y];
+        }
     }
   }
   const int G = P.Hv / P.Hk;
@@ -182,37 +192,42 @@ __global__ void __launch_bounds__(THREADS) gprep_kernel(const SimtArgs P) {
       reinterpret_cast<double*>(rec + 3 * C)[tid] = gam[tid];
     }
     for (int e = tid; e < C * C; e += THREADS) {
-      const int r = e / C, s = e - r * C;
+      const int r = e / C, s = e % C;
       const float ex = s <= r ? expf((float)(gam[r] - gam[s])) : 0.0f;
-      A[r * ldc + s] = s < r ? bet[r] * ex * KK[r * ldc + s] : 0.0f;
+      At[s * ldc + r] = s < r ? bet[r] * ex * KK[r * ldc + s] : 0.0f;
       tp[C * C + e] = s <= r ? ex * QK[r * ldc + s] : 0.0f;
     }
     __syncthreads();
-    // T = (I + A)^{-1}, one column per thread by forward substitution
-    if (tid < C) {
-      const int c = tid;
-      for (int r = 0; r < C; ++r) {
-        float x = r == c ? 1.0f : 0.0f;
-        if (r > c) {
-          float x1 = 0.0f, x2 = 0.0f, x3 = 0.0f;
-          int s = c;
-          for (; s + 3 < r; s += 4) {
-            x = fmaf(-A[r * ldc + s], Ti[s * ldc + c], x);
-            x1 = fmaf(-A[r * ldc + s + 1], Ti[(s + 1) * ldc + c], x1);
-            x2 = fmaf(-A[r * ldc + s + 2], Ti[(s + 2) * ldc + c], x2);
-            x3 = fmaf(-A[r * ldc + s + 3], Ti[(s + 3) * ldc + c], x3);
+    // T = (I + A)^{-1} by right-looking substitution: a thread holds C / 4 consecutive rows of one column;
+    // row s, once final, is handed to everybody and taken off the later rows
+    const int g = tid / 64, c = tid % 64;
+    const bool on = c < C;
+    float x[RG];
+#pragma unroll
+    for (int q = 0; q < RG; ++q) x[q] = g * RG + q == c ? 1.0f : 0.0f;
+    for (int og = 0; og < 4; ++og) {
+#pragma unroll
+      for (int q = 0; q < RG; ++q) {
+        const int s = og * RG + q;
+        float* ln = line + (s & 1) * C;
+        if (g == og && on) ln[c] = x[q];
+        __syncthreads();
+        if (on && g >= og) {
+          const float t = ln[c];
+#pragma unroll
+          for (int k = 0; k < RG; k += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(At + s * ldc + g * RG + k);
+            x[k] = fmaf(-a.x, t, x[k]);  // A is zero on and above the diagonal
+            x[k + 1] = fmaf(-a.y, t, x[k + 1]);
+            x[k + 2] = fmaf(-a.z, t, x[k + 2]);
+            x[k + 3] = fmaf(-a.w, t, x[k + 3]);
           }
-          for (; s < r; ++s) x = fmaf(-A[r * ldc + s], Ti[s * ldc + c], x);
-          x += (x1 + x2) + x3;
         }
-        Ti[r * ldc + c] = x;
       }
     }
-    __syncthreads();
-    for (int e = tid; e < C * C; e += THREADS) {
-      const int r = e / C, s = e - r * C;
-      tp[e] = s <= r ? Ti[r * ldc + s] * bet[s] : 0.0f;
-    }
+    if (on)
+#pragma unroll
+      for (int q = 0; q < RG; ++q) tp[(g * RG + q) * C + c] = c <= g * RG + q ? x[q] * bet[c] : 0.0f;
   }
 }
 
@@ -237,9 +252,51 @@ __device__ __forceinline__ bool walk_of(const SimtArgs& P, Walk& W) {
   return true;
 }
 
-template <typename T>
+// Thread (j = tid % 16, rg = tid / 16) holds rows rg, rg + 16, .. of one value column j.
+// acc[m] += sum_i A[rg + 16 m][i] B[i] over rows of A in shared memory (float4 steps)
+template <int R>
+__device__ __forceinline__ void rows_dot(const float* A, int lda, const float* b, int n, int rg,
+                                         float (&acc)[R]) {
+#pragma unroll 4
+  for (int i = 0; i < n; i += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(b + i);
+#pragma unroll
+    for (int m = 0; m < R; ++m)
+      acc[m] = dot4(*reinterpret_cast<const float4*>(A + (rg + 16 * m) * lda + i), v, acc[m]);
+  }
+}
+// acc[m] += sum_s A[rg + 16 m][s] B[s][j]
+template <int R, int C>
+__device__ __forceinline__ void rows_mul(const float* A, const float* B, int rg, int j,
+                                         float (&acc)[R]) {
+#pragma unroll 4
+  for (int s = 0; s < C; s += 4) {
+    float b[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) b[q] = B[(s + q) * DVS + j];
+#pragma unroll
+    for (int m = 0; m < R; ++m) {
+      const float4 a = *reinterpret_cast<const float4*>(A + (rg + 16 * m) * (C + 4) + s);
+      acc[m] = fmaf(a.x, b[0], fmaf(a.y, b[1], fmaf(a.z, b[2], fmaf(a.w, b[3], acc[m]))));
+    }
+  }
+}
+// acc[m] += sum_r A[r][rg + 16 m] B[r][j]
+template <int R, int C>
+__device__ __forceinline__ void cols_mul(const float* A, const float* B, int rg, int j,
+                                         float (&acc)[R]) {
+#pragma unroll 8
+  for (int r = 0; r < C; ++r) {
+    const float b = B[r * DVS + j];
+#pragma unroll
+    for (int m = 0; m < R; ++m) acc[m] = fmaf(A[r * (C + 4) + rg + 16 * m], b, acc[m]);
+  }
+}
+
+template <typename T, int C>
 __device__ __forceinline__ void walk_forward(const SimtArgs& P, const Walk& W, float* sm) {
-  const int C = P.C, ldk = P.dk + 4, ldc = C + 4, tid = threadIdx.x;
+  constexpr int ldc = C + 4, R = C / 16;
+  const int ldk = P.dk + 4, tid = threadIdx.x;
   float* Ss = sm;                 // [DVS][ldk]
   float* Ks = Ss + DVS * ldk;     // [C][ldk]
   float* Ts = Ks + C * ldk;       // [C][ldc]
@@ -249,9 +306,12 @@ __device__ __forceinline__ void walk_forward(const SimtArgs& P, const Walk& W, f
   float* dd = Gm + C;
   const SimtWs w = simt_ws(P.ws, P.slots, P.Hv, P.dk, P.dv, C);
   const int64_t sbase = ((int64_t)W.n * P.Hv + W.h) * P.dv * P.dk + (int64_t)W.j0 * P.dk;
-  for (int e = tid; e < DVS * P.dk; e += THREADS)
-    Ss[(e / P.dk) * ldk + e % P.dk] = P.S0 ? P.S0[sbase + e] : 0.0f;
-  const int w4 = P.dk / 4, jst = THREADS / w4;
+  const int w4 = P.dk / 4, jst = THREADS / w4, sj = tid / w4, si = 4 * (tid - sj * w4);
+  const int j = tid % DVS, rg = tid / DVS;
+  for (int jj = sj; sj < jst && jj < DVS; jj += jst)
+    *reinterpret_cast<float4*>(Ss + jj * ldk + si) =
+        P.S0 ? *reinterpret_cast<const float4*>(P.S0 + sbase + jj * P.dk + si)
+             : make_float4(0.f, 0.f, 0.f, 0.f);
   for (int64_t c = 0; c < W.nch; ++c) {
     const int64_t t0 = W.s_beg + c * C, sh = (W.slot0 + c) * P.Hv + W.h;
     const int L = (int)min((int64_t)C, W.s_end - t0);
@@ -261,45 +321,47 @@ __device__ __forceinline__ void walk_forward(const SimtArgs& P, const Walk& W, f
     load_rows_f(w.tp + sh * 2 * C * C, C, C, Ts, ldc);
     load_rows((const T*)P.v + W.h * P.dv + W.j0, P.ts.v, t0, L, C, DVS, Ws, DVS);
     float* So = w.S + sh * P.dv * P.dk + W.j0 * P.dk;
-    for (int e = tid; e < DVS * P.dk; e += THREADS) So[e] = Ss[(e / P.dk) * ldk + e % P.dk];
+    for (int jj = sj; sj < jst && jj < DVS; jj += jst)
+      *reinterpret_cast<float4*>(So + jj * P.dk + si) = *reinterpret_cast<float4*>(Ss + jj * ldk + si);
     __syncthreads();
-    const int j = tid % DVS;
-    for (int r = tid / DVS; r < C; r += THREADS / DVS) {  // W = V - Gamma K S^T
-      float acc = 0.0f;
-      for (int i = 0; i < P.dk; i += 4)
-        acc = dot4(*reinterpret_cast<const float4*>(Ks + r * ldk + i),
-                   *reinterpret_cast<const float4*>(Ss + j * ldk + i), acc);
-      Ws[r * DVS + j] -= Gm[r] * acc;
+    {  // W = V - Gamma K S^T
+      float acc[R] = {};
+      rows_dot<R>(Ks, ldk, Ss + j * ldk, P.dk, rg, acc);
+#pragma unroll
+      for (int m = 0; m < R; ++m) Ws[(rg + 16 * m) * DVS + j] -= Gm[rg + 16 * m] * acc[m];
     }
     __syncthreads();
-    for (int r = tid / DVS; r < C; r += THREADS / DVS) {  // U = T' W
-      float acc = 0.0f;
-      for (int s = 0; s <= r; ++s) acc = fmaf(Ts[r * ldc + s], Ws[s * DVS + j], acc);
-      Us[r * DVS + j] = acc * dd[r];
-      w.U[sh * C * P.dv + r * P.dv + W.j0 + j] = acc;
+    {  // U = T' W
+      float acc[R] = {};
+      rows_mul<R, C>(Ts, Ws, rg, j, acc);
+#pragma unroll
+      for (int m = 0; m < R; ++m) {
+        const int r = rg + 16 * m;
+        Us[r * DVS + j] = acc[m] * dd[r];
+        w.U[sh * C * P.dv + r * P.dv + W.j0 + j] = acc[m];
+      }
     }
     __syncthreads();
     const float gl = Gm[C - 1];
-    if (tid < jst * w4) {
-      const int i = 4 * (tid % w4);
-      for (int jj = tid / w4; jj < DVS; jj += jst) {
-        float4 a = *reinterpret_cast<float4*>(Ss + jj * ldk + i);
-        a.x *= gl; a.y *= gl; a.z *= gl; a.w *= gl;
-        for (int s = 0; s < C; ++s) {
-          const float u = Us[s * DVS + jj];
-          const float4 kv = *reinterpret_cast<const float4*>(Ks + s * ldk + i);
-          a.x = fmaf(u, kv.x, a.x); a.y = fmaf(u, kv.y, a.y);
-          a.z = fmaf(u, kv.z, a.z); a.w = fmaf(u, kv.w, a.w);
-        }
-        *reinterpret_cast<float4*>(Ss + jj * ldk + i) = a;
+    for (int jj = sj; sj < jst && jj < DVS; jj += jst) {
+      float4 a = *reinterpret_cast<float4*>(Ss + jj * ldk + si);
+      a.x *= gl; a.y *= gl; a.z *= gl; a.w *= gl;
+#pragma unroll 8
+      for (int s = 0; s < C; ++s) {
+        const float u = Us[s * DVS + jj];
+        const float4 kv = *reinterpret_cast<const float4*>(Ks + s * ldk + si);
+        a.x = fmaf(u, kv.x, a.x); a.y = fmaf(u, kv.y, a.y);
+        a.z = fmaf(u, kv.z, a.z); a.w = fmaf(u, kv.w, a.w);
       }
+      *reinterpret_cast<float4*>(Ss + jj * ldk + si) = a;
     }
   }
 }
 
-template <typename T>
+template <typename T, int C>
 __device__ __forceinline__ void walk_backward(const SimtArgs& P, const Walk& W, float* sm) {
-  const int C = P.C, ldk = P.dk + 4, ldc = C + 4, tid = threadIdx.x;
+  constexpr int ldc = C + 4, R = C / 16;
+  const int ldk = P.dk + 4, tid = threadIdx.x;
   float* Ss = sm;              // [DVS][ldk] dS
   float* Ks = Ss + DVS * ldk;  // [C][ldk]
   float* Qs = Ks + C * ldk;    // [C][ldk]
@@ -312,9 +374,12 @@ __device__ __forceinline__ void walk_backward(const SimtArgs& P, const Walk& W, 
   float* dd = Gm + C;
   const SimtWs w = simt_ws(P.ws, P.slots, P.Hv, P.dk, P.dv, C);
   const int64_t sbase = ((int64_t)W.n * P.Hv + W.h) * P.dv * P.dk + (int64_t)W.j0 * P.dk;
-  for (int e = tid; e < DVS * P.dk; e += THREADS)
-    Ss[(e / P.dk) * ldk + e % P.dk] = P.dST ? P.dST[sbase + e] : 0.0f;
-  const int w4 = P.dk / 4, jst = THREADS / w4;
+  const int w4 = P.dk / 4, jst = THREADS / w4, sj = tid / w4, si = 4 * (tid - sj * w4);
+  const int j = tid % DVS, rg = tid / DVS;
+  for (int jj = sj; sj < jst && jj < DVS; jj += jst)
+    *reinterpret_cast<float4*>(Ss + jj * ldk + si) =
+        P.dST ? *reinterpret_cast<const float4*>(P.dST + sbase + jj * P.dk + si)
+              : make_float4(0.f, 0.f, 0.f, 0.f);
   for (int64_t c = W.nch - 1; c >= 0; --c) {
     const int64_t t0 = W.s_beg + c * C, sh = (W.slot0 + c) * P.Hv + W.h;
     const int L = (int)min((int64_t)C, W.s_end - t0);
@@ -327,72 +392,76 @@ __device__ __forceinline__ void walk_backward(const SimtArgs& P, const Walk& W, 
     load_rows((const T*)P.dout + W.h * P.dv + W.j0, (int64_t)P.Hv * P.dv, t0, L, C, DVS, Os, DVS,
               P.scale);
     float* So = w.dS + sh * P.dv * P.dk + W.j0 * P.dk;
-    for (int e = tid; e < DVS * P.dk; e += THREADS) So[e] = Ss[(e / P.dk) * ldk + e % P.dk];
+    for (int jj = sj; sj < jst && jj < DVS; jj += jst)
+      *reinterpret_cast<float4*>(So + jj * P.dk + si) = *reinterpret_cast<float4*>(Ss + jj * ldk + si);
     __syncthreads();
-    const int j = tid % DVS;
-    for (int s = tid / DVS; s < C; s += THREADS / DVS) {  // dU = P^T dO' + d K dS^T
-      float acc = 0.0f;
-      for (int i = 0; i < P.dk; i += 4)
-        acc = dot4(*reinterpret_cast<const float4*>(Ks + s * ldk + i),
-                   *reinterpret_cast<const float4*>(Ss + j * ldk + i), acc);
-      acc *= dd[s];
-      for (int r = s; r < C; ++r) acc = fmaf(Ps[r * ldc + s], Os[r * DVS + j], acc);
-      Us[s * DVS + j] = acc;
+    {  // dU = P^T dO' + d K dS^T
+      float acc[R] = {};
+      rows_dot<R>(Ks, ldk, Ss + j * ldk, P.dk, rg, acc);
+#pragma unroll
+      for (int m = 0; m < R; ++m) acc[m] *= dd[rg + 16 * m];
+      cols_mul<R, C>(Ps, Os, rg, j, acc);
+#pragma unroll
+      for (int m = 0; m < R; ++m) Us[(rg + 16 * m) * DVS + j] = acc[m];
     }
     __syncthreads();
-    for (int s = tid / DVS; s < C; s += THREADS / DVS) {  // dW = T'^T dU
-      float acc = 0.0f;
-      for (int r = s; r < C; ++r) acc = fmaf(Ts[r * ldc + s], Us[r * DVS + j], acc);
-      Ws[s * DVS + j] = Gm[s] * acc;
-      w.dW[sh * C * P.dv + s * P.dv + W.j0 + j] = acc;
-      if (s < L) {
-        const float bf = w.rec[sh * 5 * C + 2 * C + s];
-        float out = acc;
-        if (fabsf(bf) == kBetaFloor) out *= P.beta[(t0 + s) * P.Hv + W.h] / bf;  // T' used the floor
-        ((T*)P.dv_)[((t0 + s) * P.Hv + W.h) * P.dv + W.j0 + j] = from_f<T>(out);
+    {  // dW = T'^T dU
+      float acc[R] = {};
+      cols_mul<R, C>(Ts, Us, rg, j, acc);
+#pragma unroll
+      for (int m = 0; m < R; ++m) {
+        const int s = rg + 16 * m;
+        Ws[s * DVS + j] = Gm[s] * acc[m];
+        w.dW[sh * C * P.dv + s * P.dv + W.j0 + j] = acc[m];
+        if (s < L) {
+          const float bf = w.rec[sh * 5 * C + 2 * C + s];
+          float out = acc[m];
+          if (fabsf(bf) == kBetaFloor) out *= P.beta[(t0 + s) * P.Hv + W.h] / bf;  // T' used the floor
+          ((T*)P.dv_)[((t0 + s) * P.Hv + W.h) * P.dv + W.j0 + j] = from_f<T>(out);
+        }
       }
     }
     __syncthreads();
     const float gl = Gm[C - 1];
-    if (tid < jst * w4) {
-      const int i = 4 * (tid % w4);
-      for (int jj = tid / w4; jj < DVS; jj += jst) {
-        float4 a = *reinterpret_cast<float4*>(Ss + jj * ldk + i);
-        a.x *= gl; a.y *= gl; a.z *= gl; a.w *= gl;
-        for (int s = 0; s < C; ++s) {
-          const float u = Os[s * DVS + jj] * Gm[s], x = -Ws[s * DVS + jj];
-          const float4 qv = *reinterpret_cast<const float4*>(Qs + s * ldk + i);
-          const float4 kv = *reinterpret_cast<const float4*>(Ks + s * ldk + i);
-          a.x = fmaf(u, qv.x, fmaf(x, kv.x, a.x)); a.y = fmaf(u, qv.y, fmaf(x, kv.y, a.y));
-          a.z = fmaf(u, qv.z, fmaf(x, kv.z, a.z)); a.w = fmaf(u, qv.w, fmaf(x, kv.w, a.w));
-        }
-        *reinterpret_cast<float4*>(Ss + jj * ldk + i) = a;
+    for (int jj = sj; sj < jst && jj < DVS; jj += jst) {
+      float4 a = *reinterpret_cast<float4*>(Ss + jj * ldk + si);
+      a.x *= gl; a.y *= gl; a.z *= gl; a.w *= gl;
+#pragma unroll 8
+      for (int s = 0; s < C; ++s) {
+        const float u = Os[s * DVS + jj] * Gm[s], x = -Ws[s * DVS + jj];
+        const float4 qv = *reinterpret_cast<const float4*>(Qs + s * ldk + si);
+        const float4 kv = *reinterpret_cast<const float4*>(Ks + s * ldk + si);
+        a.x = fmaf(u, qv.x, fmaf(x, kv.x, a.x)); a.y = fmaf(u, qv.y, fmaf(x, kv.y, a.y));
+        a.z = fmaf(u, qv.z, fmaf(x, kv.z, a.z)); a.w = fmaf(u, qv.w, fmaf(x, kv.w, a.w));
       }
+      *reinterpret_cast<float4*>(Ss + jj * ldk + si) = a;
     }
   }
   __syncthreads();
   if (P.dS0)
-    for (int e = tid; e < DVS * P.dk; e += THREADS)
-      P.dS0[sbase + e] = Ss[(e / P.dk) * ldk + e % P.dk];
+    for (int jj = sj; sj < jst && jj < DVS; jj += jst)
+      *reinterpret_cast<float4*>(P.dS0 + sbase + jj * P.dk + si) =
+          *reinterpret_cast<float4*>(Ss + jj * ldk + si);
 }
 
-template <typename T>
+template <typename T, int C>
 __global__ void __launch_bounds__(THREADS) gwalk_kernel(const SimtArgs P) {
   extern __shared__ __align__(16) float sm[];
   Walk W;
   if (!walk_of(P, W)) return;
   if (blockIdx.x & 1)
-    walk_forward<T>(P, W, sm);
+    walk_forward<T, C>(P, W, sm);
   else
-    walk_backward<T>(P, W, sm);
+    walk_backward<T, C>(P, W, sm);
 }
 
 // ------------------------------------------------------------------------------- ggrad -----
-// Warp w holds rows 8w .. 8w + 7 of the chunk, lane l columns 4l .. 4l + 3 of dq, dKe and dKw.
-template <typename T>
-__global__ void __launch_bounds__(THREADS) ggrad_kernel(const SimtArgs P) {
+// CW (a power of two >= dk / 4) neighbouring threads share RPT rows; each holds 4 columns of dq, dKe, dKw.
+template <typename T, int C, int RPT>
+__global__ void __launch_bounds__(THREADS) ggrad_kernel(const SimtArgs P, int CW) {
   extern __shared__ __align__(16) float sm[];
-  const int C = P.C, ldk = P.dk + 4, ldv = P.dv + 4, ldc = C + 4, tid = threadIdx.x;
+  constexpr int ldc = C + 4, TS = C / 16;
+  const int ldk = P.dk + 4, ldv = P.dv + 4, tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
   float* Ks = sm;                // [C][ldk]
   float* Qs = Ks + C * ldk;      // [C][ldk]
@@ -418,9 +487,14 @@ __global__ void __launch_bounds__(THREADS) ggrad_kernel(const SimtArgs P) {
   const int64_t t0 = ch.t0;
   load_rows((const T*)P.k + hk * P.dk, P.ts.k, t0, L, C, P.dk, Ks, ldk);
   load_rows((const T*)P.q + hk * P.dk, P.ts.q, t0, L, C, P.dk, Qs, ldk);
-  const int r0 = 8 * warp, c0 = 4 * lane;
+  const int rg = tid / CW, r0 = RPT * rg, c0 = 4 * (tid - rg * CW);
   const bool rows_on = r0 < C, on = rows_on && c0 < P.dk;
-  float dq[8][4] = {}, dk[8][4] = {};  // summed over the v-heads
+  // sum over the threads that share a row (all lanes take part)
+  auto row_sum = [&](float v) {
+    for (int o = CW >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  float dq[RPT][4] = {}, dk[RPT][4] = {};  // summed over the v-heads
   for (int gi = 0; gi < G; ++gi) {
     const int h = hk * G + gi;
     const int64_t sh = slot * P.Hv + h;
@@ -432,63 +506,82 @@ __global__ void __launch_bounds__(THREADS) ggrad_kernel(const SimtArgs P) {
     load_rows_f(w.U + sh * C * P.dv, C, P.dv, Us, ldv);
     load_rows_f(w.dW + sh * C * P.dv, C, P.dv, Ws, ldv);
     load_rows((const T*)P.dout + h * P.dv, (int64_t)P.Hv * P.dv, t0, L, C, P.dv, Os, ldv, P.scale);
-    __syncthreads();
     float frob = 0.0f;
-    for (int e = tid; e < P.dv * P.dk; e += THREADS) frob = fmaf(S[e], dS[e], frob);
+    for (int e = 4 * tid; e < P.dv * P.dk; e += 4 * THREADS)
+      frob = dot4(*reinterpret_cast<const float4*>(S + e), *reinterpret_cast<const float4*>(dS + e),
+                  frob);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) frob += __shfl_xor_sync(0xffffffffu, frob, o);
     if (lane == 0) red[warp] = frob;
     __syncthreads();
-    // dN, dM and p: this warp's rows, columns lane and lane + 32
-    if (rows_on) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int s = lane + 32 * half;
-        if (s >= C) break;
-        float on_[8] = {}, om[8] = {};
+    // dN, dM (zero on and above the diagonal), p and dbeta: TS x TS entries a thread
+    {
+      const int rb = TS * (tid / 16), sb = TS * (tid % 16);
+      float a[TS][TS] = {}, b[TS][TS] = {};
+      if (sb <= rb) {
         for (int jx = 0; jx < P.dv; jx += 4) {
-          const float4 u = *reinterpret_cast<const float4*>(Us + s * ldv + jx);
+          float4 u[TS];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            on_[x] = dot4(*reinterpret_cast<const float4*>(Os + (r0 + x) * ldv + jx), u, on_[x]);
-            om[x] = dot4(*reinterpret_cast<const float4*>(Ws + (r0 + x) * ldv + jx), u, om[x]);
-          }
-        }
+          for (int y = 0; y < TS; ++y) u[y] = *reinterpret_cast<const float4*>(Us + (sb + y) * ldv + jx);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int r = r0 + x;
-          const float e = s < r ? expf((float)(gam[r] - gam[s])) : 0.0f;
-          Ns[r * ldc + s] = e * on_[x];
-          Ms[r * ldc + s] = -e * om[x];
-          if (s == r) {
-            own[r] = on_[x];
-            if (r < L)
-              ((T*)P.dbeta)[(t0 + r) * P.Hv + h] = from_f<T>(om[x] / bet[r] / bet[r]);
+          for (int x = 0; x < TS; ++x) {
+            const float4 o = *reinterpret_cast<const float4*>(Os + (rb + x) * ldv + jx);
+            const float4 d = *reinterpret_cast<const float4*>(Ws + (rb + x) * ldv + jx);
+#pragma unroll
+            for (int y = 0; y < TS; ++y) {
+              a[x][y] = dot4(o, u[y], a[x][y]);
+              b[x][y] = dot4(d, u[y], b[x][y]);
+            }
           }
         }
       }
+#pragma unroll
+      for (int x = 0; x < TS; ++x)
+#pragma unroll
+        for (int y = 0; y < TS; ++y) {
+          const int r = rb + x, s = sb + y;
+          const float e = s < r ? expf((float)(gam[r] - gam[s])) : 0.0f;
+          Ns[r * ldc + s] = e * a[x][y];
+          Ms[r * ldc + s] = -e * b[x][y];
+          if (s == r) {
+            own[r] = a[x][y];
+            if (r < L)
+              ((T*)P.dbeta)[(t0 + r) * P.Hv + h] = from_f<T>(b[x][y] / bet[r] / bet[r]);
+          }
+        }
     }
     __syncthreads();
-    float aq[8][4] = {}, ae[8][4] = {}, aw[8][4] = {};
+    float aq[RPT][4] = {}, ae[RPT][4] = {}, aw[RPT][4] = {};
     if (on) {
-      for (int jx = 0; jx < P.dv; ++jx) {
-        const float4 s4 = *reinterpret_cast<const float4*>(S + jx * P.dk + c0);
-        const float4 d4 = *reinterpret_cast<const float4*>(dS + jx * P.dk + c0);
-        const float sv[4] = {s4.x, s4.y, s4.z, s4.w}, dv4[4] = {d4.x, d4.y, d4.z, d4.w};
+      for (int jx = 0; jx < P.dv; jx += 4) {
+        float4 s4[4], d4[4];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const float o = Os[(r0 + x) * ldv + jx], ww = Ws[(r0 + x) * ldv + jx],
-                      u = Us[(r0 + x) * ldv + jx];
+        for (int q = 0; q < 4; ++q) {
+          s4[q] = *reinterpret_cast<const float4*>(S + (jx + q) * P.dk + c0);
+          d4[q] = *reinterpret_cast<const float4*>(dS + (jx + q) * P.dk + c0);
+        }
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            aq[x][y] = fmaf(o, sv[y], aq[x][y]);
-            ae[x][y] = fmaf(ww, sv[y], ae[x][y]);
-            aw[x][y] = fmaf(u, dv4[y], aw[x][y]);
+        for (int x = 0; x < RPT; ++x) {
+          const float4 o4 = *reinterpret_cast<const float4*>(Os + (r0 + x) * ldv + jx);
+          const float4 w4 = *reinterpret_cast<const float4*>(Ws + (r0 + x) * ldv + jx);
+          const float4 u4 = *reinterpret_cast<const float4*>(Us + (r0 + x) * ldv + jx);
+          const float o[4] = {o4.x, o4.y, o4.z, o4.w}, ww[4] = {w4.x, w4.y, w4.z, w4.w},
+                      u[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float sv[4] = {s4[q].x, s4[q].y, s4[q].z, s4[q].w};
+            const float dv[4] = {d4[q].x, d4[q].y, d4[q].z, d4[q].w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              aq[x][y] = fmaf(o[q], sv[y], aq[x][y]);
+              ae[x][y] = fmaf(ww[q], sv[y], ae[x][y]);
+              aw[x][y] = fmaf(u[q], dv[y], aw[x][y]);
+            }
           }
         }
       }
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
+      for (int x = 0; x < RPT; ++x)
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           aq[x][y] *= Gm[r0 + x];
@@ -496,79 +589,96 @@ __global__ void __launch_bounds__(THREADS) ggrad_kernel(const SimtArgs P) {
           aw[x][y] *= dd[r0 + x];
         }
     }
-    if (rows_on) {
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        float v = 0.0f;
-        if (on)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) v = fmaf(Ks[(r0 + x) * ldk + c0 + y], aw[x][y], v);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) kw[r0 + x] = v;
-      }
+    for (int x = 0; x < RPT; ++x) {
+      float v = 0.0f;
+      if (on)
+        v = dot4(*reinterpret_cast<const float4*>(Ks + (r0 + x) * ldk + c0),
+                 make_float4(aw[x][0], aw[x][1], aw[x][2], aw[x][3]), 0.0f);
+      v = row_sum(v);
+      if (rows_on && c0 == 0) kw[r0 + x] = v;
     }
     if (on) {
-      for (int s = 0; s < r0 + 8; ++s) {  // rows of this warp against earlier tokens
-        const float4 k4 = *reinterpret_cast<const float4*>(Ks + s * ldk + c0);
-        const float kv[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll 2
+      for (int s = 0; s < r0 + RPT; s += 4) {  // these rows against earlier tokens (C is a multiple of 4)
+        float4 k4[4];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const float nn = Ns[(r0 + x) * ldc + s], mm = Ms[(r0 + x) * ldc + s];
+        for (int q = 0; q < 4; ++q) k4[q] = *reinterpret_cast<const float4*>(Ks + (s + q) * ldk + c0);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            aq[x][y] = fmaf(nn, kv[y], aq[x][y]);
-            ae[x][y] = fmaf(mm, kv[y], ae[x][y]);
+        for (int x = 0; x < RPT; ++x) {
+          const float4 n4 = *reinterpret_cast<const float4*>(Ns + (r0 + x) * ldc + s);
+          const float4 m4 = *reinterpret_cast<const float4*>(Ms + (r0 + x) * ldc + s);
+          const float nn[4] = {n4.x, n4.y, n4.z, n4.w}, mm[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float kv[4] = {k4[q].x, k4[q].y, k4[q].z, k4[q].w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              aq[x][y] = fmaf(nn[q], kv[y], aq[x][y]);
+              ae[x][y] = fmaf(mm[q], kv[y], ae[x][y]);
+            }
           }
         }
       }
+#pragma unroll 4
       for (int r = r0; r < C; ++r) {  // and later tokens
         const float4 k4 = *reinterpret_cast<const float4*>(Ks + r * ldk + c0);
         const float4 q4 = *reinterpret_cast<const float4*>(Qs + r * ldk + c0);
         const float kv[4] = {k4.x, k4.y, k4.z, k4.w}, qv[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
+        for (int x = 0; x < RPT; ++x) {
           const float nn = Ns[r * ldc + r0 + x], mm = Ms[r * ldc + r0 + x];
 #pragma unroll
           for (int y = 0; y < 4; ++y) aw[x][y] = fmaf(nn, qv[y], fmaf(mm, kv[y], aw[x][y]));
         }
       }
     }
-    if (rows_on) {
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int r = r0 + x;
-        float v = 0.0f;
-        if (on) {
-          const float p = own[r];
+    for (int x = 0; x < RPT; ++x) {
+      const int r = r0 + x;
+      float v = 0.0f;
+      if (on) {
+        const float p = own[r];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float kv = Ks[r * ldk + c0 + y], qv = Qs[r * ldk + c0 + y];
-            v = fmaf(qv, aq[x][y], fmaf(kv, ae[x][y] - aw[x][y], v));
-            dq[x][y] += fmaf(p, kv, aq[x][y]);
-            dk[x][y] += fmaf(p, qv, ae[x][y] + aw[x][y]);
-          }
+        for (int y = 0; y < 4; ++y) {
+          const float kv = Ks[r * ldk + c0 + y], qv = Qs[r * ldk + c0 + y];
+          v = fmaf(qv, aq[x][y], fmaf(kv, ae[x][y] - aw[x][y], v));
+          dq[x][y] += fmaf(p, kv, aq[x][y]);
+          dk[x][y] += fmaf(p, qv, ae[x][y] + aw[x][y]);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) dgm[r] = v;
       }
+      v = row_sum(v);
+      if (rows_on && c0 == 0) dgm[r] = v;
     }
     __syncthreads();
-    if (tid == 0) {  // dg: suffix sums, and what leaves through the state
-      float f = 0.0f, acc = 0.0f;
+    // dg: suffix sums, and what leaves through the state
+    if (warp == 0) {
+      float f = 0.0f;
       for (int x = 0; x < THREADS / 32; ++x) f += red[x];
       f *= Gm[C - 1];
-      for (int r = 0; r < L; ++r) f += kw[r];
-      for (int r = L - 1; r >= 0; --r) {
-        acc += dgm[r];
-        ((T*)P.dg)[(t0 + r) * P.Hv + h] = from_f<T>(acc + f);
+      float k0 = lane < L ? kw[lane] : 0.0f;
+      if (C > 32 && 32 + lane < L) k0 += kw[32 + lane];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) k0 += __shfl_xor_sync(0xffffffffu, k0, o);
+      f += k0;
+      float a0 = lane < L ? dgm[lane] : 0.0f, a1 = C > 32 && 32 + lane < L ? dgm[32 + lane] : 0.0f;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float u0 = __shfl_down_sync(0xffffffffu, a0, o);
+        const float u1 = __shfl_down_sync(0xffffffffu, a1, o);
+        if (lane + o < 32) {
+          a0 += u0;
+          a1 += u1;
+        }
       }
+      a0 += __shfl_sync(0xffffffffu, a1, 0);
+      if (lane < L) ((T*)P.dg)[(t0 + lane) * P.Hv + h] = from_f<T>(a0 + f);
+      if (32 + lane < L) ((T*)P.dg)[(t0 + 32 + lane) * P.Hv + h] = from_f<T>(a1 + f);
     }
   }
   if (on) {
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
+    for (int x = 0; x < RPT; ++x) {
       const int r = r0 + x;
       if (r >= L) break;
       T* oq = (T*)P.dq + ((t0 + r) * P.Hk + hk) * P.dk + c0;
@@ -582,11 +692,20 @@ __global__ void __launch_bounds__(THREADS) ggrad_kernel(const SimtArgs P) {
   }
 }
 
-template <typename T>
-cudaError_t launch_t(const SimtArgs& P, cudaStream_t s) {
-  const int C = P.C, ldk = P.dk + 4, ldv = P.dv + 4, ldc = C + 4;
+template <typename T, int C, int RPT>
+cudaError_t launch_grad(const SimtArgs& P, int cw, int64_t par, size_t bytes, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      ggrad_kernel<T, C, RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return e;
+  ggrad_kernel<T, C, RPT><<<(unsigned)par, THREADS, bytes, s>>>(P, cw);
+  return cudaGetLastError();
+}
+
+template <typename T, int C>
+cudaError_t launch_c(const SimtArgs& P, cudaStream_t s) {
+  const int ldk = P.dk + 4, ldv = P.dv + 4, ldc = C + 4;
   const size_t f = sizeof(float);
-  const size_t sm_prep = (2 * (size_t)C * ldk + 4 * C * ldc + C) * f + C * 8;
+  const size_t sm_prep = (2 * (size_t)C * ldk + 3 * C * ldc + 3 * C) * f + C * 8;
   const size_t sm_walk =  // the backward walk's; the forward one needs less
       ((size_t)(DVS + 2 * C) * ldk + 2 * C * ldc + 3 * C * DVS + 2 * C) * f;
   const size_t sm_grad =
@@ -594,16 +713,28 @@ cudaError_t launch_t(const SimtArgs& P, cudaStream_t s) {
   auto set = [](auto kern, size_t bytes) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   };
-  cudaError_t e = set(gprep_kernel<T>, sm_prep);
-  if (e == cudaSuccess) e = set(gwalk_kernel<T>, sm_walk);
-  if (e == cudaSuccess) e = set(ggrad_kernel<T>, sm_grad);
+  cudaError_t e = set(gprep_kernel<T, C>, sm_prep);
+  if (e == cudaSuccess) e = set(gwalk_kernel<T, C>, sm_walk);
   if (e != cudaSuccess) return e;
   const int64_t par = P.slots * P.Hk, walks = 2 * (int64_t)P.N * P.Hv * (P.dv / DVS);
   if (par > 0x7fffffff || walks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if (par > 0) gprep_kernel<T><<<(unsigned)par, THREADS, sm_prep, s>>>(P);
-  if (walks > 0) gwalk_kernel<T><<<(unsigned)walks, THREADS, sm_walk, s>>>(P);
-  if (par > 0) ggrad_kernel<T><<<(unsigned)par, THREADS, sm_grad, s>>>(P);
-  return cudaGetLastError();
+  if (par > 0) gprep_kernel<T, C><<<(unsigned)par, THREADS, sm_prep, s>>>(P);
+  if (walks > 0) gwalk_kernel<T, C><<<(unsigned)walks, THREADS, sm_walk, s>>>(P);
+  e = cudaGetLastError();
+  if (par == 0 || e != cudaSuccess) return e;
+  int cw = 4;
+  while (4 * cw < P.dk) cw *= 2;
+  switch (C * cw / THREADS) {  // rows a thread
+    case 8: return launch_grad<T, C, C == 64 ? 8 : 1>(P, cw, par, sm_grad, s);
+    case 4: return launch_grad<T, C, C >= 32 ? 4 : 1>(P, cw, par, sm_grad, s);
+    case 2: return launch_grad<T, C, 2>(P, cw, par, sm_grad, s);
+    default: return launch_grad<T, C, 1>(P, cw, par, sm_grad, s);
+  }
+}
+
+template <typename T>
+cudaError_t launch_t(const SimtArgs& P, cudaStream_t s) {
+  return P.C == 64 ? launch_c<T, 64>(P, s) : P.C == 32 ? launch_c<T, 32>(P, s) : launch_c<T, 16>(P, s);
 }
 
 }  // namespace
