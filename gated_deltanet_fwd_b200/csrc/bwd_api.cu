@@ -64,9 +64,15 @@ int64_t conv_parts(int64_t n_tok, int C) {
   const int64_t need = (n_tok + 15) / 16;
   return need < 1 ? 1 : need < most ? need : most;
 }
-// The shape of the tensor-core backward pass of the rule, as of the forward.
-bool tensor_cores(gdn_dtype dtype, int dk, int dv, int chunk) {
-  return dtype == GDN_BF16 && dk == 128 && dv == 128 && chunk == 64;
+// Whether the rule's backward pass runs on tensor cores: the shape of the forward's tensor-core path, and
+// at least 512 gate values (tokens x v-heads).  The tensor-core kernels round their operands to bf16; over
+// many values the relative error of dg and dbeta is 3 to 4e-3, but of a handful each is one dot product,
+// and the norm of that few can be off by more than the 5e-3 promised (5.05e-3 measured at 6 values).  The
+// CUDA-core kernels carry fp32 throughout.  At 100 tokens and 4 v-heads they take CUDA_US us, the tensor
+// cores TC_US.
+constexpr int64_t TC_MIN_VALUES = 512;
+bool tensor_cores(gdn_dtype dtype, int64_t n_tok, int Hv, int dk, int dv, int chunk) {
+  return dtype == GDN_BF16 && dk == 128 && dv == 128 && chunk == 64 && n_tok * Hv >= TC_MIN_VALUES;
 }
 bool norm_dim_ok(int dim) {
   return dim == 8 || dim == 16 || dim == 32 || dim == 64 || dim == 128 || dim == 256;
@@ -279,7 +285,7 @@ size_t gdn_chunk_bwd_workspace_size(gdn_dtype dtype, int N, int B, int64_t T, in
   if (N < 0 || B < 0 || T < 0 || Hv < 1 || dk < 1 || dv < 1 || chunk < 1) return 256;
   const int64_t n_tok = (int64_t)B * T;
   if (n_tok == 0) return bwd::HEADER;
-  return round256(tensor_cores(dtype, dk, dv, chunk)
+  return round256(tensor_cores(dtype, n_tok, Hv, dk, dv, chunk)
                       ? bwd::tc_workspace_bytes(N, n_tok, Hv)
                       : bwd::simt_workspace_bytes(N, n_tok, Hv, dk, dv, chunk));
 }
@@ -344,8 +350,8 @@ gdn_status gdn_chunk_bwd(const void* q, int64_t q_tok_stride, const void* k, int
   a.status = reinterpret_cast<int*>(workspace);
   const cudaStream_t s = as_stream(stream);
   if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return GDN_ERR_CUDA;
-  return from_cuda(n_tok > 0 && tensor_cores(dtype, dk, dv, chunk) ? bwd::launch_tc(a, s)
-                                                                   : bwd::launch_simt(a, s));
+  return from_cuda(tensor_cores(dtype, n_tok, Hv, dk, dv, chunk) ? bwd::launch_tc(a, s)
+                                                                 : bwd::launch_simt(a, s));
 }
 
 }  // extern "C"

@@ -367,11 +367,12 @@ __device__ __forceinline__ void walk_backward(const SimtArgs& P, const Walk& W, 
   float* Qs = Ks + C * ldk;    // [C][ldk]
   float* Ts = Qs + C * ldk;    // [C][ldc] T'
   float* Ps = Ts + C * ldc;    // [C][ldc] P
-  float* Os = Ps + C * ldc;    // [C][DVS] dO'
+  float* Os = Ps + C * ldc;    // [C][DVS] dO', then Gamma dO'
   float* Us = Os + C * DVS;    // [C][DVS] dU
-  float* Ws = Us + C * DVS;    // [C][DVS] Gamma dW
+  float* Ws = Us + C * DVS;    // [C][DVS] -Gamma dW
   float* Gm = Ws + C * DVS;
   float* dd = Gm + C;
+  float* bet = dd + C;
   const SimtWs w = simt_ws(P.ws, P.slots, P.Hv, P.dk, P.dv, C);
   const int64_t sbase = ((int64_t)W.n * P.Hv + W.h) * P.dv * P.dk + (int64_t)W.j0 * P.dk;
   const int w4 = P.dk / 4, jst = THREADS / w4, sj = tid / w4, si = 4 * (tid - sj * w4);
@@ -384,7 +385,7 @@ __device__ __forceinline__ void walk_backward(const SimtArgs& P, const Walk& W, 
     const int64_t t0 = W.s_beg + c * C, sh = (W.slot0 + c) * P.Hv + W.h;
     const int L = (int)min((int64_t)C, W.s_end - t0);
     __syncthreads();
-    if (tid < 2 * C) Gm[tid] = w.rec[sh * 5 * C + tid];  // Gamma, d
+    if (tid < 3 * C) Gm[tid] = w.rec[sh * 5 * C + tid];  // Gamma, d, beta
     load_rows((const T*)P.k + W.hk * P.dk, P.ts.k, t0, L, C, P.dk, Ks, ldk);
     load_rows((const T*)P.q + W.hk * P.dk, P.ts.q, t0, L, C, P.dk, Qs, ldk);
     load_rows_f(w.tp + sh * 2 * C * C, C, C, Ts, ldc);
@@ -405,16 +406,18 @@ __device__ __forceinline__ void walk_backward(const SimtArgs& P, const Walk& W, 
       for (int m = 0; m < R; ++m) Us[(rg + 16 * m) * DVS + j] = acc[m];
     }
     __syncthreads();
+#pragma unroll
+    for (int m = 0; m < R; ++m) Os[(rg + 16 * m) * DVS + j] *= Gm[rg + 16 * m];
     {  // dW = T'^T dU
       float acc[R] = {};
       cols_mul<R, C>(Ts, Us, rg, j, acc);
 #pragma unroll
       for (int m = 0; m < R; ++m) {
         const int s = rg + 16 * m;
-        Ws[s * DVS + j] = Gm[s] * acc[m];
+        Ws[s * DVS + j] = -Gm[s] * acc[m];
         w.dW[sh * C * P.dv + s * P.dv + W.j0 + j] = acc[m];
         if (s < L) {
-          const float bf = w.rec[sh * 5 * C + 2 * C + s];
+          const float bf = bet[s];
           float out = acc[m];
           if (fabsf(bf) == kBetaFloor) out *= P.beta[(t0 + s) * P.Hv + W.h] / bf;  // T' used the floor
           ((T*)P.dv_)[((t0 + s) * P.Hv + W.h) * P.dv + W.j0 + j] = from_f<T>(out);
@@ -428,7 +431,7 @@ __device__ __forceinline__ void walk_backward(const SimtArgs& P, const Walk& W, 
       a.x *= gl; a.y *= gl; a.z *= gl; a.w *= gl;
 #pragma unroll 8
       for (int s = 0; s < C; ++s) {
-        const float u = Os[s * DVS + jj] * Gm[s], x = -Ws[s * DVS + jj];
+        const float u = Os[s * DVS + jj], x = Ws[s * DVS + jj];
         const float4 qv = *reinterpret_cast<const float4*>(Qs + s * ldk + si);
         const float4 kv = *reinterpret_cast<const float4*>(Ks + s * ldk + si);
         a.x = fmaf(u, qv.x, fmaf(x, kv.x, a.x)); a.y = fmaf(u, qv.y, fmaf(x, kv.y, a.y));
@@ -707,7 +710,7 @@ cudaError_t launch_c(const SimtArgs& P, cudaStream_t s) {
   const size_t f = sizeof(float);
   const size_t sm_prep = (2 * (size_t)C * ldk + 3 * C * ldc + 3 * C) * f + C * 8;
   const size_t sm_walk =  // the backward walk's; the forward one needs less
-      ((size_t)(DVS + 2 * C) * ldk + 2 * C * ldc + 3 * C * DVS + 2 * C) * f;
+      ((size_t)(DVS + 2 * C) * ldk + 2 * C * ldc + 3 * C * DVS + 3 * C) * f;
   const size_t sm_grad =
       (2 * (size_t)C * ldk + 3 * C * ldv + 2 * C * ldc + 6 * C + 8) * f + C * 8;
   auto set = [](auto kern, size_t bytes) {
