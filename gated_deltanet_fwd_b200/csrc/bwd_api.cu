@@ -68,11 +68,17 @@ int64_t conv_parts(int64_t n_tok, int C) {
 // at least 512 gate values (tokens x v-heads).  The tensor-core kernels round their operands to bf16; over
 // many values the relative error of dg and dbeta is 3 to 4e-3, but of a handful each is one dot product,
 // and the norm of that few can be off by more than the 5e-3 promised (5.05e-3 measured at 6 values).  The
-// CUDA-core kernels carry fp32 throughout.  At 100 tokens and 4 v-heads they take CUDA_US us, the tensor
-// cores TC_US.
+// CUDA-core kernels carry fp32 throughout.  At 100 tokens and 4 v-heads they take 84 us, the tensor cores 47.
 constexpr int64_t TC_MIN_VALUES = 512;
 bool tensor_cores(gdn_dtype dtype, int64_t n_tok, int Hv, int dk, int dv, int chunk) {
   return dtype == GDN_BF16 && dk == 128 && dv == 128 && chunk == 64 && n_tok * Hv >= TC_MIN_VALUES;
+}
+// Chunk length on CUDA cores: the caller's, but shorter where a call is only too small for the tensor cores.
+// One v-head per k-head and 1 token: 33 us with chunks of 16, 49 with 32, 98 with 64; 100 tokens, 4 v-heads:
+// 84, 111, 185; 250 tokens, 2 v-heads: 129, 143, 221; 500 tokens, 1 v-head: 182, 172, 231.
+int simt_chunk(gdn_dtype dtype, int64_t n_tok, int dk, int dv, int chunk) {
+  if (dtype != GDN_BF16 || dk != 128 || dv != 128 || chunk != 64) return chunk;
+  return n_tok <= 256 ? 16 : 32;
 }
 bool norm_dim_ok(int dim) {
   return dim == 8 || dim == 16 || dim == 32 || dim == 64 || dim == 128 || dim == 256;
@@ -287,7 +293,8 @@ size_t gdn_chunk_bwd_workspace_size(gdn_dtype dtype, int N, int B, int64_t T, in
   if (n_tok == 0) return bwd::HEADER;
   return round256(tensor_cores(dtype, n_tok, Hv, dk, dv, chunk)
                       ? bwd::tc_workspace_bytes(N, n_tok, Hv)
-                      : bwd::simt_workspace_bytes(N, n_tok, Hv, dk, dv, chunk));
+                      : bwd::simt_workspace_bytes(N, n_tok, Hv, dk, dv,
+                                                  simt_chunk(dtype, n_tok, dk, dv, chunk)));
 }
 
 gdn_status gdn_chunk_bwd(const void* q, int64_t q_tok_stride, const void* k, int64_t k_tok_stride,
@@ -350,8 +357,9 @@ gdn_status gdn_chunk_bwd(const void* q, int64_t q_tok_stride, const void* k, int
   a.status = reinterpret_cast<int*>(workspace);
   const cudaStream_t s = as_stream(stream);
   if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return GDN_ERR_CUDA;
-  return from_cuda(tensor_cores(dtype, n_tok, Hv, dk, dv, chunk) ? bwd::launch_tc(a, s)
-                                                                 : bwd::launch_simt(a, s));
+  if (tensor_cores(dtype, n_tok, Hv, dk, dv, chunk)) return from_cuda(bwd::launch_tc(a, s));
+  a.C = simt_chunk(dtype, n_tok, dk, dv, chunk);
+  return from_cuda(bwd::launch_simt(a, s));
 }
 
 }  // extern "C"

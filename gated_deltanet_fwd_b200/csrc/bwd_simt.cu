@@ -556,6 +556,8 @@ __global__ void __launch_bounds__(THREADS) ggrad_kernel(const SimtArgs P, int CW
     __syncthreads();
     float aq[RPT][4] = {}, ae[RPT][4] = {}, aw[RPT][4] = {};
     if (on) {
+      // unrolled for the latency of the state loads (from L2), as far as registers allow
+#pragma unroll(RPT <= 2 ? 4 : 1)
       for (int jx = 0; jx < P.dv; jx += 4) {
         float4 s4[4], d4[4];
 #pragma unroll
