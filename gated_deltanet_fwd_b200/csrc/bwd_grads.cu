@@ -1,7 +1,9 @@
 // bwd_grads.cu -- the parallel half of the tensor-core backward pass (bwd_tc.cuh): dq, dk, dg and dbeta of
 // every chunk from the chains' states S, dS, U and dv.  Formulas in bwd_simt.cu.
 //
-// Work item = (chunk, k-head), persistent CTAs; an item runs through the v-heads that share the k-head.
+// Work item = (chunk, k-head); an item runs through the v-heads that share the k-head.  Persistent CTAs, which
+// take their items from a counter (the first one is the CTA's own number): the SMs finish equal work up
+// to a fifth apart, by their way to memory.  Which CTA does an item changes none of its results.
 // Everything is computed transposed -- lane i of tensor memory is channel i of q and k, columns are
 // tokens -- so that every product has M = 128 and the sums over the shared heads stay in registers of
 // the thread that owns the channel:
@@ -12,17 +14,17 @@
 //          D5 = Q^T dN + K^T dM         M 128, N 64,  K 64 twice
 // Epilogue A (token rows): decay masks on D2 -> [dN; dM] in shared memory as bf16 (with the diagonal of dN,
 // a token's own pair: its two contributions to dgamma are sums of the same rounded products and cancel
-// to fp32 rounding), and dbeta from the diagonal of dW U^T; <S, dS> from shared memory, by mma.sync on
-// 16-row diagonal blocks (32 warp instructions a warp; element by element it was 210).  Epilogue B
+// to fp32 rounding), dbeta from the diagonal of dW U^T, and <S, dS> from shared memory.  Epilogue B
 // (channel rows): Gamma and d applied in fp32, dq and dk summed over the heads, dgamma = q.dq +
 // k.(dKe - dKw) reduced over channels; two tokens per instruction (fp32x2).
-// MMA_s does not wait for epilogue A, and a head's tiles are refilled as soon as MMA_s is done with them,
-// while MMA_n and epilogue B of that head still run.
+// MMA_p of the next head runs beside epilogue B of this one.  [dO; dW] and U have two buffers; S and dS have one,
+// free again before epilogue B; dq and dk leave through the [dO; dW] buffer of the item's last step.  So the
+// loads of a step run beside the epilogues of the step before.
 //
 // Warp roles (384 threads): warps 0-7 the epilogues (lane quarter warp % 4; columns, in epilogue B tokens,
-// split in two by warp / 4), warp 8 the TMA producer, warp 9 the MMA issuer.  Bounds: 144 KB of tiles per
-// (chunk, v-head) at two v-heads a k-head against about 6 units of 64 x 128 x 128 products: HBM, with the
-// epilogues' instructions close behind (a step took 9400 cycles when they were written plainly).
+// split in two by warp / 4), warp 8 the TMA producer, warp 9 the MMA issuer, warp 10 sends dq and dk out.
+// Bounds: 144 KB of tiles per (chunk, v-head) at two v-heads a k-head against about 6 units of
+// 64 x 128 x 128 products: HBM, with the epilogues' instructions close behind.
 // Bounded waits and the abort protocol as in bwd_chain.cu.
 #include "bwd_tc.cuh"
 #include "f32x2.cuh"
@@ -34,32 +36,31 @@ namespace {
 
 using namespace ptx;
 
-// Three warpgroups: epilogues (two), and producer + issuer (two warps idle).  168 registers a thread at
+// Three warpgroups: epilogues (two), and producer, issuer and sender (one warp idle).  168 registers a thread at
 // launch; 2 x 184 + 136 = 3 x 168 (the issuer keeps its loop-invariant descriptors in registers).
 constexpr int THREADS = 384;
-constexpr int W_PROD = 8, W_MMA = 9;
+constexpr int W_PROD = 8, W_MMA = 9, W_OUT = 10;
 
 // shared memory, from a 1024-aligned base
 constexpr uint32_t SM_KQ = 0;               // [K; Q]: two 64-column halves x 128 rows x 128 B
-constexpr uint32_t SM_OW = SM_KQ + 32768;   // [dO; dW]: the same
-constexpr uint32_t SM_U = SM_OW + 32768;    // U^T: 128 rows x 128 B
-constexpr uint32_t SM_S = SM_U + 16384;     // S: two halves x 128 rows x 128 B
-constexpr uint32_t SM_DS = SM_S + 32768;    // dS: the same
-constexpr uint32_t SM_NM = SM_DS + 32768;   // [dN; dM]: 128 rows x 128 B
-constexpr uint32_t SM_GD = SM_NM + 16384;   // two records
-constexpr uint32_t SM_OUT = SM_GD + 2 * GD_BYTES;  // dq, dk on their way out: each two halves x 64 x 128 B
-constexpr uint32_t SM_RED = SM_OUT + 32768;        // 2 x (dgamma parts [4][64], sums [8] + [8])
+constexpr uint32_t SM_OW = SM_KQ + 32768;   // [dO; dW]: two buffers of the same form; at the end of an
+                                            // item dq, dk: each two halves x 64 x 128 B
+constexpr uint32_t SM_U = SM_OW + 2 * 32768;  // U^T: two buffers of 128 rows x 128 B
+constexpr uint32_t SM_S = SM_U + 2 * 16384;   // S: two halves x 128 rows x 128 B
+constexpr uint32_t SM_DS = SM_S + 32768;      // dS: the same
+constexpr uint32_t SM_NM = SM_DS + 32768;     // [dN; dM]: 128 rows x 128 B
+constexpr uint32_t SM_GD = SM_NM + 16384;     // four records: one is read until its step ends
+constexpr uint32_t SM_RED = SM_GD + 4 * GD_BYTES;  // 2 x (dgamma parts [4][64], sums [8] + [8])
 constexpr uint32_t RED_FLOATS = 4 * 64 + 16;
 constexpr uint32_t SM_BAR = SM_RED + 2 * RED_FLOATS * 4;
-static_assert(SM_OUT % 1024 == 0, "swizzled tiles");
-constexpr uint32_t SM_BYTES = SM_BAR + 128 + 1024;
+constexpr uint32_t SM_BYTES = SM_BAR + 192 + 1024;
 static_assert(SM_BYTES <= 232448, "shared memory budget");
-constexpr uint32_t TX_KQ = 32768, TX_HEAD = 32768 + 16384 + 65536 + GD_BYTES;
+constexpr uint32_t TX_KQ = 32768, TX_HEAD = 32768 + 16384 + GD_BYTES, TX_STATE = 65536;
 
-enum { B_KQ = 0, B_KQE = 1, B_H = 2, B_HE = 3, B_P = 4, B_N = 5, B_FIX = 6, B_DRAIN = 7, B_COUNT = 8 };
-enum { NB_NM = 1, NB_D = 2, NB_E = 3, NB_O = 4 };
-constexpr int NB_ALL = 288;  // epilogue warps + issuer
-constexpr int NB_EPI = 256;
+// B_H, B_HE: two of each, by the step's parity; B_O: by the item's
+enum { B_KQ, B_KQE, B_H, B_HE = B_H + 2, B_O = B_HE + 2, B_S = B_O + 2, B_SE, B_P, B_NM, B_N, B_D, B_FIX, B_DRAIN, B_COUNT };
+static_assert(B_COUNT * 8 + 8 + 24 <= 192, "barriers");
+constexpr int NB_E = 1, NB_EPI = 256;  // named barrier of the epilogues
 
 // tensor-memory columns
 constexpr uint32_t TM_D2 = 0, TM_D1 = 64, TM_D4 = 192, TM_D3 = 320, TM_D5 = 384;
@@ -69,6 +70,7 @@ struct GradParams {
   const float* S0;  // only whether there is one
   const int32_t* cu;
   const unsigned char* ws;
+  int* next;  // items handed out beyond the CTAs' first ones
   __nv_bfloat16 *dq, *dk, *dv, *dg, *dbeta;
   int* status;
   int64_t T, items;
@@ -99,39 +101,33 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-// c (16 x 8) += a (16 x 16) b (16 x 8), bf16
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// This lane's part of the sum of X o Y over rows 16 w .. 16 w + 15 of two swizzled [2][128][64] images:
-// the diagonal of X Y^T on that block.
-__device__ __forceinline__ float dot_rows16(uint32_t x, uint32_t y, int w, int lane) {
-  float c0[4] = {}, c1[4] = {};
-  // ldmatrix: lanes 0-7 rows 0-7 of columns 0-7, lanes 8-15 rows 8-15, lanes 16-31 columns 8-15 -- as
-  // A (a0..a3); read the same way, registers 0, 2 are B of columns 0-7 and 1, 3 of columns 8-15
-  const int row = 16 * w + (lane & 15);
+// acc + the products of eight bf16 pairs, in fp32
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t off = (uint32_t)(k >> 2) * 16384 + sw128(row, 16 * (k & 3) + 8 * (lane >> 4));
-    uint32_t a[4], b[4];
-    ldmatrix4(a, x + off);
-    ldmatrix4(b, y + off);
-    mma_16816(c0, a, b[0], b[2]);
-    mma_16816(c1, a, b[1], b[3]);
-  }
-  // c0: (g, 2t), (g, 2t + 1) of the block's first 8 columns; c1[2..3]: rows g + 8 of its last 8
-  const int g = lane >> 2, t = 2 * (lane & 3);
-  return (g == t ? c0[0] + c1[2] : 0.0f) + (g == t + 1 ? c0[1] + c1[3] : 0.0f);
+  for (int i = 0; i < 4; ++i)
+    asm("{\n\t.reg .b16 al, ah, bl, bh;\n\t"
+        "mov.b32 {al, ah}, %1;\n\t"
+        "mov.b32 {bl, bh}, %2;\n\t"
+        "fma.rn.f32.bf16 %0, al, bl, %0;\n\t"
+        "fma.rn.f32.bf16 %0, ah, bh, %0;\n\t}"
+        : "+f"(acc)
+        : "r"(x[i]), "r"(y[i]));
+  return acc;
+}
+
+// Named barrier of `count` threads that tells whether `ok` holds for all of them.
+__device__ __forceinline__ bool bar_all(int id, int count, bool ok) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"((int)ok)
+      : "memory");
+  return r != 0;
 }
 
 __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
@@ -146,6 +142,9 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM_BAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM_BAR + B_COUNT * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM_BAR + B_COUNT * 8 + 4);
+  // items, -1 behind the last: of a step (published with its tiles), and of dq, dk on their way out
+  volatile int* step_item = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* out_item = step_item + 4;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = P.Hv / P.Hk;
 
@@ -163,7 +162,11 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
     if (!locate(blockIdx.x, ch, slot, hk)) return;  // nothing allocated yet
   }
   if (tid == 0) {
-    for (int i = 0; i < B_COUNT; ++i) mbar_init(&bars[i], i == B_KQE || i == B_HE ? 9 : 1);
+    for (int i = 0; i < B_COUNT; ++i) {
+      const bool all = i == B_HE || i == B_HE + 1 || i == B_SE || i == B_KQE;
+      const bool epi = i == B_NM || i == B_D || i == B_O || i == B_O + 1;
+      mbar_init(&bars[i], all ? 9 : epi ? 8 : 1);  // 8 epilogue warps, one commit
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -204,11 +207,15 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
     const int quad = warp & 3, half = warp >> 2;
     const int row = 32 * quad + lane;  // epilogue A: row of [dO; dW]; epilogue B: channel
     const uint32_t lo = (uint32_t)(32 * quad) << 16;
-    for (int64_t it = blockIdx.x;; it += gridDim.x, ++y) {
+    for (;; ++y) {
+      // all warps leave together: the named barriers need every one of them
+      const bool got = wait_w(B_H + (x & 1), (x >> 1) & 1);
+      if (!bar_all(NB_E, NB_EPI, got)) break;
+      const int it = step_item[x & 3];
       Chunk ch;
       int64_t slot;
       int hk;
-      if (!locate(it, ch, slot, hk)) break;
+      if (it < 0 || !locate(it, ch, slot, hk)) break;
       const int L = ch.L;
       // tokens 32 half + 2 q, + 1 of channel `row`: dq, dk summed over the heads, and q, k
       f32x2 aq[16], ak[16];
@@ -222,8 +229,10 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
         const int h = hk * G + gi;
         float* red = reinterpret_cast<float*>(smem + SM_RED) + (x & 1) * RED_FLOATS;
         float* sums = red + 256;  // [8] <S, dS>, [8] k.dKw of the state part
-        const float* gd = reinterpret_cast<const float*>(smem + SM_GD + (x & 1) * GD_BYTES);
-        const bool in = wait_w(B_H, x & 1);
+        const float* gd = reinterpret_cast<const float*>(smem + SM_GD + (x & 3) * GD_BYTES);
+        const bool in = wait_w(B_H + (x & 1), (x >> 1) & 1);
+        // seen: the next use may be published; at the end of an item dq and dk go through the buffer first
+        if (lane == 0 && gi < G - 1) mbar_arrive(&bars[B_HE + (x & 1)]);
         // ---- epilogue A
         const int r = row & 63;
         float diag = 0.0f;
@@ -268,12 +277,20 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        named_bar(NB_NM, NB_ALL);  // [dN; dM] written, D2 read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_NM]);  // [dN; dM] written, D2 read
         // ---- <S, dS>, dbeta; q and k of the item
         float fr = 0.0f;
-        if (in) fr = dot_rows16(sbase + SM_S, sbase + SM_DS, warp, lane);
+        if (wait_w(B_S, x & 1)) {
+          const uint4* s = reinterpret_cast<const uint4*>(smem + SM_S) + tid;
+          const uint4* ds = reinterpret_cast<const uint4*>(smem + SM_DS) + tid;
+          float f[4] = {};
+#pragma unroll
+          for (int q = 0; q < 8; ++q) f[q & 3] = dot8(s[q * 256], ds[q * 256], f[q & 3]);
+          fr = (f[0] + f[1]) + (f[2] + f[3]);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_HE]);
+        if (lane == 0) mbar_arrive(&bars[B_SE]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) fr += __shfl_xor_sync(0xffffffffu, fr, o);
         if (lane == 0) sums[warp] = fr;
@@ -296,6 +313,8 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
                       (uint32_t) * reinterpret_cast<const uint16_t*>(p1 + 8192) << 16;
             }
           }
+        }
+        if (gi == 0) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[B_KQE]);  // this warp needs K and Q no more
         }
@@ -360,9 +379,8 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
           if (lane == 0) sums[8 + warp] = kws;
         }
         tc_fence_before();
-        named_bar_arrive(NB_D, NB_ALL);  // D1, D3, D4, D5 read
-        if (tid == 0 && gi == G - 1) bulk_wait_read<0>();  // the previous item's dq and dk have left
         __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_D]);  // D1, D3, D4, D5 read
         named_bar(NB_E, NB_EPI);         // dgamma parts and sums of all warps
         // ---- dg: suffix sums over the chunk, and what leaves through the state
         const bool live = __all_sync(0xffffffffu, !*abort_flag) != 0;
@@ -407,9 +425,9 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
         }
       }
       // ---- dq, dk: two bytes at a time into shared memory (a warp's 32 channels are 64 consecutive
-      // bytes), out as boxes of tensor maps; a partial chunk row by row
+      // bytes) where dO and dW were, out as boxes of tensor maps; a partial chunk row by row
       if (L == tm::C) {
-        unsigned char* tile = smem + SM_OUT + (row >> 6) * 8192 + half * 4096 + (row & 7) * 2;
+        unsigned char* tile = smem + SM_OW + ((x - 1) & 1) * 32768 + (row >> 6) * 8192 + half * 4096 + (row & 7) * 2;
         const uint32_t c8 = ((uint32_t)row & 63) >> 3;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
@@ -440,18 +458,13 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
           }
         }
       }
-      named_bar(NB_O, NB_EPI);
-      if (tid == 0 && L == tm::C && !*abort_flag) {
-        const int32_t t0 = (int32_t)ch.t0;
-        tma_store_3d(&map_dq, smem + SM_OUT, 0, hk, t0);
-        tma_store_3d(&map_dq, smem + SM_OUT + 8192, 64, hk, t0);
-        tma_store_3d(&map_dk, smem + SM_OUT + 16384, 0, hk, t0);
-        tma_store_3d(&map_dk, smem + SM_OUT + 24576, 64, hk, t0);
-        bulk_commit();
-      }
       __syncwarp();
+      if (tid == 0) out_item[y & 1] = it;
+      if (lane == 0) mbar_arrive(&bars[B_O + (y & 1)]);
     }
-    if (tid == 0) bulk_wait<0>();  // nothing on its way out of shared memory
+    if (tid == 0) out_item[y & 1] = -1;
+    if (lane == 0) mbar_arrive(&bars[B_O + (y & 1)]);
+    __syncwarp();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
     if (warp == W_PROD) {
@@ -464,6 +477,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
     }
     uint32_t fix = 0;
     bool stop = false;
+    int z = 0;  // copies of S and dS
     // Copies of one group of tiles, published on `full`.  Rows behind the sequence end hold whatever
     // follows in memory: a partial chunk's copies are awaited here and those rows cleared (`tiles`
     // 64-row half tiles one after the other from `clear`) before the group is published.
@@ -500,7 +514,8 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
       }
       return __shfl_sync(0xffffffffu, (int)go, 0) != 0;
     };
-    for (int64_t it = blockIdx.x; !stop; it += gridDim.x) {
+    for (int it = blockIdx.x, next = 0;; it = next) {
+      if (lane == 0) next = (int)gridDim.x + atomicAdd(P.next, 1);  // used an item later
       Chunk ch;
       int64_t slot;
       int hk;
@@ -509,25 +524,33 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
       for (int gi = 0; gi < G; ++gi) {
         const int h = hk * G + gi;
         const size_t sh = (size_t)slot * P.Hv + h;
-        if (!may(B_HE, x)) {
-          stop = true;
-          break;
-        }
-        if (!group(B_H, TX_HEAD, ch.L, smem + SM_OW, 4, [&](uint64_t* fb) {
-              tma_load_3d(smem + SM_OW, &map_do, fb, 0, h, t0);
-              tma_load_3d(smem + SM_OW + 8192, &map_dv, fb, 0, h, t0);
-              tma_load_3d(smem + SM_OW + 16384, &map_do, fb, 64, h, t0);
-              tma_load_3d(smem + SM_OW + 24576, &map_dv, fb, 64, h, t0);
-              bulk_load(smem + SM_U, P.ws + P.at.u + sh * 16384, 16384, fb);
-              bulk_load(smem + SM_S, P.ws + P.at.s + sh * 32768, 32768, fb);
-              bulk_load(smem + SM_DS, P.ws + P.at.ds + sh * 32768, 32768, fb);
-              bulk_load(smem + SM_GD + (x & 1) * GD_BYTES, P.ws + P.at.gd + sh * GD_BYTES, GD_BYTES,
+        unsigned char* ow = smem + SM_OW + (x & 1) * 32768;
+        const bool go = may(B_HE + (x & 1), x >> 1);
+        if (go && lane == 0) step_item[x & 3] = it;
+        __syncwarp();
+        if (!go ||
+            !group(B_H + (x & 1), TX_HEAD, ch.L, ow, 4, [&](uint64_t* fb) {
+              tma_load_3d(ow, &map_do, fb, 0, h, t0);
+              tma_load_3d(ow + 8192, &map_dv, fb, 0, h, t0);
+              tma_load_3d(ow + 16384, &map_do, fb, 64, h, t0);
+              tma_load_3d(ow + 24576, &map_dv, fb, 64, h, t0);
+              bulk_load(smem + SM_U + (x & 1) * 16384, P.ws + P.at.u + sh * 16384, 16384, fb);
+              bulk_load(smem + SM_GD + (x & 3) * GD_BYTES, P.ws + P.at.gd + sh * GD_BYTES, GD_BYTES,
                         fb);
             })) {
           stop = true;
           break;
         }
         ++x;
+        if (!may(B_SE, z) ||
+            !group(B_S, TX_STATE, tm::C, nullptr, 0, [&](uint64_t* fb) {
+              bulk_load(smem + SM_S, P.ws + P.at.s + sh * 32768, 32768, fb);
+              bulk_load(smem + SM_DS, P.ws + P.at.ds + sh * 32768, 32768, fb);
+            })) {
+          stop = true;
+          break;
+        }
+        ++z;
         if (gi == 0) {  // needed last: after the head's own tiles
           if (!may(B_KQE, y) ||
               !group(B_KQ, TX_KQ, ch.L, smem + SM_KQ, 4, [&](uint64_t* fb) {
@@ -542,12 +565,25 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
           ++y;
         }
       }
+      if (stop) break;
+      next = __shfl_sync(0xffffffffu, next, 0);
     }
     // never leave the CTA with copies still landing in shared memory (each wait bounded)
     if (lane == 0) {
-      if (x > 0 && !mbar_wait(&bars[B_H], (uint32_t)(x - 1) & 1)) report(P.status, GDN_ERR_TIMEOUT);
-      if (y > 0 && !mbar_wait(&bars[B_KQ], (uint32_t)(y - 1) & 1)) report(P.status, GDN_ERR_TIMEOUT);
+      bool ok = true;
+      for (int b = 0; b < 2; ++b)  // uses b, b + 2, ... of each buffer
+        if (x > b) ok = mbar_wait(&bars[B_H + b], (uint32_t)((x - 1 - b) >> 1) & 1) && ok;
+      if (z > 0) ok = mbar_wait(&bars[B_S], (uint32_t)(z - 1) & 1) && ok;
+      if (y > 0) ok = mbar_wait(&bars[B_KQ], (uint32_t)(y - 1) & 1) && ok;
+      if (!ok) report(P.status, GDN_ERR_TIMEOUT);
     }
+    __syncwarp();
+    // the end of the items, after the wait above: it is one more phase of the same barrier
+    if (!stop && may(B_HE + (x & 1), x >> 1) && lane == 0) {
+      step_item[x & 3] = -1;
+      mbar_arrive(&bars[B_H + (x & 1)]);
+    }
+    __syncwarp();
     } else if (warp == W_MMA) {
     // ------------------------------------------------------------------ MMA issuer -----------
     const uint32_t id_p = idesc_bf16(128, 64, 0, 1);    // A = [dO; dW] K-major, B = U^T MN-major
@@ -563,43 +599,46 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
     const uint64_t dNn = sdesc_sw128(sbase + SM_NM, 8192, 1024);
     const uint64_t dMn = sdesc_sw128(sbase + SM_NM + 8192, 8192, 1024);
     auto live = [&]() { return __all_sync(0xffffffffu, !*abort_flag) != 0; };
-    for (int64_t it = blockIdx.x;; it += gridDim.x, ++y) {
-      Chunk ch;
-      int64_t slot;
-      int hk;
-      if (!locate(it, ch, slot, hk)) break;
-      for (int gi = 0; gi < G; ++gi, ++x) {
-        const bool have = wait_w(B_H, x & 1);
-        if (have && live()) {
-          tc_fence_after();
-          // D2 was read before the previous step's NB_NM
-          if (elect_one()) {
+    auto products_p = [&](int k) {  // MMA_p of step k: the previous step's B_NM said that D2 is read
+      const bool have = wait_w(B_H + (k & 1), (k >> 1) & 1) && step_item[k & 3] >= 0 && live();
+      if (have) {
+        tc_fence_after();
+        const uint64_t ow = dadd(dOW, (k & 1) * 32768), u = dadd(dU, (k & 1) * 16384);
+        if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              mma_bf16_ss(tmem + TM_D2, dadd(dOW, (ks >> 2) * 16384 + (ks & 3) * 32),
-                          dadd(dU, ks * 2048), id_p, ks > 0);
-            mma_commit(&bars[B_P]);
-          }
+          for (int ks = 0; ks < 8; ++ks)
+            mma_bf16_ss(tmem + TM_D2, dadd(ow, (ks >> 2) * 16384 + (ks & 3) * 32),
+                        dadd(u, ks * 2048), id_p, ks > 0);
+          mma_commit(&bars[B_P]);
         }
-        __syncwarp();
-        if (x > 0) named_bar(NB_D, NB_ALL);  // the previous step's D1, D3, D4, D5 are read
+      }
+      __syncwarp();
+      return have;
+    };
+    for (bool have = products_p(0); have; ++y) {
+      for (int gi = 0; gi < G; ++gi, ++x) {
+        const bool st = wait_w(B_S, x & 1);
+        const bool d = x == 0 || wait_w(B_D, (x - 1) & 1);  // the previous step's D1, D3, D4, D5 are read
+        have = have && st && d;
         if (have && live()) {
           tc_fence_after();
+          const uint64_t ow = dadd(dOW, (x & 1) * 32768), u = dadd(dU, (x & 1) * 16384);
           if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
               mma_bf16_ss(tmem + TM_D1, dadd(dSt, ks * 2048),
-                          dadd(dOW, (ks >> 2) * 16384 + (ks & 3) * 32), id_d1, ks > 0);
+                          dadd(ow, (ks >> 2) * 16384 + (ks & 3) * 32), id_d1, ks > 0);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              mma_bf16_ss(tmem + TM_D3, dadd(dDSt, ks * 2048), dadd(dU, ks * 2048), id_d3, ks > 0);
-            mma_commit(&bars[B_HE]);
+              mma_bf16_ss(tmem + TM_D3, dadd(dDSt, ks * 2048), dadd(u, ks * 2048), id_d3, ks > 0);
+            mma_commit(&bars[B_SE]);
+            mma_commit(&bars[B_HE + (x & 1)]);
           }
         }
         __syncwarp();
         const bool kq = wait_w(B_KQ, y & 1);
-        named_bar(NB_NM, NB_ALL);  // [dN; dM] written
-        if (have && kq && live()) {
+        const bool nm = wait_w(B_NM, x & 1);  // [dN; dM] written
+        if (have && kq && nm && live()) {
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -616,13 +655,39 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
           }
         }
         __syncwarp();
+        have = have && products_p(x + 1);
       }
     }
-    if (x > 0) named_bar(NB_D, NB_ALL);  // the last step's arrivals
     if (elect_one()) {
       mma_commit(&bars[B_DRAIN]);
       if (!mbar_wait(&bars[B_DRAIN], 0)) fail(GDN_ERR_TIMEOUT);
     }
+    __syncwarp();
+    } else if (warp == W_OUT) {
+    // ------------------------------------------------------------------ dq, dk ---------------
+    for (;; ++y) {
+      if (!wait_w(B_O + (y & 1), (y >> 1) & 1)) break;
+      const int it = out_item[y & 1];
+      Chunk ch;
+      int64_t slot;
+      int hk;
+      if (it < 0 || !locate(it, ch, slot, hk)) break;
+      x += G;
+      const int b = (x - 1) & 1;
+      if (lane == 0 && ch.L == tm::C && !*abort_flag) {
+        const unsigned char* out = smem + SM_OW + b * 32768;
+        const int32_t t0 = (int32_t)ch.t0;
+        tma_store_3d(&map_dq, out, 0, hk, t0);
+        tma_store_3d(&map_dq, out + 8192, 64, hk, t0);
+        tma_store_3d(&map_dk, out + 16384, 0, hk, t0);
+        tma_store_3d(&map_dk, out + 24576, 64, hk, t0);
+        bulk_commit();
+        bulk_wait_read<0>();
+      }
+      __syncwarp();
+      if (lane < 8) mbar_arrive(&bars[B_HE + b]);  // in place of the epilogue warps
+    }
+    if (lane == 0) bulk_wait<0>();  // nothing on its way out of shared memory
     __syncwarp();
     }
   }
@@ -644,6 +709,7 @@ cudaError_t launch_bwd_grads(const Args& a, cudaStream_t s) {
   p.S0 = a.S0;
   p.cu = a.cu;
   p.ws = ws;
+  p.next = reinterpret_cast<int*>(ws + 8);  // zero at the start of the call
   p.dq = (__nv_bfloat16*)a.dq;
   p.dk = (__nv_bfloat16*)a.dk_;
   p.dv = (__nv_bfloat16*)a.dv_;
