@@ -112,6 +112,7 @@ __device__ __forceinline__ bool find_chunk(const int32_t* cu, int64_t T, int N, 
 // persistent block reads each entry of cu_seqlens about once.
 struct ChunkCursor {
   int m = 0;
+  bool bad = false;  // a malformed entry was met (and reported)
   int64_t base = 0, a = -1, b = -1;  // sequence m: slot of its first chunk, its tokens (a < 0: not read yet)
   __device__ __forceinline__ bool find(const int32_t* cu, int64_t T, int N, int C, int64_t slot,
                                        Chunk& ch, int* status) {
@@ -123,6 +124,7 @@ struct ChunkCursor {
         if (a < 0 || b < a || b > T) {
           if (threadIdx.x == 0) report(status, GDN_ERR_DEVICE_ARG);
           a = -1;
+          bad = true;
           return false;
         }
       }

@@ -208,10 +208,19 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
   };
   // 1: `I` is a chunk; 0: past the last chunk (so is every later item); -1: malformed cu_seqlens
   // (reported; nothing may be read through it).  Uniform across the CTA.
+  bwd::ChunkCursor cursor;
   auto locate = [&](int64_t it, Item& I) -> int {
     I.it = it;
     I.slot = it / P.Hk;
     I.hk = (int)(it - I.slot * P.Hk);
+    if (BWD) {
+      bwd::Chunk ch;
+      if (!cursor.find(P.cu, P.T, P.N, tm::C, I.slot, ch, P.status)) return cursor.bad ? -1 : 0;
+      I.t0 = ch.t0;
+      I.s_end = ch.t0 + ch.L;
+      I.L = ch.L;
+      return 1;
+    }
     int n = -1;
     int64_t s_beg = 0;
     if (!P.cu) {
@@ -261,6 +270,34 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
     }
   };
 
+  // this lane's gate values (tokens lane, 32 + lane) of a v-head
+  auto gates = [&](const Item& I, int h, float& x0, float& x1, float& b0, float& b1) {
+    const int64_t t0 = I.t0;
+    const int L = I.L;
+    x0 = x1 = b0 = b1 = 0.f;
+    if (P.a) {
+      // the gates of the layer: beta = sigmoid(b), g = -exp(A_log) softplus(a + dt_bias)
+      const float ea = expf(__ldg(P.A_log + h)), db = __ldg(P.dt_bias + h);
+      if (lane < L) {
+        x0 = -ea * softplusf_(__bfloat162float(P.a[(t0 + lane) * P.Hv + h]) + db);
+        b0 = sigmoidf_(__bfloat162float(P.b[(t0 + lane) * P.Hv + h]));
+      }
+      if (32 + lane < L) {
+        x1 = -ea * softplusf_(__bfloat162float(P.a[(t0 + 32 + lane) * P.Hv + h]) + db);
+        b1 = sigmoidf_(__bfloat162float(P.b[(t0 + 32 + lane) * P.Hv + h]));
+      }
+    } else {
+      if (lane < L) {
+        x0 = P.g[(t0 + lane) * P.Hv + h];
+        b0 = P.beta[(t0 + lane) * P.Hv + h];
+      }
+      if (32 + lane < L) {
+        x1 = P.g[(t0 + 32 + lane) * P.Hv + h];
+        b1 = P.beta[(t0 + 32 + lane) * P.Hv + h];
+      }
+    }
+  };
+
   Item cur;
   int st = locate(blockIdx.x, cur);
   if (st <= 0) return;  // nothing allocated yet
@@ -304,42 +341,25 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
   PP_TS(1);
   uint32_t mma_phase = 0;
   bool ok = true;
+  float nx0 = 0.f, nx1 = 0.f, nb0 = 0.f, nb1 = 0.f;  // BWD: gates of this warp's next head
+  if (BWD && warp < min(PAIR, G)) gates(cur, cur.hk * G + warp, nx0, nx1, nb0, nb1);
   while (st > 0 && ok) {
     const int64_t slot = cur.slot, t0 = cur.t0;
     const int hk = cur.hk, L = cur.L;
     Item nxt;
     const int nst = locate(cur.it + gridDim.x, nxt);
     float* gl2_all = reinterpret_cast<float*>(smem + PP_GB);
-    const float* gxp = P.g;
-    const float* bxp = P.beta;
   for (int h0 = 0; h0 < G; h0 += PAIR) {
     const int npair = min(PAIR, G - h0);
     // ---- cumulative log-decays (x log2 e) and betas of the pair's v-heads (warp gi: head gi)
     if (warp < npair) {
       const int h = hk * G + h0 + warp;
       float* gl2 = gl2_all + warp * 128;
-      float x0 = 0.f, x1 = 0.f, b0 = 0.f, b1 = 0.f;
-      if (P.a) {
-        // the gates of the layer: beta = sigmoid(b), g = -exp(A_log) softplus(a + dt_bias)
-        const float ea = expf(__ldg(P.A_log + h)), db = __ldg(P.dt_bias + h);
-        if (lane < L) {
-          x0 = -ea * softplusf_(__bfloat162float(P.a[(t0 + lane) * P.Hv + h]) + db);
-          b0 = sigmoidf_(__bfloat162float(P.b[(t0 + lane) * P.Hv + h]));
-        }
-        if (32 + lane < L) {
-          x1 = -ea * softplusf_(__bfloat162float(P.a[(t0 + 32 + lane) * P.Hv + h]) + db);
-          b1 = sigmoidf_(__bfloat162float(P.b[(t0 + 32 + lane) * P.Hv + h]));
-        }
-      } else {
-        if (lane < L) {
-          x0 = gxp[(t0 + lane) * P.Hv + h];
-          b0 = bxp[(t0 + lane) * P.Hv + h];
-        }
-        if (32 + lane < L) {
-          x1 = gxp[(t0 + 32 + lane) * P.Hv + h];
-          b1 = bxp[(t0 + 32 + lane) * P.Hv + h];
-        }
-      }
+      float x0, x1, b0, b1;
+      if (BWD)
+        x0 = nx0, x1 = nx1, b0 = nb0, b1 = nb1;  // fetched an item ahead
+      else
+        gates(cur, h, x0, x1, b0, b1);
       if (BWD) {
         if (lane < L) b0 = bwd::floor_beta(b0);
         if (32 + lane < L) b1 = bwd::floor_beta(b1);
@@ -367,24 +387,43 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
     tc_fence_before();
     if (!__syncthreads_and(ok)) break;
     tc_fence_after();
-    // scale Gamma Q of the pair as the swizzled image of two 64-column halves.  From global memory (L2):
-    // the shared-memory copy is about to be replaced.
+    // scale Gamma Q of the pair as the swizzled image of two 64-column halves.  A thread takes the parts of Q
+    // that issue_loads has it replace next; later pairs of the item find them in L2 only.
     if (BWD) {
-      for (int e = tid; e < npair * 1024; e += PP_THREADS) {
-        const int gi = e >> 10, r = (e >> 4) & 63, ch = e & 15;
-        const int h = hk * G + h0 + gi;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (r < L) {
-          w = *reinterpret_cast<const uint4*>(P.q + (t0 + r) * P.q_stride + hk * tm::D + ch * 8);
+      uint4 w[4];
+      const int ch = tid & 15;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = (tid >> 4) + 16 * i;
+        if (h0 == 0)  // rows >= L are zero there
+          w[i] = *reinterpret_cast<const uint4*>(smem + PP_KQ + (ch >> 3) * 16384 + 8192 +
+                                                 sw128(r, (ch & 7) * 8));
+        else
+          w[i] = r < L ? *reinterpret_cast<const uint4*>(P.q + (t0 + r) * P.q_stride + hk * tm::D +
+                                                         ch * 8)
+                       : make_uint4(0u, 0u, 0u, 0u);
+      }
+      for (int gi = 0; gi < npair; ++gi) {
+        unsigned char* out = P.ws + P.qg_off + ((size_t)slot * P.Hv + hk * G + h0 + gi) * 16384 +
+                             (ch >> 3) * 8192;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = (tid >> 4) + 16 * i;
           const float f = P.scale * ex2f(gl2_all[gi * 128 + r]);
-          uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+          const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          uint32_t y[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            x[q] = pack_bf16x2(f * __uint_as_float(x[q] << 16),
-                               f * __uint_as_float(x[q] & 0xffff0000u));
+            y[q] = pack_bf16x2(f * __uint_as_float(x[q] << 16), f * __uint_as_float(x[q] & 0xffff0000u));
+          *reinterpret_cast<uint4*>(out + sw128(r, (ch & 7) * 8)) = make_uint4(y[0], y[1], y[2], y[3]);
         }
-        *reinterpret_cast<uint4*>(P.ws + P.qg_off + ((size_t)slot * P.Hv + h) * 16384 +
-                                  (ch >> 3) * 8192 + sw128(r, (ch & 7) * 8)) = w;
+      }
+      // the next head's gates, while this pair is worked on
+      if (h0 + PAIR < G) {
+        if (warp < min(PAIR, G - h0 - PAIR))
+          gates(cur, hk * G + h0 + PAIR + warp, nx0, nx1, nb0, nb1);
+      } else if (nst > 0 && warp < min(PAIR, G)) {
+        gates(nxt, nxt.hk * G + warp, nx0, nx1, nb0, nb1);
       }
     }
     // the MMA has read [K; Q]: the next item's K and Q may land there while this one is worked on
@@ -454,16 +493,17 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
       PP_TS(4);
       // T' = T diag(beta), zero above the diagonal -> rows 0..63 of the [T'; P] tile
       unsigned char* tp = P.ws + tm::tp_offset() + ((size_t)slot * P.Hv + h) * tm::TP_BYTES;
-      const int r = t4 >> 1, s0 = 32 * (t4 & 1);
-      float tv[32];
 #pragma unroll
-      for (int q = 0; q < 32; ++q) {
-        const int s = s0 + q;
-        tv[q] = (s <= r) ? (BWD ? Tf[r * AS + s] : Tf[r * AS + s] * gl2[64 + s]) : 0.0f;
+      for (int i = 0; i < 4; ++i) {  // a warp writes whole rows
+        const int r = (t4 >> 3) + 16 * i, s0 = 8 * (t4 & 7);
+        float tv[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int s = s0 + q;
+          tv[q] = (s <= r) ? (BWD ? Tf[r * AS + s] : Tf[r * AS + s] * gl2[64 + s]) : 0.0f;
+        }
+        *reinterpret_cast<uint4*>(tp + (size_t)r * 128 + s0 * 2) = pack8(tv);
       }
-      uint4* dst = reinterpret_cast<uint4*>(tp + (size_t)r * 128 + s0 * 2);
-#pragma unroll
-      for (int q8 = 0; q8 < 4; ++q8) dst[q8] = pack8(tv + 8 * q8);
       // Gamma_r and d_s (gamma is constant past the sequence end, so gamma_63 is the chunk's total)
       if (t4 < 64) {
         constexpr size_t gd_bytes = BWD ? bwd::GD_BYTES : tm::GD_BYTES;
