@@ -23,6 +23,11 @@ inline size_t elem(gdn_dtype d) { return d == GDN_BF16 ? 2 : 4; }
 inline gdn_status from_cuda(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 inline bool ptr_ok(const void* p) { return p != nullptr && aligned16(p); }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// whether every pointer (null is fine) lies on a multiple of `bytes`, a power of two
+template <typename... Ptr>
+inline bool aligned_to(size_t bytes, Ptr... p) {
+  return (((reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0) && ...);
+}
 
 // A range of device memory that a call reads or writes; ranges without a pointer or bytes overlap
 // nothing.
@@ -103,6 +108,9 @@ gdn_status gdn_gates_bwd(const void* a, const void* b, gdn_dtype dtype, const fl
   if (bad_dtype(dtype) || n_tok < 0 || Hv < 1) return GDN_ERR_INVALID_ARG;
   if (!A_log || !dt_bias || !dA_log || !ddt_bias) return GDN_ERR_INVALID_ARG;
   if (n_tok > 0 && (!a || !b || !dg || !dbeta || !da || !db)) return GDN_ERR_INVALID_ARG;
+  if (!aligned_to(elem(dtype), a, b, dg, dbeta, da, db) ||
+      !aligned_to(4, A_log, dt_bias, dA_log, ddt_bias))
+    return GDN_ERR_INVALID_ARG;
   if (!ws_ok(workspace, workspace_bytes, gdn_gates_bwd_workspace_size(n_tok, Hv)))
     return GDN_ERR_INVALID_ARG;
   const size_t n = (size_t)n_tok * Hv * elem(dtype), hb = (size_t)Hv * sizeof(float);
@@ -159,7 +167,7 @@ gdn_status gdn_gated_rmsnorm_ckpt8(const void* x, const void* z, gdn_dtype dtype
   if (!norm_dim_ok(dim)) return GDN_ERR_UNSUPPORTED;
   if (n_rows == 0) return GDN_OK;
   if (!ptr_ok(x) || !ptr_ok(z) || !ptr_ok(y) || !w || !ptr_ok(x_codes) || !ptr_ok(z_codes) ||
-      !x_scales || !z_scales || !aligned4(x_scales) || !aligned4(z_scales))
+      !x_scales || !z_scales || !aligned_to(4, w, x_scales, z_scales))
     return GDN_ERR_INVALID_ARG;
   const size_t n = (size_t)n_rows * dim, sb = (size_t)n_rows * sizeof(float);
   const Span in[] = {{z, n * elem(dtype)}, {w, dim * sizeof(float)}};
@@ -193,7 +201,7 @@ gdn_status gdn_gated_rmsnorm_bwd(const void* dy, const void* x, const float* x_s
   if ((x_scales == nullptr) != (z_scales == nullptr)) return GDN_ERR_INVALID_ARG;
   if (n_rows > 0 && (!ptr_ok(dy) || !ptr_ok(x) || !ptr_ok(z) || !ptr_ok(dx) || !ptr_ok(dz)))
     return GDN_ERR_INVALID_ARG;
-  if (!aligned4(x_scales) || !aligned4(z_scales)) return GDN_ERR_INVALID_ARG;
+  if (!aligned_to(4, x_scales, z_scales, w, dw)) return GDN_ERR_INVALID_ARG;
   const size_t n = (size_t)n_rows * dim, nb = n * elem(dtype), kept = x_scales ? n : nb;
   const size_t sb = x_scales ? (size_t)n_rows * sizeof(float) : 0, wb = dim * sizeof(float);
   const Span in[] = {{dy, nb}, {x, kept}, {z, kept}, {x_scales, sb}, {z_scales, sb}, {w, wb}};
@@ -238,7 +246,9 @@ gdn_status gdn_causal_conv1d_silu_bwd(const void* dy, const void* x, const float
   if (cu_seqlens && n_tok > 0 && N < 1) return GDN_ERR_INVALID_ARG;
   if (!w || !dw || (bias != nullptr) != (dbias != nullptr)) return GDN_ERR_INVALID_ARG;
   if (n_tok > 0 && (!ptr_ok(dy) || !ptr_ok(x) || !ptr_ok(dx))) return GDN_ERR_INVALID_ARG;
-  if (!aligned4(x_scales) || !aligned4(cu_seqlens)) return GDN_ERR_INVALID_ARG;
+  if (!aligned_to(4, x_scales, cu_seqlens, w, bias, conv_state_in, dconv_state_out, dw, dbias,
+                  dconv_state_in))
+    return GDN_ERR_INVALID_ARG;
   if (!ws_ok(workspace, workspace_bytes, gdn_causal_conv1d_silu_bwd_workspace_size(B, T, C, K)))
     return GDN_ERR_INVALID_ARG;
   const size_t n = (size_t)n_tok * C, nb = n * elem(dtype);
@@ -325,8 +335,8 @@ gdn_status gdn_chunk_bwd(const void* q, int64_t q_tok_stride, const void* k, int
                     !ptr_ok(dout) || !ptr_ok(dq) || !ptr_ok(dk_out) || !ptr_ok(dv_out) || !dg ||
                     !dbeta))
     return GDN_ERR_INVALID_ARG;
-  if (!aligned16(initial_state) || !aligned16(dfinal_state) || !aligned16(dinitial_state) ||
-      !aligned4(cu_seqlens))
+  if (!aligned_to(16, initial_state, dfinal_state, dinitial_state) || !aligned4(cu_seqlens) ||
+      !aligned_to(elem(dtype), dg, dbeta))
     return GDN_ERR_INVALID_ARG;
   const size_t e = elem(dtype), st = (size_t)N * Hv * dv * dk * sizeof(float);
   const size_t hk = (size_t)Hk * dk, hv = (size_t)Hv * dv, nt = (size_t)n_tok;

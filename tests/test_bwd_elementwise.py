@@ -491,3 +491,33 @@ def test_binding_refusals():
     with pytest.raises(gdn.GdnError):  # the library's own refusal: a workspace that is too small
         gdn.gdn_gates_bwd(z(4, 8), z(4, 8), z(8, dt=f32), z(8, dt=f32), z(4, 8), z(4, 8),
                           workspace=z(64, dt=torch.uint8))
+
+
+@no_gpu
+def test_addresses_between_elements_are_refused():
+    """Vectors that are read one element at a time have to lie on a multiple of that element."""
+    lib = gdn.load()
+    gates = lambda **o: lib.gdn_gates_bwd(*[o.get(n, d) for n, d in dict(
+        a=at(1), b=at(2), dt=o.get("dt", 0), A=at(3), bi=at(4), dg=at(5), de=at(6), n=64, Hv=8, da=at(7), db=at(8),
+        dA=at(9), dbi=at(10), ws=at(11), wsb=BIG, st=None).items()])
+    for n, i in dict(a=1, b=2, dg=5, de=6, da=7, db=8).items():
+        assert gates(**{n: at(i) + 1}) == E and gates(**{n: at(i) + 2}, dt=1) == E, n
+    for n, i in dict(A=3, bi=4, dA=9, dbi=10).items():
+        assert gates(**{n: at(i) + 2}) == E, n
+    norm = lambda **o: lib.gdn_gated_rmsnorm_bwd(*[o.get(n, d) for n, d in dict(
+        dy=at(1), x=at(2), xs=None, z=at(3), zs=None, dt=0, w=at(4), eps=1e-6, n=64, dim=128, dx=at(5), dz=at(6),
+        dw=at(7), ws=at(8), wsb=BIG, st=None).items()])
+    assert norm(w=at(4) + 2) == E and norm(dw=at(7) + 1) == E
+    assert norm(xs=at(9) + 2, zs=at(10)) == E
+    assert lib.gdn_gated_rmsnorm_ckpt8(at(1), at(2), 0, at(8) + 2, 1e-6, 64, 128, at(3), at(4), at(5), at(6), at(7),
+                                       None) == E
+    conv = lambda **o: lib.gdn_causal_conv1d_silu_bwd(*[o.get(n, d) for n, d in dict(
+        dy=at(1), x=at(2), xs=None, xg=0, dt=0, w=at(3), bias=at(7), B=1, T=64, C=256, K=4, cu=None, N=1, l2=0,
+        group=0, eps=1e-6, h=at(8), dl=at(9), dx=at(4), dw=at(5), db=at(10), dh=at(12), ws=at(6), wsb=BIG,
+        st=None).items()])
+    for n, i in dict(w=3, bias=7, h=8, dl=9, dw=5, db=10, dh=12).items():
+        assert conv(**{n: at(i) + 2}) == E, n
+    rule = lambda dt, dg, db: lib.gdn_chunk_bwd(
+        at(1), 256, at(2), 256, at(3), 512, at(4), at(5), at(6), dt, 0.1, None, None, None, 1, 1, 64, 2, 4, 128, 128,
+        64, at(7), at(8), at(9), dg, db, None, at(64), 1 << 40, None)
+    assert rule(0, at(10) + 1, at(11)) == E and rule(0, at(10), at(11) + 1) == E and rule(1, at(10) + 2, at(11)) == E
