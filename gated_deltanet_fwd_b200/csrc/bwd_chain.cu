@@ -15,9 +15,11 @@
 //     W  = X T~                N 64,  K 64    critical: dW^T = dV^T
 //     dS = Gamma_63 dS + dO^T (scale Gamma Q) - (Gamma W) K     N 128, K 64 twice, the second critical
 // Warp roles (512 threads): warps 0-7 the critical epilogues (warps w and w + 4 share 32 lanes and split the
-// columns) and, while the first product of a chunk runs, the carried matrix scaled by Gamma_63; warps 8-11
-// its bf16 copy, and U or dv, to memory; warp 12 the TMA producer; warp 13 the MMA issuer.  What bounds it is the latency of the critical sequence of
-// one chunk, not traffic.  Three things that shorten it, by clock stamps of a 64-chunk run:
+// columns) and, while the first product of a chunk runs, the carried matrix scaled by Gamma_63; warps
+// 8-11 its bf16 copy, and U or dv, to memory; warp 12 the TMA producer; warp 13 the MMA issuer.  What bounds
+// it is the latency of the critical sequence of one chunk, 3400 cycles forward and 3800 backward, not
+// traffic (32 v-heads, sequences of 16384, 8192, 6144 and 2048 tokens: 577 us for 2.8 GB).  Three things
+// that shorten it, by clock stamps of a 64-chunk run:
 //   - MMAs are issued under elect.sync, which tells the compiler that one thread is active, with
 //     descriptors that are loop-invariant but for constants (the stage is a template argument): about 10
 //     cycles apart, against 134 under a plain lane test and 45 with descriptors computed in the loop;
@@ -449,155 +451,155 @@ __device__ __forceinline__ void chain(const CUtensorMap* map_k, const CUtensorMa
   } else {
     if (BACK) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == W_PROD) {
-    // -------------------------------------------------------------- TMA producer -------------
-    if (elect_one()) {
-      prefetch_tensormap(map_k);
-      prefetch_tensormap(map_x);
-      prefetch_tensormap(map_tp);
-    }
-    int issued = 0;
-    for (int i = 0; i < nch; ++i) {
-      const int st = i % L_::STAGES, c = chunk_of(i), L = rows_of(c);
-      bool go = true;
-      if (lane == 0) {
-        if (i >= L_::STAGES) go = wait(B_EMPTY0 + st, ((uint32_t)(i / L_::STAGES) & 1) ^ 1);
-        go = go && !*abort_flag;
-      }
-      if (!__shfl_sync(0xffffffffu, (int)go, 0)) break;
-      unsigned char* sp = smem + st * L_::STAGE;
-      // a partial chunk's copies are awaited here, on a barrier of their own
-      const bool part = L < tm::C;
-      uint64_t* fb = part ? &bars[B_FIX] : &bars[B_FULL0 + st];
+      // -------------------------------------------------------------- TMA producer -------------
       if (elect_one()) {
-        const int32_t t0 = (int32_t)(s_beg + (int64_t)tm::C * c);
-        const size_t sh = (size_t)(slot0 + c) * P.Hv + h;
-        mbar_arrive_expect_tx(fb, L_::TX);
-        tma_load_3d(sp + L_::K, map_k, fb, 0, hk, t0);
-        tma_load_3d(sp + L_::K + 8192, map_k, fb, 64, hk, t0);
-        if (BACK) {
-          bulk_load(sp + L_::Q, P.ws + P.at.qg + sh * 16384, 16384, fb);
-        }
-        tma_load_3d(sp + L_::X, map_x, fb, 0, h, t0);
-        tma_load_3d(sp + L_::X + 8192, map_x, fb, 64, h, t0);
-        tma_load_2d(sp + L_::TP, map_tp, fb, 0, (int32_t)(sh * 128));
-        bulk_load(sp + L_::GD, P.ws + P.at.gd + sh * GD_BYTES, GD_BYTES, fb);
+        prefetch_tensormap(map_k);
+        prefetch_tensormap(map_x);
+        prefetch_tensormap(map_tp);
       }
-      if (part) {  // once per sequence: its last chunk
-        bool ok = mbar_wait(fb, 0);
-        if (!ok && lane == 0) fail(GDN_ERR_TIMEOUT);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          constexpr int TILES = BACK ? 6 : 4;  // 64-row half tiles of K, [Q,] X, one after the other
-          for (int e = lane; e < TILES * (tm::C - L) * 8; e += 32) {
-            const int tile = e / ((tm::C - L) * 8), rest = e - tile * ((tm::C - L) * 8);
-            *reinterpret_cast<uint4*>(sp + tile * 8192 + (L + rest / 8) * 128 + (rest % 8) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+      int issued = 0;
+      for (int i = 0; i < nch; ++i) {
+        const int st = i % L_::STAGES, c = chunk_of(i), L = rows_of(c);
+        bool go = true;
+        if (lane == 0) {
+          if (i >= L_::STAGES) go = wait(B_EMPTY0 + st, ((uint32_t)(i / L_::STAGES) & 1) ^ 1);
+          go = go && !*abort_flag;
+        }
+        if (!__shfl_sync(0xffffffffu, (int)go, 0)) break;
+        unsigned char* sp = smem + st * L_::STAGE;
+        // a partial chunk's copies are awaited here, on a barrier of their own
+        const bool part = L < tm::C;
+        uint64_t* fb = part ? &bars[B_FIX] : &bars[B_FULL0 + st];
+        if (elect_one()) {
+          const int32_t t0 = (int32_t)(s_beg + (int64_t)tm::C * c);
+          const size_t sh = (size_t)(slot0 + c) * P.Hv + h;
+          mbar_arrive_expect_tx(fb, L_::TX);
+          tma_load_3d(sp + L_::K, map_k, fb, 0, hk, t0);
+          tma_load_3d(sp + L_::K + 8192, map_k, fb, 64, hk, t0);
+          if (BACK) {
+            bulk_load(sp + L_::Q, P.ws + P.at.qg + sh * 16384, 16384, fb);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[B_FULL0 + st]);
-        } else {
-          mbar_wait(fb, 0);  // its copies may still be under way
-          break;
+          tma_load_3d(sp + L_::X, map_x, fb, 0, h, t0);
+          tma_load_3d(sp + L_::X + 8192, map_x, fb, 64, h, t0);
+          tma_load_2d(sp + L_::TP, map_tp, fb, 0, (int32_t)(sh * 128));
+          bulk_load(sp + L_::GD, P.ws + P.at.gd + sh * GD_BYTES, GD_BYTES, fb);
         }
+        if (part) {  // once per sequence: its last chunk
+          bool ok = mbar_wait(fb, 0);
+          if (!ok && lane == 0) fail(GDN_ERR_TIMEOUT);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            constexpr int TILES = BACK ? 6 : 4;  // 64-row half tiles of K, [Q,] X, one after the other
+            for (int e = lane; e < TILES * (tm::C - L) * 8; e += 32) {
+              const int tile = e / ((tm::C - L) * 8), rest = e - tile * ((tm::C - L) * 8);
+              *reinterpret_cast<uint4*>(sp + tile * 8192 + (L + rest / 8) * 128 + (rest % 8) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_FULL0 + st]);
+          } else {
+            mbar_wait(fb, 0);  // its copies may still be under way
+            break;
+          }
+        }
+        issued = i + 1;
       }
-      issued = i + 1;
-    }
-    // never leave the CTA with copies still landing in shared memory (each wait bounded)
-    if (lane == 0)
-      for (int i = issued > L_::STAGES ? issued - L_::STAGES : 0; i < issued; ++i)
-        if (!mbar_wait(&bars[B_FULL0 + i % L_::STAGES], (uint32_t)(i / L_::STAGES) & 1))
-          report(P.status, GDN_ERR_TIMEOUT);
+      // never leave the CTA with copies still landing in shared memory (each wait bounded)
+      if (lane == 0)
+        for (int i = issued > L_::STAGES ? issued - L_::STAGES : 0; i < issued; ++i)
+          if (!mbar_wait(&bars[B_FULL0 + i % L_::STAGES], (uint32_t)(i / L_::STAGES) & 1))
+            report(P.status, GDN_ERR_TIMEOUT);
     } else if (warp == W_MMA) {
-    // -------------------------------------------------------------- MMA issuer ---------------
-    const uint32_t id_k = idesc_bf16(128, 64, 0, 0);             // A tensor memory, B K-major
-    const uint32_t id_e = idesc_bf16(128, 64, 1, BACK ? 1 : 0);  // A smem MN-major
-    const uint32_t id_u = idesc_bf16(128, 64, 0, BACK ? 1 : 0);  // T~^T forward, T~ backward
-    const uint32_t id_s = idesc_bf16(128, 128, 0, 1);            // B = K, MN-major
-    const uint32_t id_q = idesc_bf16(128, 128, 1, 1);            // A = dO^T, B = scale Gamma Q
-    const uint64_t dK0 = sdesc_sw128(sbase + L_::K, 16, 1024);       // K as K-major B
-    const uint64_t dKn0 = sdesc_sw128(sbase + L_::K, 8192, 1024);    // K as MN-major B
-    const uint64_t dQn0 = sdesc_sw128(sbase + L_::Q, 8192, 1024);    // scale Gamma Q as MN-major B
-    const uint64_t dXt0 = sdesc_sw128(sbase + L_::X, 8192, 1024);    // V^T / dO^T as MN-major A
-    const uint64_t dT0 = BACK ? sdesc_sw128(sbase + L_::TP, 8192, 1024)   // T~ as MN-major B
-                              : sdesc_sw128(sbase + L_::TP, 16, 1024);    // T~ as K-major B
-    const uint64_t dP0 = sdesc_sw128(sbase + L_::TP + 8192, 8192, 1024);  // P as MN-major B
-    constexpr uint32_t t_step = BACK ? 2048 : 32;
-    auto step = [&](auto stage, int i) {
-      constexpr uint32_t o = decltype(stage)::value * L_::STAGE;
-      // the chunk's tiles have landed and nothing failed so far; a failure later in the chunk leaves its
-      // MMAs to run on whatever is there, in bounds all the same
-      const bool go = wait_full(i) && __all_sync(0xffffffffu, !*abort_flag);
-      if (BACK && go) {  // state-independent; D2 was read before the previous chunk's NB_U
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ss(tmem + TM_D2, dadd(dXt0, o + ks * 2048), dadd(dP0, o + ks * 2048), id_e,
-                        ks > 0);
-        }
-      }
-      __syncwarp();
-      named_bar(NB_S, NB_CSI);  // bf16 copy in place, U / dW of the previous chunk read
-      if (go) {
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_bf16_ts(tmem + TM_D, tmem + TM_SB + 8 * ks,
-                        dadd(dK0, o + (ks >> 2) * 8192 + (ks & 3) * 32), id_k, ks > 0);
-          mma_commit(&bars[B_K]);
-          if (!BACK) {  // state-independent, while X' is formed
+      // -------------------------------------------------------------- MMA issuer ---------------
+      const uint32_t id_k = idesc_bf16(128, 64, 0, 0);             // A tensor memory, B K-major
+      const uint32_t id_e = idesc_bf16(128, 64, 1, BACK ? 1 : 0);  // A smem MN-major
+      const uint32_t id_u = idesc_bf16(128, 64, 0, BACK ? 1 : 0);  // T~^T forward, T~ backward
+      const uint32_t id_s = idesc_bf16(128, 128, 0, 1);            // B = K, MN-major
+      const uint32_t id_q = idesc_bf16(128, 128, 1, 1);            // A = dO^T, B = scale Gamma Q
+      const uint64_t dK0 = sdesc_sw128(sbase + L_::K, 16, 1024);       // K as K-major B
+      const uint64_t dKn0 = sdesc_sw128(sbase + L_::K, 8192, 1024);    // K as MN-major B
+      const uint64_t dQn0 = sdesc_sw128(sbase + L_::Q, 8192, 1024);    // scale Gamma Q as MN-major B
+      const uint64_t dXt0 = sdesc_sw128(sbase + L_::X, 8192, 1024);    // V^T / dO^T as MN-major A
+      const uint64_t dT0 = BACK ? sdesc_sw128(sbase + L_::TP, 8192, 1024)   // T~ as MN-major B
+                                : sdesc_sw128(sbase + L_::TP, 16, 1024);    // T~ as K-major B
+      const uint64_t dP0 = sdesc_sw128(sbase + L_::TP + 8192, 8192, 1024);  // P as MN-major B
+      constexpr uint32_t t_step = BACK ? 2048 : 32;
+      auto step = [&](auto stage, int i) {
+        constexpr uint32_t o = decltype(stage)::value * L_::STAGE;
+        // the chunk's tiles have landed and nothing failed so far; a failure later in the chunk leaves its
+        // MMAs to run on whatever is there, in bounds all the same
+        const bool go = wait_full(i) && __all_sync(0xffffffffu, !*abort_flag);
+        if (BACK && go) {  // state-independent; D2 was read before the previous chunk's NB_U
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_bf16_ss(tmem + TM_U, dadd(dXt0, o + ks * 2048), dadd(dT0, o + ks * 32), id_e,
+              mma_bf16_ss(tmem + TM_D2, dadd(dXt0, o + ks * 2048), dadd(dP0, o + ks * 2048), id_e,
                           ks > 0);
           }
         }
-      }
-      __syncwarp();
-      named_bar(NB_X, NB_CI);  // X' written, matrix scaled
-      if (go) {
-        tc_fence_after();
-        if (elect_one()) {
+        __syncwarp();
+        named_bar(NB_S, NB_CSI);  // bf16 copy in place, U / dW of the previous chunk read
+        if (go) {
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ts(tmem + TM_U, tmem + TM_X + 8 * ks, dadd(dT0, o + ks * t_step), id_u,
-                        !BACK || ks > 0);
-          mma_commit(&bars[B_U]);
-          if (BACK) {
+            for (int ks = 0; ks < 8; ++ks)
+              mma_bf16_ts(tmem + TM_D, tmem + TM_SB + 8 * ks,
+                          dadd(dK0, o + (ks >> 2) * 8192 + (ks & 3) * 32), id_k, ks > 0);
+            mma_commit(&bars[B_K]);
+            if (!BACK) {  // state-independent, while X' is formed
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_bf16_ss(tmem + TM_S, dadd(dXt0, o + ks * 2048), dadd(dQn0, o + ks * 2048), id_q,
-                          1);
+              for (int ks = 0; ks < 4; ++ks)
+                mma_bf16_ss(tmem + TM_U, dadd(dXt0, o + ks * 2048), dadd(dT0, o + ks * 32), id_e,
+                            ks > 0);
+            }
           }
         }
-      }
-      __syncwarp();
-      named_bar(NB_U, NB_CSI);  // the update's operand written
-      if (go) {
-        tc_fence_after();
-        if (elect_one()) {
+        __syncwarp();
+        named_bar(NB_X, NB_CI);  // X' written, matrix scaled
+        if (go) {
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ts(tmem + TM_S, tmem + TM_UD + 8 * ks, dadd(dKn0, o + ks * 2048), id_s, 1);
-          mma_commit(&bars[B_S]);
-          mma_commit(&bars[B_EMPTY0 + decltype(stage)::value]);
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_ts(tmem + TM_U, tmem + TM_X + 8 * ks, dadd(dT0, o + ks * t_step), id_u,
+                          !BACK || ks > 0);
+            mma_commit(&bars[B_U]);
+            if (BACK) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_bf16_ss(tmem + TM_S, dadd(dXt0, o + ks * 2048), dadd(dQn0, o + ks * 2048), id_q,
+                            1);
+            }
+          }
         }
+        __syncwarp();
+        named_bar(NB_U, NB_CSI);  // the update's operand written
+        if (go) {
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_bf16_ts(tmem + TM_S, tmem + TM_UD + 8 * ks, dadd(dKn0, o + ks * 2048), id_s, 1);
+            mma_commit(&bars[B_S]);
+            mma_commit(&bars[B_EMPTY0 + decltype(stage)::value]);
+          }
+        }
+        __syncwarp();
+      };
+      for (int i = 0; i < nch; i += L_::STAGES) {
+        step(std::integral_constant<int, 0>(), i);
+        if (i + 1 < nch) step(std::integral_constant<int, 1>(), i + 1);
+        if (L_::STAGES > 2 && i + 2 < nch) step(std::integral_constant<int, L_::STAGES - 1>(), i + 2);
+      }
+      // every MMA has completed before tensor memory is read back or released
+      if (elect_one()) {
+        mma_commit(&bars[B_DRAIN]);
+        if (!mbar_wait(&bars[B_DRAIN], 0)) fail(GDN_ERR_TIMEOUT);
       }
       __syncwarp();
-    };
-    for (int i = 0; i < nch; i += L_::STAGES) {
-      step(std::integral_constant<int, 0>(), i);
-      if (i + 1 < nch) step(std::integral_constant<int, 1>(), i + 1);
-      if (L_::STAGES > 2 && i + 2 < nch) step(std::integral_constant<int, L_::STAGES - 1>(), i + 2);
-    }
-    // every MMA has completed before tensor memory is read back or released
-    if (elect_one()) {
-      mma_commit(&bars[B_DRAIN]);
-      if (!mbar_wait(&bars[B_DRAIN], 0)) fail(GDN_ERR_TIMEOUT);
-    }
-    __syncwarp();
     }
   }
 

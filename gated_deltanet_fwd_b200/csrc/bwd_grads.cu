@@ -468,227 +468,227 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
     if (warp == W_PROD) {
-    // ------------------------------------------------------------------ TMA producer ---------
-    if (elect_one()) {
-      prefetch_tensormap(&map_k);
-      prefetch_tensormap(&map_q);
-      prefetch_tensormap(&map_do);
-      prefetch_tensormap(&map_dv);
-    }
-    uint32_t fix = 0;
-    bool stop = false;
-    int z = 0;  // copies of S and dS
-    // Copies of one group of tiles, published on `full`.  Rows behind the sequence end hold whatever
-    // follows in memory: a partial chunk's copies are awaited here and those rows cleared (`tiles`
-    // 64-row half tiles one after the other from `clear`) before the group is published.
-    auto group = [&](int full, uint32_t bytes, int L, unsigned char* clear, int tiles, auto&& copy) {
-      const bool part = L < tm::C;
-      uint64_t* fb = &bars[part ? B_FIX : full];
+      // ------------------------------------------------------------------ TMA producer ---------
       if (elect_one()) {
-        mbar_arrive_expect_tx(fb, bytes);
-        copy(fb);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_do);
+        prefetch_tensormap(&map_dv);
       }
-      if (!part) return true;
-      bool ok = __all_sync(0xffffffffu, mbar_wait(fb, fix)) != 0;
-      fix ^= 1;
-      if (!ok) {
-        if (lane == 0) fail(GDN_ERR_TIMEOUT);
-        mbar_wait(fb, fix ^ 1);  // its copies may still be under way
-        return false;
-      }
-      for (int e = lane; e < tiles * (tm::C - L) * 8; e += 32) {
-        const int tile = e / ((tm::C - L) * 8), rest = e - tile * ((tm::C - L) * 8);
-        *reinterpret_cast<uint4*>(clear + tile * 8192 + (L + rest / 8) * 128 + (rest % 8) * 16) =
-            make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[full]);
-      return true;
-    };
-    auto may = [&](int b, int k) {  // the k-th use of a buffer: after its use k - 1 was released
-      bool go = true;
-      if (lane == 0) {
-        if (k > 0) go = wait(b, (uint32_t)(k - 1) & 1);
-        go = go && !*abort_flag;
-      }
-      return __shfl_sync(0xffffffffu, (int)go, 0) != 0;
-    };
-    for (int it = blockIdx.x, next = 0;; it = next) {
-      if (lane == 0) next = (int)gridDim.x + atomicAdd(P.next, 1);  // used an item later
-      Chunk ch;
-      int64_t slot;
-      int hk;
-      if (!locate(it, ch, slot, hk)) break;
-      const int32_t t0 = (int32_t)ch.t0;
-      for (int gi = 0; gi < G; ++gi) {
-        const int h = hk * G + gi;
-        const size_t sh = (size_t)slot * P.Hv + h;
-        unsigned char* ow = smem + SM_OW + (x & 1) * 32768;
-        const bool go = may(B_HE + (x & 1), x >> 1);
-        if (go && lane == 0) step_item[x & 3] = it;
+      uint32_t fix = 0;
+      bool stop = false;
+      int z = 0;  // copies of S and dS
+      // Copies of one group of tiles, published on `full`.  Rows behind the sequence end hold whatever
+      // follows in memory: a partial chunk's copies are awaited here and those rows cleared (`tiles`
+      // 64-row half tiles one after the other from `clear`) before the group is published.
+      auto group = [&](int full, uint32_t bytes, int L, unsigned char* clear, int tiles, auto&& copy) {
+        const bool part = L < tm::C;
+        uint64_t* fb = &bars[part ? B_FIX : full];
+        if (elect_one()) {
+          mbar_arrive_expect_tx(fb, bytes);
+          copy(fb);
+        }
+        if (!part) return true;
+        bool ok = __all_sync(0xffffffffu, mbar_wait(fb, fix)) != 0;
+        fix ^= 1;
+        if (!ok) {
+          if (lane == 0) fail(GDN_ERR_TIMEOUT);
+          mbar_wait(fb, fix ^ 1);  // its copies may still be under way
+          return false;
+        }
+        for (int e = lane; e < tiles * (tm::C - L) * 8; e += 32) {
+          const int tile = e / ((tm::C - L) * 8), rest = e - tile * ((tm::C - L) * 8);
+          *reinterpret_cast<uint4*>(clear + tile * 8192 + (L + rest / 8) * 128 + (rest % 8) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
         __syncwarp();
-        if (!go ||
-            !group(B_H + (x & 1), TX_HEAD, ch.L, ow, 4, [&](uint64_t* fb) {
-              tma_load_3d(ow, &map_do, fb, 0, h, t0);
-              tma_load_3d(ow + 8192, &map_dv, fb, 0, h, t0);
-              tma_load_3d(ow + 16384, &map_do, fb, 64, h, t0);
-              tma_load_3d(ow + 24576, &map_dv, fb, 64, h, t0);
-              bulk_load(smem + SM_U + (x & 1) * 16384, P.ws + P.at.u + sh * 16384, 16384, fb);
-              bulk_load(smem + SM_GD + (x & 3) * GD_BYTES, P.ws + P.at.gd + sh * GD_BYTES, GD_BYTES,
-                        fb);
-            })) {
-          stop = true;
-          break;
+        if (lane == 0) mbar_arrive(&bars[full]);
+        return true;
+      };
+      auto may = [&](int b, int k) {  // the k-th use of a buffer: after its use k - 1 was released
+        bool go = true;
+        if (lane == 0) {
+          if (k > 0) go = wait(b, (uint32_t)(k - 1) & 1);
+          go = go && !*abort_flag;
         }
-        ++x;
-        if (!may(B_SE, z) ||
-            !group(B_S, TX_STATE, tm::C, nullptr, 0, [&](uint64_t* fb) {
-              bulk_load(smem + SM_S, P.ws + P.at.s + sh * 32768, 32768, fb);
-              bulk_load(smem + SM_DS, P.ws + P.at.ds + sh * 32768, 32768, fb);
-            })) {
-          stop = true;
-          break;
-        }
-        ++z;
-        if (gi == 0) {  // needed last: after the head's own tiles
-          if (!may(B_KQE, y) ||
-              !group(B_KQ, TX_KQ, ch.L, smem + SM_KQ, 4, [&](uint64_t* fb) {
-                tma_load_3d(smem + SM_KQ, &map_k, fb, 0, hk, t0);
-                tma_load_3d(smem + SM_KQ + 8192, &map_q, fb, 0, hk, t0);
-                tma_load_3d(smem + SM_KQ + 16384, &map_k, fb, 64, hk, t0);
-                tma_load_3d(smem + SM_KQ + 24576, &map_q, fb, 64, hk, t0);
+        return __shfl_sync(0xffffffffu, (int)go, 0) != 0;
+      };
+      for (int it = blockIdx.x, next = 0;; it = next) {
+        if (lane == 0) next = (int)gridDim.x + atomicAdd(P.next, 1);  // used an item later
+        Chunk ch;
+        int64_t slot;
+        int hk;
+        if (!locate(it, ch, slot, hk)) break;
+        const int32_t t0 = (int32_t)ch.t0;
+        for (int gi = 0; gi < G; ++gi) {
+          const int h = hk * G + gi;
+          const size_t sh = (size_t)slot * P.Hv + h;
+          unsigned char* ow = smem + SM_OW + (x & 1) * 32768;
+          const bool go = may(B_HE + (x & 1), x >> 1);
+          if (go && lane == 0) step_item[x & 3] = it;
+          __syncwarp();
+          if (!go ||
+              !group(B_H + (x & 1), TX_HEAD, ch.L, ow, 4, [&](uint64_t* fb) {
+                tma_load_3d(ow, &map_do, fb, 0, h, t0);
+                tma_load_3d(ow + 8192, &map_dv, fb, 0, h, t0);
+                tma_load_3d(ow + 16384, &map_do, fb, 64, h, t0);
+                tma_load_3d(ow + 24576, &map_dv, fb, 64, h, t0);
+                bulk_load(smem + SM_U + (x & 1) * 16384, P.ws + P.at.u + sh * 16384, 16384, fb);
+                bulk_load(smem + SM_GD + (x & 3) * GD_BYTES, P.ws + P.at.gd + sh * GD_BYTES, GD_BYTES,
+                          fb);
               })) {
             stop = true;
             break;
           }
-          ++y;
+          ++x;
+          if (!may(B_SE, z) ||
+              !group(B_S, TX_STATE, tm::C, nullptr, 0, [&](uint64_t* fb) {
+                bulk_load(smem + SM_S, P.ws + P.at.s + sh * 32768, 32768, fb);
+                bulk_load(smem + SM_DS, P.ws + P.at.ds + sh * 32768, 32768, fb);
+              })) {
+            stop = true;
+            break;
+          }
+          ++z;
+          if (gi == 0) {  // needed last: after the head's own tiles
+            if (!may(B_KQE, y) ||
+                !group(B_KQ, TX_KQ, ch.L, smem + SM_KQ, 4, [&](uint64_t* fb) {
+                  tma_load_3d(smem + SM_KQ, &map_k, fb, 0, hk, t0);
+                  tma_load_3d(smem + SM_KQ + 8192, &map_q, fb, 0, hk, t0);
+                  tma_load_3d(smem + SM_KQ + 16384, &map_k, fb, 64, hk, t0);
+                  tma_load_3d(smem + SM_KQ + 24576, &map_q, fb, 64, hk, t0);
+                })) {
+              stop = true;
+              break;
+            }
+            ++y;
+          }
         }
+        if (stop) break;
+        next = __shfl_sync(0xffffffffu, next, 0);
       }
-      if (stop) break;
-      next = __shfl_sync(0xffffffffu, next, 0);
-    }
-    // never leave the CTA with copies still landing in shared memory (each wait bounded)
-    if (lane == 0) {
-      bool ok = true;
-      for (int b = 0; b < 2; ++b)  // uses b, b + 2, ... of each buffer
-        if (x > b) ok = mbar_wait(&bars[B_H + b], (uint32_t)((x - 1 - b) >> 1) & 1) && ok;
-      if (z > 0) ok = mbar_wait(&bars[B_S], (uint32_t)(z - 1) & 1) && ok;
-      if (y > 0) ok = mbar_wait(&bars[B_KQ], (uint32_t)(y - 1) & 1) && ok;
-      if (!ok) report(P.status, GDN_ERR_TIMEOUT);
-    }
-    __syncwarp();
-    // the end of the items, after the wait above: it is one more phase of the same barrier
-    if (!stop && may(B_HE + (x & 1), x >> 1) && lane == 0) {
-      step_item[x & 3] = -1;
-      mbar_arrive(&bars[B_H + (x & 1)]);
-    }
-    __syncwarp();
+      // never leave the CTA with copies still landing in shared memory (each wait bounded)
+      if (lane == 0) {
+        bool ok = true;
+        for (int b = 0; b < 2; ++b)  // uses b, b + 2, ... of each buffer
+          if (x > b) ok = mbar_wait(&bars[B_H + b], (uint32_t)((x - 1 - b) >> 1) & 1) && ok;
+        if (z > 0) ok = mbar_wait(&bars[B_S], (uint32_t)(z - 1) & 1) && ok;
+        if (y > 0) ok = mbar_wait(&bars[B_KQ], (uint32_t)(y - 1) & 1) && ok;
+        if (!ok) report(P.status, GDN_ERR_TIMEOUT);
+      }
+      __syncwarp();
+      // the end of the items, after the wait above: it is one more phase of the same barrier
+      if (!stop && may(B_HE + (x & 1), x >> 1) && lane == 0) {
+        step_item[x & 3] = -1;
+        mbar_arrive(&bars[B_H + (x & 1)]);
+      }
+      __syncwarp();
     } else if (warp == W_MMA) {
-    // ------------------------------------------------------------------ MMA issuer -----------
-    const uint32_t id_p = idesc_bf16(128, 64, 0, 1);    // A = [dO; dW] K-major, B = U^T MN-major
-    const uint32_t id_d1 = idesc_bf16(128, 128, 1, 0);  // A = S^T MN-major, B = [dO; dW] K-major
-    const uint32_t id_d3 = idesc_bf16(128, 64, 1, 1);   // A = dS^T, B = U^T; also Q^T, K^T with dN, dM
-    const uint64_t dOW = sdesc_sw128(sbase + SM_OW, 16, 1024);
-    const uint64_t dU = sdesc_sw128(sbase + SM_U, 16384, 1024);
-    const uint64_t dSt = sdesc_sw128(sbase + SM_S, 16384, 1024);
-    const uint64_t dDSt = sdesc_sw128(sbase + SM_DS, 16384, 1024);
-    const uint64_t dKt = sdesc_sw128(sbase + SM_KQ, 16384, 1024);
-    const uint64_t dQt = sdesc_sw128(sbase + SM_KQ + 8192, 16384, 1024);
-    const uint64_t dNM = sdesc_sw128(sbase + SM_NM, 16, 1024);
-    const uint64_t dNn = sdesc_sw128(sbase + SM_NM, 8192, 1024);
-    const uint64_t dMn = sdesc_sw128(sbase + SM_NM + 8192, 8192, 1024);
-    auto live = [&]() { return __all_sync(0xffffffffu, !*abort_flag) != 0; };
-    auto products_p = [&](int k) {  // MMA_p of step k: the previous step's B_NM said that D2 is read
-      const bool have = wait_w(B_H + (k & 1), (k >> 1) & 1) && step_item[k & 3] >= 0 && live();
-      if (have) {
-        tc_fence_after();
-        const uint64_t ow = dadd(dOW, (k & 1) * 32768), u = dadd(dU, (k & 1) * 16384);
-        if (elect_one()) {
+      // ------------------------------------------------------------------ MMA issuer -----------
+      const uint32_t id_p = idesc_bf16(128, 64, 0, 1);    // A = [dO; dW] K-major, B = U^T MN-major
+      const uint32_t id_d1 = idesc_bf16(128, 128, 1, 0);  // A = S^T MN-major, B = [dO; dW] K-major
+      const uint32_t id_d3 = idesc_bf16(128, 64, 1, 1);   // A = dS^T, B = U^T; also Q^T, K^T with dN, dM
+      const uint64_t dOW = sdesc_sw128(sbase + SM_OW, 16, 1024);
+      const uint64_t dU = sdesc_sw128(sbase + SM_U, 16384, 1024);
+      const uint64_t dSt = sdesc_sw128(sbase + SM_S, 16384, 1024);
+      const uint64_t dDSt = sdesc_sw128(sbase + SM_DS, 16384, 1024);
+      const uint64_t dKt = sdesc_sw128(sbase + SM_KQ, 16384, 1024);
+      const uint64_t dQt = sdesc_sw128(sbase + SM_KQ + 8192, 16384, 1024);
+      const uint64_t dNM = sdesc_sw128(sbase + SM_NM, 16, 1024);
+      const uint64_t dNn = sdesc_sw128(sbase + SM_NM, 8192, 1024);
+      const uint64_t dMn = sdesc_sw128(sbase + SM_NM + 8192, 8192, 1024);
+      auto live = [&]() { return __all_sync(0xffffffffu, !*abort_flag) != 0; };
+      auto products_p = [&](int k) {  // MMA_p of step k: the previous step's B_NM said that D2 is read
+        const bool have = wait_w(B_H + (k & 1), (k >> 1) & 1) && step_item[k & 3] >= 0 && live();
+        if (have) {
+          tc_fence_after();
+          const uint64_t ow = dadd(dOW, (k & 1) * 32768), u = dadd(dU, (k & 1) * 16384);
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_bf16_ss(tmem + TM_D2, dadd(ow, (ks >> 2) * 16384 + (ks & 3) * 32),
-                        dadd(u, ks * 2048), id_p, ks > 0);
-          mma_commit(&bars[B_P]);
+            for (int ks = 0; ks < 8; ++ks)
+              mma_bf16_ss(tmem + TM_D2, dadd(ow, (ks >> 2) * 16384 + (ks & 3) * 32),
+                          dadd(u, ks * 2048), id_p, ks > 0);
+            mma_commit(&bars[B_P]);
+          }
         }
+        __syncwarp();
+        return have;
+      };
+      for (bool have = products_p(0); have; ++y) {
+        for (int gi = 0; gi < G; ++gi, ++x) {
+          const bool st = wait_w(B_S, x & 1);
+          const bool d = x == 0 || wait_w(B_D, (x - 1) & 1);  // the previous step's D1, D3, D4, D5 are read
+          have = have && st && d;
+          if (have && live()) {
+            tc_fence_after();
+            const uint64_t ow = dadd(dOW, (x & 1) * 32768), u = dadd(dU, (x & 1) * 16384);
+            if (elect_one()) {
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                mma_bf16_ss(tmem + TM_D1, dadd(dSt, ks * 2048),
+                            dadd(ow, (ks >> 2) * 16384 + (ks & 3) * 32), id_d1, ks > 0);
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                mma_bf16_ss(tmem + TM_D3, dadd(dDSt, ks * 2048), dadd(u, ks * 2048), id_d3, ks > 0);
+              mma_commit(&bars[B_SE]);
+              mma_commit(&bars[B_HE + (x & 1)]);
+            }
+          }
+          __syncwarp();
+          const bool kq = wait_w(B_KQ, y & 1);
+          const bool nm = wait_w(B_NM, x & 1);  // [dN; dM] written
+          if (have && kq && nm && live()) {
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_bf16_ss(tmem + TM_D4, dadd(dKt, ks * 2048), dadd(dNM, ks * 32), id_d1, ks > 0);
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_bf16_ss(tmem + TM_D5, dadd(dQt, ks * 2048), dadd(dNn, ks * 2048), id_d3, ks > 0);
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_bf16_ss(tmem + TM_D5, dadd(dKt, ks * 2048), dadd(dMn, ks * 2048), id_d3, 1);
+              mma_commit(&bars[B_N]);
+              if (gi == G - 1) mma_commit(&bars[B_KQE]);
+            }
+          }
+          __syncwarp();
+          have = have && products_p(x + 1);
+        }
+      }
+      if (elect_one()) {
+        mma_commit(&bars[B_DRAIN]);
+        if (!mbar_wait(&bars[B_DRAIN], 0)) fail(GDN_ERR_TIMEOUT);
       }
       __syncwarp();
-      return have;
-    };
-    for (bool have = products_p(0); have; ++y) {
-      for (int gi = 0; gi < G; ++gi, ++x) {
-        const bool st = wait_w(B_S, x & 1);
-        const bool d = x == 0 || wait_w(B_D, (x - 1) & 1);  // the previous step's D1, D3, D4, D5 are read
-        have = have && st && d;
-        if (have && live()) {
-          tc_fence_after();
-          const uint64_t ow = dadd(dOW, (x & 1) * 32768), u = dadd(dU, (x & 1) * 16384);
-          if (elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              mma_bf16_ss(tmem + TM_D1, dadd(dSt, ks * 2048),
-                          dadd(ow, (ks >> 2) * 16384 + (ks & 3) * 32), id_d1, ks > 0);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              mma_bf16_ss(tmem + TM_D3, dadd(dDSt, ks * 2048), dadd(u, ks * 2048), id_d3, ks > 0);
-            mma_commit(&bars[B_SE]);
-            mma_commit(&bars[B_HE + (x & 1)]);
-          }
-        }
-        __syncwarp();
-        const bool kq = wait_w(B_KQ, y & 1);
-        const bool nm = wait_w(B_NM, x & 1);  // [dN; dM] written
-        if (have && kq && nm && live()) {
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_bf16_ss(tmem + TM_D4, dadd(dKt, ks * 2048), dadd(dNM, ks * 32), id_d1, ks > 0);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_bf16_ss(tmem + TM_D5, dadd(dQt, ks * 2048), dadd(dNn, ks * 2048), id_d3, ks > 0);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_bf16_ss(tmem + TM_D5, dadd(dKt, ks * 2048), dadd(dMn, ks * 2048), id_d3, 1);
-            mma_commit(&bars[B_N]);
-            if (gi == G - 1) mma_commit(&bars[B_KQE]);
-          }
-        }
-        __syncwarp();
-        have = have && products_p(x + 1);
-      }
-    }
-    if (elect_one()) {
-      mma_commit(&bars[B_DRAIN]);
-      if (!mbar_wait(&bars[B_DRAIN], 0)) fail(GDN_ERR_TIMEOUT);
-    }
-    __syncwarp();
     } else if (warp == W_OUT) {
-    // ------------------------------------------------------------------ dq, dk ---------------
-    for (;; ++y) {
-      if (!wait_w(B_O + (y & 1), (y >> 1) & 1)) break;
-      const int it = out_item[y & 1];
-      Chunk ch;
-      int64_t slot;
-      int hk;
-      if (it < 0 || !locate(it, ch, slot, hk)) break;
-      x += G;
-      const int b = (x - 1) & 1;
-      if (lane == 0 && ch.L == tm::C && !*abort_flag) {
-        const unsigned char* out = smem + SM_OW + b * 32768;
-        const int32_t t0 = (int32_t)ch.t0;
-        tma_store_3d(&map_dq, out, 0, hk, t0);
-        tma_store_3d(&map_dq, out + 8192, 64, hk, t0);
-        tma_store_3d(&map_dk, out + 16384, 0, hk, t0);
-        tma_store_3d(&map_dk, out + 24576, 64, hk, t0);
-        bulk_commit();
-        bulk_wait_read<0>();
+      // ------------------------------------------------------------------ dq, dk ---------------
+      for (;; ++y) {
+        if (!wait_w(B_O + (y & 1), (y >> 1) & 1)) break;
+        const int it = out_item[y & 1];
+        Chunk ch;
+        int64_t slot;
+        int hk;
+        if (it < 0 || !locate(it, ch, slot, hk)) break;
+        x += G;
+        const int b = (x - 1) & 1;
+        if (lane == 0 && ch.L == tm::C && !*abort_flag) {
+          const unsigned char* out = smem + SM_OW + b * 32768;
+          const int32_t t0 = (int32_t)ch.t0;
+          tma_store_3d(&map_dq, out, 0, hk, t0);
+          tma_store_3d(&map_dq, out + 8192, 64, hk, t0);
+          tma_store_3d(&map_dk, out + 16384, 0, hk, t0);
+          tma_store_3d(&map_dk, out + 24576, 64, hk, t0);
+          bulk_commit();
+          bulk_wait_read<0>();
+        }
+        __syncwarp();
+        if (lane < 8) mbar_arrive(&bars[B_HE + b]);  // in place of the epilogue warps
       }
+      if (lane == 0) bulk_wait<0>();  // nothing on its way out of shared memory
       __syncwarp();
-      if (lane < 8) mbar_arrive(&bars[B_HE + b]);  // in place of the epilogue warps
-    }
-    if (lane == 0) bulk_wait<0>();  // nothing on its way out of shared memory
-    __syncwarp();
     }
   }
   tc_fence_before();
