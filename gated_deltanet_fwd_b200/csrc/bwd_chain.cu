@@ -490,11 +490,7 @@ __device__ __forceinline__ void chain(const CUtensorMap* map_k, const CUtensorMa
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
             constexpr int TILES = BACK ? 6 : 4;  // 64-row half tiles of K, [Q,] X, one after the other
-            for (int e = lane; e < TILES * (tm::C - L) * 8; e += 32) {
-              const int tile = e / ((tm::C - L) * 8), rest = e - tile * ((tm::C - L) * 8);
-              *reinterpret_cast<uint4*>(sp + tile * 8192 + (L + rest / 8) * 128 + (rest % 8) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
+            clear_rows(sp, TILES, L, lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_FULL0 + st]);

@@ -496,11 +496,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
           mbar_wait(fb, fix ^ 1);  // its copies may still be under way
           return false;
         }
-        for (int e = lane; e < tiles * (tm::C - L) * 8; e += 32) {
-          const int tile = e / ((tm::C - L) * 8), rest = e - tile * ((tm::C - L) * 8);
-          *reinterpret_cast<uint4*>(clear + tile * 8192 + (L + rest / 8) * 128 + (rest % 8) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-        }
+        clear_rows(clear, tiles, L, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[full]);
