@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
   // item -> chunk and k-head; false past the last one or for a malformed cu_seqlens
   ChunkCursor cursor;
   auto locate = [&](int64_t it, Chunk& ch, int64_t& slot, int& hk) {
-    slot = it / P.Hk;
-    hk = (int)(it - slot * P.Hk);
+    slot = (uint32_t)it / (uint32_t)P.Hk;  // items fit 32 bits (launch_tc)
+    hk = (int)((uint32_t)it - (uint32_t)slot * (uint32_t)P.Hk);
     return it < P.items && cursor.find(P.cu, P.T, P.N, tm::C, slot, ch, P.status);
   };
   {
@@ -744,7 +744,10 @@ size_t tc_workspace_bytes(int N, int64_t n_tok, int Hv) {
 
 cudaError_t launch_tc(const Args& a, cudaStream_t s) {
   ChunkFusion f;
-  const TcLayout at = tc_layout(max_slots(a.N, (int64_t)a.B * a.T, tm::C), a.Hv);
+  const int64_t slots = max_slots(a.N, (int64_t)a.B * a.T, tm::C);
+  // rows of the [T~; P] tiles are TMA coordinates; all three kernels count in 32 bits
+  if (slots > 0x7fffffff / 128 / a.Hv) return cudaErrorInvalidConfiguration;
+  const TcLayout at = tc_layout(slots, a.Hv);
   f.bwd_gd_off = at.gd;
   f.bwd_qg_off = at.qg;
   f.scale = a.scale;

@@ -40,6 +40,7 @@ using namespace ptx;
 
 constexpr int PP_THREADS = 256;  // two warpgroups
 constexpr int AS = 68;           // fp32 row stride of the A and T matrices
+constexpr int PS = 144;          // byte stride of P's rows on their way out (BWD; in T's place)
 constexpr int MS = 20;           // fp32 row stride of the 16 x 16 block-product scratch
 constexpr int PAIR = 2;          // v-heads solved side by side (one per warpgroup)
 
@@ -211,9 +212,9 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
   bwd::ChunkCursor cursor;
   auto locate = [&](int64_t it, Item& I) -> int {
     I.it = it;
-    I.slot = it / P.Hk;
-    I.hk = (int)(it - I.slot * P.Hk);
-    if (BWD) {
+    if (BWD) {  // items fit 32 bits (launch_tc); the cursor reads each entry of cu_seqlens once
+      I.slot = (uint32_t)it / (uint32_t)P.Hk;
+      I.hk = (int)((uint32_t)it - (uint32_t)I.slot * (uint32_t)P.Hk);
       bwd::Chunk ch;
       if (!cursor.find(P.cu, P.T, P.N, tm::C, I.slot, ch, P.status)) return cursor.bad ? -1 : 0;
       I.t0 = ch.t0;
@@ -221,6 +222,8 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
       I.L = ch.L;
       return 1;
     }
+    I.slot = it / P.Hk;
+    I.hk = (int)(it - I.slot * P.Hk);
     int n = -1;
     int64_t s_beg = 0;
     if (!P.cu) {
@@ -320,7 +323,8 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid == 0) {
+    // under elect.sync the MMAs are issued some ten cycles apart, under a plain lane test 134
+    if (BWD ? warp == 0 && elect_one() : tid == 0) {
       const uint32_t id = idesc_bf16(128, 64, 0, 0);
       const uint64_t d0 = sdesc_sw128(sbase + PP_KQ, 16, 1024);
 #pragma unroll
@@ -432,7 +436,52 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
     // ---- decay masks straight out of tensor memory.  Thread: row R = 32 (warp & 3) + lane of
     // [K; Q], columns 32 (warp >> 2) .. + 31.  Rows 0..63 -> A (fp32, smem), 64..127 -> P (bf16,
     // workspace).  e^{gamma_r - gamma_s} = 2^{(gamma_r - gamma_s) log2 e}, never above 1.
-    {
+    if constexpr (BWD) {
+      // The same masks with the gates read four at a time, blocks above the diagonal skipped by whole warps,
+      // and P by way of shared memory (where T will be), to leave in whole rows: 16 bytes a lane, 128 apart,
+      // took most of this phase's 7500 cycles.
+      const int R = 32 * (warp & 3) + lane, r = R & 63, cb = 32 * (warp >> 2);
+      const bool keys = (warp & 3) < 2, above = cb > 0 && (warp & 1) == 0;
+      const int last = keys ? r - 1 : r;
+      float d[32];
+      if (!above) {
+        tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + cb, *reinterpret_cast<float(*)[16]>(d));
+        tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + cb + 16,
+                  *reinterpret_cast<float(*)[16]>(d + 16));
+        tmem_ld_wait();
+      }
+      for (int gi = 0; gi < npair; ++gi) {
+        const float* gl2 = gl2_all + gi * 128;
+        const float gr = gl2[r];
+        float* Af = reinterpret_cast<float*>(smem + PP_A) + gi * 64 * AS + r * AS + cb;
+        unsigned char* Pf = smem + PP_T + gi * 64 * AS * 4 + r * PS + cb * 2;
+#pragma unroll
+        for (int q8 = 0; q8 < 4; ++q8) {
+          float v[8] = {};
+          if (!above) {
+#pragma unroll
+            for (int q4 = 0; q4 < 2; ++q4) {
+              const int s0 = cb + 8 * q8 + 4 * q4;
+              const float4 g4 = *reinterpret_cast<const float4*>(gl2 + s0);
+              const float4 b4 = keys ? *reinterpret_cast<const float4*>(gl2 + 64 + s0)
+                                     : make_float4(P.scale, P.scale, P.scale, P.scale);
+              const float gs[4] = {g4.x, g4.y, g4.z, g4.w}, bs[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float x = bs[e] * ex2f(gr - gs[e]) * d[8 * q8 + 4 * q4 + e];
+                v[4 * q4 + e] = s0 + e <= last ? x : 0.0f;
+              }
+            }
+          }
+          if (keys) {
+            *reinterpret_cast<float4*>(Af + 8 * q8) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(Af + 8 * q8 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+          } else {
+            *reinterpret_cast<uint4*>(Pf + 16 * q8) = pack8(v);
+          }
+        }
+      }
+    } else {
       const int R = 32 * (warp & 3) + lane, r = R & 63, cb = 32 * (warp >> 2);
       float d[32];
       tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + cb, *reinterpret_cast<float(*)[16]>(d));
@@ -443,7 +492,7 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
         const int h = hk * G + h0 + gi;
         const float* gl2 = gl2_all + gi * 128;
         const float gr = gl2[r];
-        const float br = R < 64 && !BWD ? gl2[64 + r] : 1.0f;
+        const float br = R < 64 ? gl2[64 + r] : 1.0f;
         float v[32];
 #pragma unroll
         for (int b16 = 0; b16 < 2; ++b16) {
@@ -452,8 +501,7 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
             for (int q = 16 * b16; q < 16 * b16 + 16; ++q) {
               const int s = cb + q;
               const bool keep = R < 64 ? (s < r) : (s <= r);
-              const float bs = BWD ? (R < 64 ? gl2[64 + s] : P.scale) : br;
-              v[q] = keep ? bs * ex2f(gr - gl2[s]) * d[q] : 0.0f;
+              v[q] = keep ? br * ex2f(gr - gl2[s]) * d[q] : 0.0f;
             }
           } else {  // the 16 columns lie above the diagonal
 #pragma unroll
@@ -475,6 +523,19 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
       }
     }
     __syncthreads();  // A of every head of the pair complete
+    if (BWD) {
+      const int c8 = tid & 7;
+      for (int gi = 0; gi < npair; ++gi) {
+        unsigned char* tp = P.ws + tm::tp_offset() + ((size_t)slot * P.Hv + hk * G + h0 + gi) * tm::TP_BYTES;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = (tid >> 3) + 32 * i;
+          *reinterpret_cast<uint4*>(tp + (64 + r) * 128 + c8 * 16) =
+              *reinterpret_cast<const uint4*>(smem + PP_T + gi * 64 * AS * 4 + r * PS + c8 * 16);
+        }
+      }
+      if (!(h0 + PAIR >= G && nst > 0)) __syncthreads();  // else loads_then_mma has one: T may be written
+    }
     // after the last pair's masks D1 is free: the next item's MMA runs during this item's solve
     if (h0 + PAIR >= G && nst > 0) loads_then_mma(tmem);
     PP_TS(3);
