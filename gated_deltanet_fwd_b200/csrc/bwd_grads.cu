@@ -746,7 +746,7 @@ cudaError_t launch_tc(const Args& a, cudaStream_t s) {
   ChunkFusion f;
   const int64_t slots = max_slots(a.N, (int64_t)a.B * a.T, tm::C);
   // rows of the [T~; P] tiles are TMA coordinates; all three kernels count in 32 bits
-  if (slots > 0x7fffffff / 128 / a.Hv) return cudaErrorInvalidConfiguration;
+  if (slots > 0x7fffffff / 128 / a.Hv || (int64_t)a.B * a.T > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const TcLayout at = tc_layout(slots, a.Hv);
   f.bwd_gd_off = at.gd;
   f.bwd_qg_off = at.qg;

@@ -191,13 +191,16 @@ __device__ __forceinline__ void solve64(const float* Af, float* Tf, float* Mb, i
 }
 
 template <bool BWD>
-__global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepParams P) {
+__global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(
+    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_q,  // BWD
+    const PrepParams P) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + PP_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PP_BAR + 8);
+  uint64_t* lbar = reinterpret_cast<uint64_t*>(smem + PP_BAR + 16);  // BWD: K and Q of a whole chunk
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = P.Hv / P.Hk;
@@ -301,28 +304,56 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
     }
   };
 
+  // BWD: a whole chunk comes as boxes of tensor maps, which cost the warps no instructions; the rows behind
+  // a partial chunk have to read as zeros, so it goes through issue_loads
+  auto load_item = [&](const Item& I) {
+    if (!BWD || I.L < tm::C) {
+      issue_loads(I);
+    } else if (warp == 1 && elect_one()) {
+      const int32_t t = (int32_t)I.t0;
+      mbar_arrive_expect_tx(lbar, 32768);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        tma_load_3d(smem + PP_KQ + half * 16384, &map_k, lbar, 64 * half, I.hk, t);
+        tma_load_3d(smem + PP_KQ + half * 16384 + 8192, &map_q, lbar, 64 * half, I.hk, t);
+      }
+    }
+  };
+
   Item cur;
   int st = locate(blockIdx.x, cur);
   if (st <= 0) return;  // nothing allocated yet
   PP_TS(0);
   if (tid == 0) {
     mbar_init(bar, 1);
+    mbar_init(lbar, 1);
     fence_barrier_init();
   }
   if (warp == 0) {
     tmem_alloc(tmem_slot, 64);
     tmem_relinquish();
   }
-  issue_loads(cur);
+  if (!BWD) issue_loads(cur);
   // Once this thread's copies have landed: every thread's copies visible to the tensor core, then
   // D1 = [K; Q] K^T of the item in shared memory (rows 0..63 K K^T, rows 64..127 Q K^T; M = 128,
   // N = 64, K-dim 128) into tensor memory, completion signalled on `bar`.
-  auto loads_then_mma = [&](uint32_t tmem) {
-    cp_async_wait_all();
-    fence_proxy_async_smem();
+  uint32_t load_phase = 0;
+  auto loads_then_mma = [&](uint32_t tmem, int L) {
+    if (!BWD || L < tm::C) {
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (BWD && L == tm::C) {
+      if (warp == 0 && !mbar_wait(lbar, load_phase)) {
+        report(P.status, GDN_ERR_TIMEOUT);
+        mbar_wait(lbar, load_phase);  // its copies may still be under way
+      }
+      __syncwarp();
+      load_phase ^= 1;
+    }
     // under elect.sync the MMAs are issued some ten cycles apart, under a plain lane test 134
     if (BWD ? warp == 0 && elect_one() : tid == 0) {
       const uint32_t id = idesc_bf16(128, 64, 0, 0);
@@ -341,14 +372,15 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  loads_then_mma(tmem);
+  if (BWD) load_item(cur);  // the barriers are initialised
+  loads_then_mma(tmem, cur.L);
   PP_TS(1);
   uint32_t mma_phase = 0;
   bool ok = true;
   float nx0 = 0.f, nx1 = 0.f, nb0 = 0.f, nb1 = 0.f;  // BWD: gates of this warp's next head
   if (BWD && warp < min(PAIR, G)) gates(cur, cur.hk * G + warp, nx0, nx1, nb0, nb1);
   while (st > 0 && ok) {
-    const int64_t slot = cur.slot, t0 = cur.t0;
+    const int64_t slot = cur.slot;
     const int hk = cur.hk, L = cur.L;
     Item nxt;
     const int nst = locate(cur.it + gridDim.x, nxt);
@@ -391,21 +423,15 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
     tc_fence_before();
     if (!__syncthreads_and(ok)) break;
     tc_fence_after();
-    // scale Gamma Q of the pair as the swizzled image of two 64-column halves.  A thread takes the parts of Q
-    // that issue_loads has it replace next; later pairs of the item find them in L2 only.
+    // scale Gamma Q of the pair as the swizzled image of two 64-column halves
     if (BWD) {
       uint4 w[4];
       const int ch = tid & 15;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = (tid >> 4) + 16 * i;
-        if (h0 == 0)  // rows >= L are zero there
-          w[i] = *reinterpret_cast<const uint4*>(smem + PP_KQ + (ch >> 3) * 16384 + 8192 +
-                                                 sw128(r, (ch & 7) * 8));
-        else
-          w[i] = r < L ? *reinterpret_cast<const uint4*>(P.q + (t0 + r) * P.q_stride + hk * tm::D +
-                                                         ch * 8)
-                       : make_uint4(0u, 0u, 0u, 0u);
+        w[i] = *reinterpret_cast<const uint4*>(smem + PP_KQ + (ch >> 3) * 16384 + 8192 +
+                                               sw128(r, (ch & 7) * 8));
       }
       for (int gi = 0; gi < npair; ++gi) {
         unsigned char* out = P.ws + P.qg_off + ((size_t)slot * P.Hv + hk * G + h0 + gi) * 16384 +
@@ -430,8 +456,9 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
         gates(nxt, nxt.hk * G + warp, nx0, nx1, nb0, nb1);
       }
     }
-    // the MMA has read [K; Q]: the next item's K and Q may land there while this one is worked on
-    if (h0 == 0 && nst > 0) issue_loads(nxt);
+    // the MMA has read [K; Q]: the next item's K and Q may land there while this one is worked on (BWD:
+    // after the last pair's masks)
+    if (!BWD && h0 == 0 && nst > 0) issue_loads(nxt);
     PP_TS(2);
     // ---- decay masks straight out of tensor memory.  Thread: row R = 32 (warp & 3) + lane of
     // [K; Q], columns 32 (warp >> 2) .. + 31.  Rows 0..63 -> A (fp32, smem), 64..127 -> P (bf16,
@@ -524,6 +551,7 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
     }
     __syncthreads();  // A of every head of the pair complete
     if (BWD) {
+      if (h0 + PAIR >= G && nst > 0) load_item(nxt);  // Q was read before the barrier
       const int c8 = tid & 7;
       for (int gi = 0; gi < npair; ++gi) {
         unsigned char* tp = P.ws + tm::tp_offset() + ((size_t)slot * P.Hv + hk * G + h0 + gi) * tm::TP_BYTES;
@@ -534,10 +562,10 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
               *reinterpret_cast<const uint4*>(smem + PP_T + gi * 64 * AS * 4 + r * PS + c8 * 16);
         }
       }
-      if (!(h0 + PAIR >= G && nst > 0)) __syncthreads();  // else loads_then_mma has one: T may be written
+      __syncthreads();  // T may be written
     }
     // after the last pair's masks D1 is free: the next item's MMA runs during this item's solve
-    if (h0 + PAIR >= G && nst > 0) loads_then_mma(tmem);
+    if (!BWD && h0 + PAIR >= G && nst > 0) loads_then_mma(tmem, tm::C);
     PP_TS(3);
     // ---- T = (I + A)^{-1}: warpgroup gi solves head gi
     const int gi = warp >> 2, w4 = warp & 3, t4 = tid & 127;
@@ -578,7 +606,10 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(const PrepPar
         }
       }
     }
-    __syncthreads();  // gates / A / T buffers free for the next pair
+    if (BWD && h0 + PAIR >= G && nst > 0)
+      loads_then_mma(tmem, nxt.L);  // with the barrier below
+    else
+      __syncthreads();  // gates / A / T buffers free for the next pair
     PP_TS(5);
   }
     cur = nxt;
@@ -600,7 +631,8 @@ unsigned long long* g_prep_trace = nullptr;  // trace builds: device buffer of 8
 namespace {
 
 template <bool BWD>
-cudaError_t launch_prep_t(const PrepParams& p, int64_t slots, cudaStream_t s) {
+cudaError_t launch_prep_t(const PrepParams& p, int64_t slots, cudaStream_t s, const CUtensorMap& mk,
+                          const CUtensorMap& mq) {
   static int sms_of[64] = {};  // per device; idempotent, a benign race between host threads
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -620,7 +652,7 @@ cudaError_t launch_prep_t(const PrepParams& p, int64_t slots, cudaStream_t s) {
   // persistent: two CTAs per SM, each taking every grid-th (slot, k-head) item
   const int64_t items = slots * p.Hk;
   const int64_t grid = items < 2 * (int64_t)sms ? items : 2 * (int64_t)sms;
-  chunk_prep_kernel<BWD><<<(unsigned)grid, PP_THREADS, PP_SMEM, s>>>(p);
+  chunk_prep_kernel<BWD><<<(unsigned)grid, PP_THREADS, PP_SMEM, s>>>(mk, mq, p);
   return cudaGetLastError();
 }
 
@@ -656,7 +688,11 @@ cudaError_t launch_chunk_prep(const void* q, const void* k, TokStrides ts, const
   p.dt_bias = fuse.dt_bias;
   p.qg_off = (int64_t)fuse.bwd_qg_off;
   p.scale = fuse.scale;
-  return fuse.bwd_gd_off ? launch_prep_t<true>(p, slots, s) : launch_prep_t<false>(p, slots, s);
+  CUtensorMap mk = {}, mq = {};
+  if (!fuse.bwd_gd_off) return launch_prep_t<false>(p, slots, s, mk, mq);
+  if (!make_tok_map(&mk, k, Hk, n_tok, ts.k) || !make_tok_map(&mq, q, Hk, n_tok, ts.q))
+    return cudaErrorInvalidValue;
+  return launch_prep_t<true>(p, slots, s, mk, mq);
 }
 
 }  // namespace gdn
