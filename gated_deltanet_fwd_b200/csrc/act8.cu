@@ -4,6 +4,8 @@
 // HBM-bound: pack reads an activation and writes one byte (and 4 / group bytes of scale) for it, unpack
 // the reverse.  group / 8 lanes share a group (8 elements = one 16-byte bf16 load and one 8-byte code
 // store each), the maximum is a shuffle reduction, and each thread keeps ACT_U groups in flight.
+// 16384 rows of 8192 bf16 in groups of 128: pack 75 us, unpack 66 us for 407 MB each (5.4 and 6.2 TB/s; a
+// copy reaches 6.55).
 #include "act8.cuh"
 
 namespace gdn {

@@ -12,11 +12,12 @@
 //          D3 = dS^T U^T                M 128, N 64,  K 128        (raw dKw)
 //   MMA_n  D4 = K^T [dN; dM]^T          M 128, N 128, K 64
 //          D5 = Q^T dN + K^T dM         M 128, N 64,  K 64 twice
-// Epilogue A (token rows): decay masks on D2 -> [dN; dM] in shared memory as bf16 (with the diagonal of dN,
-// a token's own pair: its two contributions to dgamma are sums of the same rounded products and cancel
-// to fp32 rounding), dbeta from the diagonal of dW U^T, and <S, dS> from shared memory.  Epilogue B
+// Epilogue A (token rows): decay masks on D2 -> [dN; dM], strictly lower, in shared memory as bf16; from the
+// diagonals p (a token's own pair, which has no decay: added to dq and dk in fp32 and kept out of dgamma,
+// where only rounding errors would be left of it) and dbeta; and <S, dS> from shared memory.  Epilogue B
 // (channel rows): Gamma and d applied in fp32, dq and dk summed over the heads, dgamma = q.dq +
-// k.(dKe - dKw) reduced over channels; two tokens per instruction (fp32x2).
+// k.(dKe - D5) and kappa = k.(d D3) reduced over channels (bwd_simt.cu); two tokens per instruction
+// (fp32x2).
 // MMA_p of the next head runs beside epilogue B of this one.  [dO; dW] and U have two buffers; S and dS have one,
 // free again before epilogue B; dq and dk leave through the [dO; dW] buffer of the item's last step.  So the
 // loads of a step run beside the epilogues of the step before.
@@ -24,7 +25,8 @@
 // Warp roles (384 threads): warps 0-7 the epilogues (lane quarter warp % 4; columns, in epilogue B tokens,
 // split in two by warp / 4), warp 8 the TMA producer, warp 9 the MMA issuer, warp 10 sends dq and dk out.
 // Bounds: 144 KB of tiles per (chunk, v-head) at two v-heads a k-head against about 6 units of
-// 64 x 128 x 128 products: HBM, with the epilogues' instructions close behind.
+// 64 x 128 x 128 products: HBM, with the epilogues' instructions close behind.  16384 (chunk, v-head) pairs: 526
+// us for 2.6 GB, 5.0 TB/s (76 % of a copy); with loads behind the epilogues and a fixed share of items 565.
 // Bounded waits and the abort protocol as in bwd_chain.cu.
 #include "bwd_tc.cuh"
 #include "f32x2.cuh"
@@ -50,9 +52,10 @@ constexpr uint32_t SM_S = SM_U + 2 * 16384;   // S: two halves x 128 rows x 128 
 constexpr uint32_t SM_DS = SM_S + 32768;      // dS: the same
 constexpr uint32_t SM_NM = SM_DS + 32768;     // [dN; dM]: 128 rows x 128 B
 constexpr uint32_t SM_GD = SM_NM + 16384;     // four records: one is read until its step ends
-constexpr uint32_t SM_RED = SM_GD + 4 * GD_BYTES;  // 2 x (dgamma parts [4][64], sums [8] + [8])
-constexpr uint32_t RED_FLOATS = 4 * 64 + 16;
-constexpr uint32_t SM_BAR = SM_RED + 2 * RED_FLOATS * 4;
+constexpr uint32_t SM_RED = SM_GD + 4 * GD_BYTES;  // 2 x (dgamma and kappa parts, each [4][64], sums [8])
+constexpr uint32_t RED_FLOATS = 2 * 4 * 64 + 8;
+constexpr uint32_t SM_OWN = SM_RED + 2 * RED_FLOATS * 4;  // p [64]
+constexpr uint32_t SM_BAR = SM_OWN + 256;
 constexpr uint32_t SM_BYTES = SM_BAR + 192 + 1024;
 static_assert(SM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TX_KQ = 32768, TX_HEAD = 32768 + 16384 + GD_BYTES, TX_STATE = 65536;
@@ -228,11 +231,12 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
       for (int gi = 0; gi < G; ++gi, ++x) {
         const int h = hk * G + gi;
         float* red = reinterpret_cast<float*>(smem + SM_RED) + (x & 1) * RED_FLOATS;
-        float* sums = red + 256;  // [8] <S, dS>, [8] k.dKw of the state part
+        float* sums = red + 512;  // <S, dS>
         const float* gd = reinterpret_cast<const float*>(smem + SM_GD + (x & 3) * GD_BYTES);
         const bool in = wait_w(B_H + (x & 1), (x >> 1) & 1);
         // seen: the next use may be published; at the end of an item dq and dk go through the buffer first
         if (lane == 0 && gi < G - 1) mbar_arrive(&bars[B_HE + (x & 1)]);
+        float* own = reinterpret_cast<float*>(smem + SM_OWN);  // read before NB_E, written after it
         // ---- epilogue A
         const int r = row & 63;
         float diag = 0.0f;
@@ -247,7 +251,6 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
             for (int q = 0; q < 16; ++q) pk[q] = 0u;
           } else {
             const bool tri = half == (quad & 1);  // the block on the diagonal
-            const int last = row < 64 ? lane : lane - 1;
 #pragma unroll
             for (int q4 = 0; q4 < 8; ++q4) {
               const float4 gs = *reinterpret_cast<const float4*>(gd + 192 + 32 * half + 4 * q4);
@@ -255,12 +258,12 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
               if (tri) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (4 * q4 + e > last) v[e] = 0.0f;
+                  if (4 * q4 + e >= lane) v[e] = 0.0f;
               }
               pk[2 * q4] = pack2(mul * v[0] * d[4 * q4], mul * v[1] * d[4 * q4 + 1]);
               pk[2 * q4 + 1] = pack2(mul * v[2] * d[4 * q4 + 2], mul * v[3] * d[4 * q4 + 3]);
             }
-            if (tri && quad >= 2) {  // dW_r . U_r: column `lane` of this block, by halving
+            if (tri) {  // dO_r . U_r or dW_r . U_r: column `lane` of this block, by halving
 #pragma unroll
               for (int w = 16; w > 0; w >>= 1)
 #pragma unroll
@@ -269,6 +272,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
               diag = d[0];
             }
           }
+          if (quad < 2 && half == quad) own[row] = P.scale * diag;
           unsigned char* nm = smem + SM_NM;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -319,14 +323,14 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
           if (lane == 0) mbar_arrive(&bars[B_KQE]);  // this warp needs K and Q no more
         }
         // ---- epilogue B
-        if (wait_w(B_N, x & 1)) {
+        const bool own_ok = wait_w(B_NM, x & 1);  // p of all warps; long since
+        if (wait_w(B_N, x & 1) && own_ok) {
           tc_fence_after();
-          f32x2 kw = 0ull;
-          float keep = 0.0f;
+          float keep = 0.0f, keepk = 0.0f;
 #pragma unroll
           for (int b = 0; b < 4; ++b) {  // 8 tokens at a time
             const int t0 = 32 * half + 8 * b;
-            float d1a[8], d1b[8], d4a[8], d4b[8], d3[8], d5[8], v[8];
+            float d1a[8], d1b[8], d4a[8], d4b[8], d3[8], d5[8], v[8], kap[8];
             tmem_ld8(tmem + lo + TM_D1 + t0, d1a);
             tmem_ld8(tmem + lo + TM_D4 + t0, d4a);
             tmem_ld8(tmem + lo + TM_D1 + 64 + t0, d1b);
@@ -347,12 +351,15 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
                                     two(d4b[e], d4b[e + 1]));
               const f32x2 w1 = mul2(two(dd.x, dd.y), two(d3[e], d3[e + 1]));
               const f32x2 fw = add2(w1, two(d5[e], d5[e + 1]));
-              const float2 vv = parts(fma2(q2, fq, mul2(k2, fma2(neg, fw, fe))));
+              const float2 vv = parts(fma2(q2, fq, mul2(k2, fma2(neg, two(d5[e], d5[e + 1]), fe))));
               v[e] = vv.x;
               v[e + 1] = vv.y;
-              kw = fma2(k2, w1, kw);
-              aq[p] = add2(aq[p], fq);
-              ak[p] = add2(ak[p], add2(fe, fw));
+              const float2 kk = parts(mul2(k2, w1));
+              kap[e] = kk.x;
+              kap[e + 1] = kk.y;
+              const f32x2 o2 = *reinterpret_cast<const f32x2*>(own + t0 + e);
+              aq[p] = fma2(o2, k2, add2(aq[p], fq));
+              ak[p] = fma2(o2, q2, add2(ak[p], add2(fe, fw)));
             }
             // sum over the warp's 32 channels: halve the tokens a lane holds three times, then add the
             // four lanes that are left with the same token: token t0 + (lane >> 2)
@@ -364,19 +371,24 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
                 if (e < w) {
                   const float give = up ? v[e] : v[e + w], stay = up ? v[e + w] : v[e];
                   v[e] = stay + __shfl_xor_sync(0xffffffffu, give, 4 * w);
+                  const float givek = up ? kap[e] : kap[e + w], stayk = up ? kap[e + w] : kap[e];
+                  kap[e] = stayk + __shfl_xor_sync(0xffffffffu, givek, 4 * w);
                 }
               }
             }
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-            if ((lane & 3) == b) keep = v[0];  // lane 4 k + b ends up with token 8 b + k
+            // the last two steps for both sums at once: odd lanes go on with kappa
+            float o = lane & 1 ? kap[0] : v[0];
+            o += __shfl_xor_sync(0xffffffffu, lane & 1 ? v[0] : kap[0], 1);
+            o += __shfl_xor_sync(0xffffffffu, o, 2);
+            const float p = __shfl_xor_sync(0xffffffffu, o, 1);
+            if ((lane & 3) == b) {  // lane 4 k + b ends up with token 8 b + k
+              keep = lane & 1 ? p : o;
+              keepk = lane & 1 ? o : p;
+            }
           }
-          red[quad * 64 + 32 * half + 8 * (lane & 3) + (lane >> 2)] = keep;
-          const float2 k2 = parts(kw);
-          float kws = k2.x + k2.y;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) kws += __shfl_xor_sync(0xffffffffu, kws, o);
-          if (lane == 0) sums[8 + warp] = kws;
+          const int at = quad * 64 + 32 * half + 8 * (lane & 3) + (lane >> 2);
+          red[at] = keep;
+          red[256 + at] = keepk;
         }
         tc_fence_before();
         __syncwarp();
@@ -385,35 +397,45 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
         // ---- dg: suffix sums over the chunk, and what leaves through the state
         const bool live = __all_sync(0xffffffffu, !*abort_flag) != 0;
         if (warp == (x & 7) && live) {
-          float f = 0.0f, k2 = 0.0f;
+          float f = 0.0f;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            f += sums[q];
-            k2 += sums[8 + q];
-          }
-          f = fmaf(gd[63], f, k2);
-          float a0 = 0.0f, a1 = 0.0f;  // tokens lane and 32 + lane
+          for (int q = 0; q < 8; ++q) f += sums[q];
+          f *= gd[63];
+          float a0 = 0.0f, a1 = 0.0f, k0 = 0.0f, k1 = 0.0f;  // tokens lane and 32 + lane
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             a0 += red[q * 64 + lane];
             a1 += red[q * 64 + 32 + lane];
+            k0 += red[256 + q * 64 + lane];
+            k1 += red[256 + q * 64 + 32 + lane];
           }
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
             const float u0 = __shfl_down_sync(0xffffffffu, a0, o);
             const float u1 = __shfl_down_sync(0xffffffffu, a1, o);
+            const float l0 = __shfl_up_sync(0xffffffffu, k0, o);
+            const float l1 = __shfl_up_sync(0xffffffffu, k1, o);
             if (lane + o < 32) {
               a0 += u0;
               a1 += u1;
             }
+            if (lane >= o) {
+              k0 += l0;
+              k1 += l1;
+            }
           }
           a0 += __shfl_sync(0xffffffffu, a1, 0);
+          const float all0 = __shfl_sync(0xffffffffu, k0, 31);  // kappa of earlier tokens
+          k0 = __shfl_up_sync(0xffffffffu, k0, 1);
+          k1 = __shfl_up_sync(0xffffffffu, k1, 1);
+          k0 = lane > 0 ? k0 : 0.0f;
+          k1 = lane > 0 ? all0 + k1 : all0;
           // the first token's decay multiplies the initial state: without one its gradient is zero
           const bool none = ch.first && !P.S0;
           __nv_bfloat16* dst = P.dg + ch.t0 * P.Hv + h;
           if (lane < L)
-            dst[(int64_t)lane * P.Hv] = __float2bfloat16_rn(lane == 0 && none ? 0.0f : a0 + f);
-          if (32 + lane < L) dst[(int64_t)(32 + lane) * P.Hv] = __float2bfloat16_rn(a1 + f);
+            dst[(int64_t)lane * P.Hv] = __float2bfloat16_rn(lane == 0 && none ? 0.0f : a0 + f + k0);
+          if (32 + lane < L) dst[(int64_t)(32 + lane) * P.Hv] = __float2bfloat16_rn(a1 + f + k1);
         }
         // ---- dv rows whose beta was floored: T' used the floored value
         if (tid < L && live && fabsf(gd[128 + tid]) == kBetaFloor) {

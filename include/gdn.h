@@ -282,8 +282,9 @@ gdn_status gdn_gated_rmsnorm(const void* x, const void* z, gdn_dtype dtype, cons
  * dA_log, ddt_bias) are fp32, added in a fixed order: the same call on the same device gives the same
  * bits.  `workspace` is device scratch, 256-byte aligned, of at least the matching _workspace_size()
  * bytes; its contents on entry are ignored; calls that may overlap on the GPU need separate ones (two
- * captured graphs too).  Gradients are written, not accumulated.  No output may overlap an input,
- * another output or the workspace.
+ * captured graphs that may run at once, too).  Gradients are written, not accumulated.  No output may
+ * overlap an input, another output or the workspace.  Pointers for which no larger alignment is given
+ * lie on a multiple of their element.  A call works on the device that is current for the calling thread.
  */
 
 /*
@@ -298,8 +299,14 @@ gdn_status gdn_gated_rmsnorm(const void* x, const void* z, gdn_dtype dtype, cons
  * dg, dbeta      : [B, T, Hv] dtype.
  * dinitial_state : [N, Hv, dv, dk] fp32 or NULL (not written).
  * Supported: what gdn_chunk_fwd supports.  Tokens behind the last sequence (cu_seqlens[N] < T) are
- * neither read nor written.  A malformed cu_seqlens lands in the workspace's status word
- * (gdn_workspace_status).  All pointers but dg, dbeta and cu_seqlens 16-byte aligned.
+ * never written, and what they hold reaches no result.  A malformed cu_seqlens lands in the
+ * workspace's status word (gdn_workspace_status).  All pointers but dg, dbeta and cu_seqlens 16-byte
+ * aligned; dg and dbeta on a multiple of their element.
+ * bf16 with dk = dv = 128, chunk = 64 and B * T * Hv >= 512 runs on tensor cores, whose operands are
+ * rounded to bf16: each output is within 5e-3 of its norm.  Everything else keeps fp32 inside, and
+ * loses only the output's own rounding (2e-5 of the norm for fp32 outputs).  A beta of magnitude below
+ * 2^-30 takes part as +-2^-30, but for dv; without an initial state dg of a sequence's first
+ * token is exactly zero.
  */
 size_t gdn_chunk_bwd_workspace_size(gdn_dtype dtype, int N, int B, int64_t T, int Hk, int Hv,
                                     int dk, int dv, int chunk);

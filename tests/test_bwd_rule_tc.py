@@ -171,3 +171,15 @@ def test_bits_graphs_and_streams():
         torch.cuda.synchronize()
         assert gdn.workspace_status(ws) == gdn.GDN_OK
         assert all(torch.equal(a, b) for a, b in zip((first, other)[i], outs[i]))
+
+
+@gpu
+@pytest.mark.parametrize("dtype,lens", [("f32", [0, 1]), ("f32", [1, 3, 2]), ("f32", [70]), ("bf16", [1] * 300),
+                                        ("bf16", [3] * 40 + [70, 66])])
+def test_decay_gradients_far_below_the_terms_they_leave(dtype, lens):
+    """A decay of e^-15 a token, states on both ends: dg is of that size, millions of times below the products
+    k.(U dS) of single tokens, which may therefore not enter its sums and cancel there."""
+    x = make(lens, 1, 2, D, D, dtype, True, seed=67)
+    x["g"][:] = -15.0 + 0.1 * x["g"].clamp(-10, 0)
+    tol = 2e-5 if dtype == "f32" else TC_TOL
+    check(x, lens, run(x, lens) if dtype == "bf16" else call(x, 32), tol, D ** -0.5)
