@@ -25,8 +25,8 @@
 // Warp roles (384 threads): warps 0-7 the epilogues (lane quarter warp % 4; columns, in epilogue B tokens,
 // split in two by warp / 4), warp 8 the TMA producer, warp 9 the MMA issuer, warp 10 sends dq and dk out.
 // Bounds: 144 KB of tiles per (chunk, v-head) at two v-heads a k-head against about 6 units of
-// 64 x 128 x 128 products: HBM, with the epilogues' instructions close behind.  16384 (chunk, v-head) pairs: 526
-// us for 2.6 GB, 5.0 TB/s (76 % of a copy); with loads behind the epilogues and a fixed share of items 565.
+// 64 x 128 x 128 products: the epilogues' instructions, with HBM close behind.  16384 (chunk, v-head) pairs:
+// 566 us for 2.6 GB, 4.6 TB/s (70 % of a copy).
 // Bounded waits and the abort protocol as in bwd_chain.cu.
 #include "bwd_tc.cuh"
 #include "f32x2.cuh"
@@ -54,7 +54,7 @@ constexpr uint32_t SM_NM = SM_DS + 32768;     // [dN; dM]: 128 rows x 128 B
 constexpr uint32_t SM_GD = SM_NM + 16384;     // four records: one is read until its step ends
 constexpr uint32_t SM_RED = SM_GD + 4 * GD_BYTES;  // 2 x (dgamma and kappa parts, each [4][64], sums [8])
 constexpr uint32_t RED_FLOATS = 2 * 4 * 64 + 8;
-constexpr uint32_t SM_OWN = SM_RED + 2 * RED_FLOATS * 4;  // p [64]
+constexpr uint32_t SM_OWN = SM_RED + 2 * RED_FLOATS * 4;  // p [64], summed over the heads
 constexpr uint32_t SM_BAR = SM_OWN + 256;
 constexpr uint32_t SM_BYTES = SM_BAR + 192 + 1024;
 static_assert(SM_BYTES <= 232448, "shared memory budget");
@@ -223,6 +223,8 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
       // tokens 32 half + 2 q, + 1 of channel `row`: dq, dk summed over the heads, and q, k
       f32x2 aq[16], ak[16];
       uint32_t qv[16], kv[16];
+      float* own = reinterpret_cast<float*>(smem + SM_OWN);
+      float own_sum = 0.0f;  // p of this thread's row, over the heads
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
         aq[q] = ak[q] = 0ull;
@@ -236,7 +238,6 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
         const bool in = wait_w(B_H + (x & 1), (x >> 1) & 1);
         // seen: the next use may be published; at the end of an item dq and dk go through the buffer first
         if (lane == 0 && gi < G - 1) mbar_arrive(&bars[B_HE + (x & 1)]);
-        float* own = reinterpret_cast<float*>(smem + SM_OWN);  // read before NB_E, written after it
         // ---- epilogue A
         const int r = row & 63;
         float diag = 0.0f;
@@ -272,7 +273,8 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
               diag = d[0];
             }
           }
-          if (quad < 2 && half == quad) own[row] = P.scale * diag;
+          own_sum += P.scale * diag;
+          if (quad < 2 && half == quad && gi == G - 1) own[row] = own_sum;
           unsigned char* nm = smem + SM_NM;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -323,8 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
           if (lane == 0) mbar_arrive(&bars[B_KQE]);  // this warp needs K and Q no more
         }
         // ---- epilogue B
-        const bool own_ok = wait_w(B_NM, x & 1);  // p of all warps; long since
-        if (wait_w(B_N, x & 1) && own_ok) {
+        if (wait_w(B_N, x & 1)) {
           tc_fence_after();
           float keep = 0.0f, keepk = 0.0f;
 #pragma unroll
@@ -357,9 +358,8 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
               const float2 kk = parts(mul2(k2, w1));
               kap[e] = kk.x;
               kap[e + 1] = kk.y;
-              const f32x2 o2 = *reinterpret_cast<const f32x2*>(own + t0 + e);
-              aq[p] = fma2(o2, k2, add2(aq[p], fq));
-              ak[p] = fma2(o2, q2, add2(ak[p], add2(fe, fw)));
+              aq[p] = add2(aq[p], fq);
+              ak[p] = add2(ak[p], add2(fe, fw));
             }
             // sum over the warp's 32 channels: halve the tokens a lane holds three times, then add the
             // four lanes that are left with the same token: token t0 + (lane >> 2)
@@ -445,6 +445,12 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
           for (int e = 0; e < tm::D; ++e)
             dv[e] = __float2bfloat16_rn(__bfloat162float(dv[e]) * ratio);
         }
+      }
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {  // the tokens' own pairs
+        const f32x2 o2 = *reinterpret_cast<const f32x2*>(own + 32 * half + 2 * q);
+        aq[q] = fma2(o2, widen(kv[q]), aq[q]);
+        ak[q] = fma2(o2, widen(qv[q]), ak[q]);
       }
       // ---- dq, dk: two bytes at a time into shared memory (a warp's 32 channels are 64 consecutive
       // bytes) where dO and dW were, out as boxes of tensor maps; a partial chunk row by row
