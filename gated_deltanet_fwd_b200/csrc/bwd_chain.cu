@@ -165,6 +165,7 @@ __device__ __forceinline__ void chain(const CUtensorMap* map_k, const CUtensorMa
   // only in long waits: both take longer than the waits of a chunk.
   auto wait = [&](int b, uint32_t parity) -> bool {
     uint64_t t0 = 0;
+#pragma unroll 1  // many inlined copies
     for (uint32_t k = 1; k < kSpinLimit; ++k) {
       if (mbar_try_wait(&bars[b], parity)) return true;
       if ((k & 255) == 0) {

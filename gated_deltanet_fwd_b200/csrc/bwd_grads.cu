@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
   };
   auto wait = [&](int b, uint32_t parity) -> bool {
     uint64_t t0 = 0;
+#pragma unroll 1  // a dozen inlined copies
     for (uint32_t k = 1; k < kSpinLimit; ++k) {
       if (mbar_try_wait(&bars[b], parity)) return true;
       if ((k & 255) == 0) {  // long waits only: the flag and the timer are slow to read
@@ -442,6 +443,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
           const int64_t at = (ch.t0 + tid) * P.Hv + h;
           const float ratio = P.beta[at] / gd[128 + tid];
           __nv_bfloat16* dv = P.dv + at * tm::D;
+#pragma unroll 1
           for (int e = 0; e < tm::D; ++e)
             dv[e] = __float2bfloat16_rn(__bfloat162float(dv[e]) * ratio);
         }

@@ -81,7 +81,7 @@ __device__ __forceinline__ bool find_chunk(const int32_t* cu, int64_t T, int N, 
   if (!cu) {
     const int64_t per = (T + C - 1) / C;
     if (per == 0 || slot >= per * N) return false;
-    ch.n = (int)(slot / per);
+    ch.n = (int)((uint32_t)slot / (uint32_t)per);  // both below 2^31: they count blocks of a grid
     const int64_t c = slot - (int64_t)ch.n * per;
     ch.t0 = (int64_t)ch.n * T + c * C;
     ch.first = c == 0;
@@ -89,6 +89,7 @@ __device__ __forceinline__ bool find_chunk(const int32_t* cu, int64_t T, int N, 
     return true;
   }
   int64_t base = 0;
+#pragma unroll 1
   for (int m = 0; m < N; ++m) {
     const int64_t a = cu[m], b = cu[m + 1];
     if (a < 0 || b < a || b > T) {
@@ -117,6 +118,7 @@ struct ChunkCursor {
   __device__ __forceinline__ bool find(const int32_t* cu, int64_t T, int N, int C, int64_t slot,
                                        Chunk& ch, int* status) {
     if (!cu) return find_chunk(cu, T, N, C, slot, ch, status);
+#pragma unroll 1
     for (; m < N; ++m, a = -1) {
       if (a < 0) {
         a = cu[m];

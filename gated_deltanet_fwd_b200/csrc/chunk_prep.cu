@@ -113,8 +113,7 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 // T = (I + A)^{-1} for the unit lower-triangular I + A (A strictly lower, fp32 [64][AS]) by one
 // warpgroup (w4 = warp within the group, bar = its named barrier).  Tf receives the lower triangle
 // and the unit diagonal; above the diagonal it is left unwritten.
-template <int bar>
-__device__ __forceinline__ void solve64(const float* Af, float* Tf, float* Mb, int w4, int lane) {
+__device__ __forceinline__ void solve64(int bar, const float* Af, float* Tf, float* Mb, int w4, int lane) {
   // diagonal 16 x 16 blocks: right-looking forward substitution, one column per lane
   if (w4 < 2) {
     const int blk = 2 * w4 + (lane >> 4), jj = lane & 15, col = 16 * blk + jj;
@@ -577,10 +576,7 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(
       float* Tf = reinterpret_cast<float*>(smem + PP_T) + gi * 64 * AS;
       float* Mb = reinterpret_cast<float*>(smem + PP_MB) + gi * 4 * 16 * MS;
       const float* gl2 = gl2_all + gi * 128;
-      if (gi == 0)
-        solve64<1>(Af, Tf, Mb, w4, lane);
-      else
-        solve64<2>(Af, Tf, Mb, w4, lane);
+      solve64(1 + gi, Af, Tf, Mb, w4, lane);
       PP_TS(4);
       // T' = T diag(beta), zero above the diagonal -> rows 0..63 of the [T'; P] tile
       unsigned char* tp = P.ws + tm::tp_offset() + ((size_t)slot * P.Hv + h) * tm::TP_BYTES;
