@@ -56,13 +56,14 @@ constexpr uint32_t SM_RED = SM_GD + 4 * GD_BYTES;  // 2 x (dgamma and kappa part
 constexpr uint32_t RED_FLOATS = 2 * 4 * 64 + 8;
 constexpr uint32_t SM_OWN = SM_RED + 2 * RED_FLOATS * 4;  // p [64], summed over the heads
 constexpr uint32_t SM_BAR = SM_OWN + 256;
-constexpr uint32_t SM_BYTES = SM_BAR + 192 + 1024;
+constexpr uint32_t SM_ITEM = SM_BAR + 160;  // four steps' and two items' records
+constexpr uint32_t SM_BYTES = SM_ITEM + 96 + 1024;
 static_assert(SM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TX_KQ = 32768, TX_HEAD = 32768 + 16384 + GD_BYTES, TX_STATE = 65536;
 
 // B_H, B_HE: two of each, by the step's parity; B_O: by the item's
 enum { B_KQ, B_KQE, B_H, B_HE = B_H + 2, B_O = B_HE + 2, B_S = B_O + 2, B_SE, B_P, B_NM, B_N, B_D, B_FIX, B_DRAIN, B_COUNT };
-static_assert(B_COUNT * 8 + 8 + 24 <= 192, "barriers");
+static_assert(B_COUNT * 8 + 8 <= 160, "barriers");
 constexpr int NB_E = 1, NB_EPI = 256;  // named barrier of the epilogues
 
 // tensor-memory columns
@@ -145,9 +146,10 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM_BAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM_BAR + B_COUNT * 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM_BAR + B_COUNT * 8 + 4);
-  // items, -1 behind the last: of a step (published with its tiles), and of dq, dk on their way out
-  volatile int* step_item = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* out_item = step_item + 4;
+  // a chunk and k-head as (tokens, 0 behind the last item; whether first of its sequence; k-head; first token):
+  // of a step, published with its tiles, and of dq, dk on their way out
+  int4* step_item = reinterpret_cast<int4*>(smem + SM_ITEM);
+  int4* out_item = step_item + 4;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = P.Hv / P.Hk;
 
@@ -215,12 +217,10 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
       // all warps leave together: the named barriers need every one of them
       const bool got = wait_w(B_H + (x & 1), (x >> 1) & 1);
       if (!bar_all(NB_E, NB_EPI, got)) break;
-      const int it = step_item[x & 3];
-      Chunk ch;
-      int64_t slot;
-      int hk;
-      if (it < 0 || !locate(it, ch, slot, hk)) break;
-      const int L = ch.L;
+      const int4 item = step_item[x & 3];
+      const int L = item.x, hk = item.z;
+      const int64_t t0 = item.w;
+      if (L == 0) break;
       // tokens 32 half + 2 q, + 1 of channel `row`: dq, dk summed over the heads, and q, k
       f32x2 aq[16], ak[16];
       uint32_t qv[16], kv[16];
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
         if (lane == 0) sums[warp] = fr;
         if (quad >= 2 && half == (quad & 1) && in && r < L) {
           const float b = gd[128 + r], t = diag / b / b;
-          P.dbeta[(ch.t0 + r) * P.Hv + h] = __float2bfloat16_rn(t);
+          P.dbeta[(t0 + r) * P.Hv + h] = __float2bfloat16_rn(t);
         }
         if (gi == 0) {
           if (wait_w(B_KQ, y & 1)) {
@@ -331,21 +331,21 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
           float keep = 0.0f, keepk = 0.0f;
 #pragma unroll
           for (int b = 0; b < 4; ++b) {  // 8 tokens at a time
-            const int t0 = 32 * half + 8 * b;
+            const int tb = 32 * half + 8 * b;
             float d1a[8], d1b[8], d4a[8], d4b[8], d3[8], d5[8], v[8], kap[8];
-            tmem_ld8(tmem + lo + TM_D1 + t0, d1a);
-            tmem_ld8(tmem + lo + TM_D4 + t0, d4a);
-            tmem_ld8(tmem + lo + TM_D1 + 64 + t0, d1b);
-            tmem_ld8(tmem + lo + TM_D4 + 64 + t0, d4b);
-            tmem_ld8(tmem + lo + TM_D3 + t0, d3);
-            tmem_ld8(tmem + lo + TM_D5 + t0, d5);
+            tmem_ld8(tmem + lo + TM_D1 + tb, d1a);
+            tmem_ld8(tmem + lo + TM_D4 + tb, d4a);
+            tmem_ld8(tmem + lo + TM_D1 + 64 + tb, d1b);
+            tmem_ld8(tmem + lo + TM_D4 + 64 + tb, d4b);
+            tmem_ld8(tmem + lo + TM_D3 + tb, d3);
+            tmem_ld8(tmem + lo + TM_D5 + tb, d5);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
               const int p = 4 * b + e / 2;
               const f32x2 k2 = widen(kv[p]), q2 = widen(qv[p]);
-              const float2 g1 = *reinterpret_cast<const float2*>(gd + t0 + e);
-              const float2 dd = *reinterpret_cast<const float2*>(gd + 64 + t0 + e);
+              const float2 g1 = *reinterpret_cast<const float2*>(gd + tb + e);
+              const float2 dd = *reinterpret_cast<const float2*>(gd + 64 + tb + e);
               const f32x2 g2 = two(g1.x, g1.y), neg = two(-1.0f, -1.0f);
               const f32x2 fq = fma2(mul2(two(P.scale, P.scale), g2), two(d1a[e], d1a[e + 1]),
                                     two(d4a[e], d4a[e + 1]));
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
               ak[p] = add2(ak[p], add2(fe, fw));
             }
             // sum over the warp's 32 channels: halve the tokens a lane holds three times, then add the
-            // four lanes that are left with the same token: token t0 + (lane >> 2)
+            // four lanes that are left with the same token: token tb + (lane >> 2)
 #pragma unroll
             for (int w = 4; w > 0; w >>= 1) {
               const bool up = lane & (4 * w);
@@ -432,15 +432,15 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
           k0 = lane > 0 ? k0 : 0.0f;
           k1 = lane > 0 ? all0 + k1 : all0;
           // the first token's decay multiplies the initial state: without one its gradient is zero
-          const bool none = ch.first && !P.S0;
-          __nv_bfloat16* dst = P.dg + ch.t0 * P.Hv + h;
+          const bool none = item.y && !P.S0;
+          __nv_bfloat16* dst = P.dg + t0 * P.Hv + h;
           if (lane < L)
             dst[(int64_t)lane * P.Hv] = __float2bfloat16_rn(lane == 0 && none ? 0.0f : a0 + f + k0);
           if (32 + lane < L) dst[(int64_t)(32 + lane) * P.Hv] = __float2bfloat16_rn(a1 + f + k1);
         }
         // ---- dv rows whose beta was floored: T' used the floored value
         if (tid < L && live && fabsf(gd[128 + tid]) == kBetaFloor) {
-          const int64_t at = (ch.t0 + tid) * P.Hv + h;
+          const int64_t at = (t0 + tid) * P.Hv + h;
           const float ratio = P.beta[at] / gd[128 + tid];
           __nv_bfloat16* dv = P.dv + at * tm::D;
 #pragma unroll 1
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
         fence_proxy_async_smem();
       } else if (__all_sync(0xffffffffu, !*abort_flag)) {
         const int64_t rs = (int64_t)P.Hk * tm::D;
-        const int64_t base = (ch.t0 + 32 * half) * rs + hk * tm::D + row;
+        const int64_t base = (t0 + 32 * half) * rs + hk * tm::D + row;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
           const float2 fq = parts(aq[q]), fk = parts(ak[q]);
@@ -489,10 +489,10 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
         }
       }
       __syncwarp();
-      if (tid == 0) out_item[y & 1] = it;
+      if (tid == 0) out_item[y & 1] = item;
       if (lane == 0) mbar_arrive(&bars[B_O + (y & 1)]);
     }
-    if (tid == 0) out_item[y & 1] = -1;
+    if (tid == 0) out_item[y & 1] = make_int4(0, 0, 0, 0);
     if (lane == 0) mbar_arrive(&bars[B_O + (y & 1)]);
     __syncwarp();
   } else {
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
           const size_t sh = (size_t)slot * P.Hv + h;
           unsigned char* ow = smem + SM_OW + (x & 1) * 32768;
           const bool go = may(B_HE + (x & 1), x >> 1);
-          if (go && lane == 0) step_item[x & 3] = it;
+          if (go && lane == 0) step_item[x & 3] = make_int4(ch.L, ch.first, hk, t0);
           __syncwarp();
           if (!go ||
               !group(B_H + (x & 1), TX_HEAD, ch.L, ow, 4, [&](uint64_t* fb) {
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
       __syncwarp();
       // the end of the items, after the wait above: it is one more phase of the same barrier
       if (!stop && may(B_HE + (x & 1), x >> 1) && lane == 0) {
-        step_item[x & 3] = -1;
+        step_item[x & 3] = make_int4(0, 0, 0, 0);
         mbar_arrive(&bars[B_H + (x & 1)]);
       }
       __syncwarp();
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
       const uint64_t dMn = sdesc_sw128(sbase + SM_NM + 8192, 8192, 1024);
       auto live = [&]() { return __all_sync(0xffffffffu, !*abort_flag) != 0; };
       auto products_p = [&](int k) {  // MMA_p of step k: the previous step's B_NM said that D2 is read
-        const bool have = wait_w(B_H + (k & 1), (k >> 1) & 1) && step_item[k & 3] >= 0 && live();
+        const bool have = wait_w(B_H + (k & 1), (k >> 1) & 1) && step_item[k & 3].x > 0 && live();
         if (have) {
           tc_fence_after();
           const uint64_t ow = dadd(dOW, (k & 1) * 32768), u = dadd(dU, (k & 1) * 16384);
@@ -693,16 +693,13 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
       // ------------------------------------------------------------------ dq, dk ---------------
       for (;; ++y) {
         if (!wait_w(B_O + (y & 1), (y >> 1) & 1)) break;
-        const int it = out_item[y & 1];
-        Chunk ch;
-        int64_t slot;
-        int hk;
-        if (it < 0 || !locate(it, ch, slot, hk)) break;
+        const int4 item = out_item[y & 1];
+        if (item.x == 0) break;
         x += G;
         const int b = (x - 1) & 1;
-        if (lane == 0 && ch.L == tm::C && !*abort_flag) {
+        if (lane == 0 && item.x == tm::C && !*abort_flag) {
           const unsigned char* out = smem + SM_OW + b * 32768;
-          const int32_t t0 = (int32_t)ch.t0;
+          const int32_t t0 = item.w, hk = item.z;
           tma_store_3d(&map_dq, out, 0, hk, t0);
           tma_store_3d(&map_dq, out + 8192, 64, hk, t0);
           tma_store_3d(&map_dk, out + 16384, 0, hk, t0);

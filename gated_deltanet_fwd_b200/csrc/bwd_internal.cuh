@@ -58,6 +58,7 @@ __device__ __forceinline__ bool seq_range(const int32_t* cu, int64_t T, int n, i
     return true;
   }
   int64_t base = 0;
+#pragma unroll 1
   for (int m = 0; m <= n; ++m) {
     const int64_t a = cu[m], b = cu[m + 1];
     if (a < 0 || b < a || b > T) return false;

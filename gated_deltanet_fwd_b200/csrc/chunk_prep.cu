@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(
   // asynchronous per-thread copies (cp.async), waited for before the item's MMA
   auto issue_loads = [&](const Item& I) {
     constexpr int PER = 2 * 64 * 16 / PP_THREADS;
-#pragma unroll
+#pragma unroll(BWD ? 1 : PER)
     for (int i = 0; i < PER; ++i) {
       const int e = tid + i * PP_THREADS;
       const int which = e >> 10, r = (e >> 4) & 63, ch = e & 15;
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(
     const int64_t t0 = I.t0;
     const int L = I.L;
     x0 = x1 = b0 = b1 = 0.f;
-    if (P.a) {
+    if (!BWD && P.a) {
       // the gates of the layer: beta = sigmoid(b), g = -exp(A_log) softplus(a + dt_bias)
       const float ea = expf(__ldg(P.A_log + h)), db = __ldg(P.dt_bias + h);
       if (lane < L) {
