@@ -366,9 +366,8 @@ gdn_status gdn_chunk_bwd(const void* q, int64_t q_tok_stride, const void* k, int
   a.ws_bytes = workspace_bytes;
   a.status = reinterpret_cast<int*>(workspace);
   const cudaStream_t s = as_stream(stream);
-  // status word; item counter of the tensor-core path
-  if (cudaMemsetAsync(workspace, 0, 16, s) != cudaSuccess) return GDN_ERR_CUDA;
   if (tensor_cores(dtype, n_tok, Hv, dk, dv, chunk)) return from_cuda(bwd::launch_tc(a, s));
+  if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return GDN_ERR_CUDA;  // status word
   a.C = simt_chunk(dtype, n_tok, dk, dv, chunk);
   return from_cuda(bwd::launch_simt(a, s));
 }

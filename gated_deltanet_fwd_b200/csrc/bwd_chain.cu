@@ -647,12 +647,9 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
 
 }  // namespace
 
-cudaError_t launch_bwd_chain(const Args& a, cudaStream_t s) {
+cudaError_t launch_bwd_chain(const Args& a, const TcMaps& m, cudaStream_t s) {
   const int64_t n_tok = (int64_t)a.B * a.T, units = 2 * (int64_t)a.N * a.Hv;
-  const int64_t slots = max_slots(a.N, n_tok, tm::C);
-  // TMA coordinates are 32-bit
-  if (units > 0x7fffffff || n_tok > 0x7fffffff || slots * a.Hv > 0x7fffffff / 128)
-    return cudaErrorInvalidConfiguration;
+  if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
   ChainParams p;
   unsigned char* ws = reinterpret_cast<unsigned char*>(a.ws);
   p.S0 = a.S0;
@@ -663,21 +660,15 @@ cudaError_t launch_bwd_chain(const Args& a, cudaStream_t s) {
   p.dv = reinterpret_cast<__nv_bfloat16*>(a.dv_);
   p.status = a.status;
   p.T = a.T;
-  p.at = tc_layout(slots, a.Hv);
+  p.at = tc_layout(max_slots(a.N, n_tok, tm::C), a.Hv);
   p.N = a.N;
   p.Hk = a.Hk;
   p.Hv = a.Hv;
-  CUtensorMap mk, mv, mo, mt, mtp, mdv;
-  const int64_t hv = (int64_t)a.Hv * tm::D, rows = slots * a.Hv * 128;
-  if (!make_tok_map(&mk, a.k, a.Hk, n_tok, a.ts.k) || !make_tok_map(&mv, a.v, a.Hv, n_tok, a.ts.v) ||
-      !make_tok_map(&mo, a.dout, a.Hv, n_tok, hv) || !make_tok_map(&mdv, a.dv_, a.Hv, n_tok, hv) ||
-      !make_rows64_map(&mt, ws + p.at.tp, rows, 64) || !make_rows64_map(&mtp, ws + p.at.tp, rows, 128))
-    return cudaErrorInvalidValue;
   constexpr uint32_t bytes = Sm<true>::BYTES > Sm<false>::BYTES ? Sm<true>::BYTES : Sm<false>::BYTES;
-  const cudaError_t e = cudaFuncSetAttribute(
-      bwd_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  int sms = 0;
+  const cudaError_t e = prepare_kernel<bwd_chain_kernel>(bytes, sms);
   if (e != cudaSuccess) return e;
-  bwd_chain_kernel<<<(unsigned)units, THREADS, bytes, s>>>(mk, mv, mo, mt, mtp, mdv, p);
+  bwd_chain_kernel<<<(unsigned)units, THREADS, bytes, s>>>(m.k, m.v, m.dout, m.t, m.tp, m.dv, p);
   return cudaGetLastError();
 }
 

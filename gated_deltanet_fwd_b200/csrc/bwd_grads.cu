@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_grads_kernel(
 
 }  // namespace
 
-cudaError_t launch_bwd_grads(const Args& a, cudaStream_t s) {
+cudaError_t launch_bwd_grads(const Args& a, const TcMaps& m, cudaStream_t s) {
   const int64_t n_tok = (int64_t)a.B * a.T, slots = max_slots(a.N, n_tok, tm::C);
   unsigned char* ws = reinterpret_cast<unsigned char*>(a.ws);
   GradParams p;
@@ -732,7 +732,7 @@ cudaError_t launch_bwd_grads(const Args& a, cudaStream_t s) {
   p.S0 = a.S0;
   p.cu = a.cu;
   p.ws = ws;
-  p.next = reinterpret_cast<int*>(ws + 8);  // zero at the start of the call
+  p.next = reinterpret_cast<int*>(ws + COUNTER);
   p.dq = (__nv_bfloat16*)a.dq;
   p.dk = (__nv_bfloat16*)a.dk_;
   p.dv = (__nv_bfloat16*)a.dv_;
@@ -746,22 +746,11 @@ cudaError_t launch_bwd_grads(const Args& a, cudaStream_t s) {
   p.N = a.N;
   p.Hk = a.Hk;
   p.Hv = a.Hv;
-  if (n_tok > 0x7fffffff) return cudaErrorInvalidConfiguration;  // TMA coordinates are 32-bit
-  CUtensorMap mk, mq, mo, mv, mdq, mdk;
-  const int64_t hv = (int64_t)a.Hv * tm::D;
-  if (!make_tok_map(&mk, a.k, a.Hk, n_tok, a.ts.k) || !make_tok_map(&mq, a.q, a.Hk, n_tok, a.ts.q) ||
-      !make_tok_map(&mo, a.dout, a.Hv, n_tok, hv) || !make_tok_map(&mv, a.dv_, a.Hv, n_tok, hv) ||
-      !make_tok_map(&mdq, a.dq, a.Hk, n_tok, (int64_t)a.Hk * tm::D) ||
-      !make_tok_map(&mdk, a.dk_, a.Hk, n_tok, (int64_t)a.Hk * tm::D))
-    return cudaErrorInvalidValue;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(bwd_grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_BYTES);
+  int sms = 0;
+  const cudaError_t e = prepare_kernel<bwd_grads_kernel>(SM_BYTES, sms);
   if (e != cudaSuccess) return e;
   const int64_t grid = p.items < sms ? p.items : sms;
-  bwd_grads_kernel<<<(unsigned)grid, THREADS, SM_BYTES, s>>>(mk, mq, mo, mv, mdq, mdk, p);
+  bwd_grads_kernel<<<(unsigned)grid, THREADS, SM_BYTES, s>>>(m.k, m.q, m.dout, m.dv, m.dq, m.dk, p);
   return cudaGetLastError();
 }
 
@@ -775,13 +764,25 @@ cudaError_t launch_tc(const Args& a, cudaStream_t s) {
   // rows of the [T~; P] tiles are TMA coordinates; all three kernels count in 32 bits
   if (slots > 0x7fffffff / 128 / a.Hv || (int64_t)a.B * a.T > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const TcLayout at = tc_layout(slots, a.Hv);
+  const int64_t n_tok = (int64_t)a.B * a.T, rows = slots * a.Hv * 128;
+  const int64_t hk = (int64_t)a.Hk * tm::D, hv = (int64_t)a.Hv * tm::D;
+  const unsigned char* tp = reinterpret_cast<const unsigned char*>(a.ws) + at.tp;
+  TcMaps m;
+  if (!make_tok_map(&m.q, a.q, a.Hk, n_tok, a.ts.q) || !make_tok_map(&m.k, a.k, a.Hk, n_tok, a.ts.k) ||
+      !make_tok_map(&m.v, a.v, a.Hv, n_tok, a.ts.v) || !make_tok_map(&m.dout, a.dout, a.Hv, n_tok, hv) ||
+      !make_tok_map(&m.dq, a.dq, a.Hk, n_tok, hk) || !make_tok_map(&m.dk, a.dk_, a.Hk, n_tok, hk) ||
+      !make_tok_map(&m.dv, a.dv_, a.Hv, n_tok, hv) || !make_rows64_map(&m.t, tp, rows, 64) ||
+      !make_rows64_map(&m.tp, tp, rows, 128))
+    return cudaErrorInvalidValue;
+  f.bwd_k = &m.k;
+  f.bwd_q = &m.q;
   f.bwd_gd_off = at.gd;
   f.bwd_qg_off = at.qg;
   f.scale = a.scale;
   cudaError_t e = launch_chunk_prep(a.q, a.k, a.ts, a.g, a.beta, a.cu, a.N, a.B, a.T, a.Hk, a.Hv,
                                     a.ws, a.status, s, f);
-  if (e == cudaSuccess) e = launch_bwd_chain(a, s);
-  if (e == cudaSuccess) e = launch_bwd_grads(a, s);
+  if (e == cudaSuccess) e = launch_bwd_chain(a, m, s);
+  if (e == cudaSuccess) e = launch_bwd_grads(a, m, s);
   return e;
 }
 

@@ -7,6 +7,7 @@ namespace gdn {
 namespace bwd {
 
 constexpr size_t HEADER = 1024;  // status word and padding at the start of the rule's workspace
+constexpr size_t COUNTER = 8;    // tensor-core path: items handed out (bwd_grads.cu), in the header
 
 // Arguments of gdn_chunk_bwd after the host checks.
 struct Args {

@@ -205,6 +205,12 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = P.Hv / P.Hk;
+  // BWD: the header's status word and item counter start at zero, without a launch of their own.  What another
+  // block reports earlier than this is a malformed cu_seqlens, which the chains meet and report again.
+  if (BWD && blockIdx.x == 0 && tid == 0) {
+    *P.status = GDN_OK;
+    *reinterpret_cast<int*>(P.ws + bwd::COUNTER) = 0;
+  }
 
   // ---- work items (slot, k-head), item = slot * Hk + hk, strided over the persistent CTAs
   struct Item {
@@ -686,11 +692,9 @@ cudaError_t launch_chunk_prep(const void* q, const void* k, TokStrides ts, const
   p.dt_bias = fuse.dt_bias;
   p.qg_off = (int64_t)fuse.bwd_qg_off;
   p.scale = fuse.scale;
-  CUtensorMap mk = {}, mq = {};
-  if (!fuse.bwd_gd_off) return launch_prep_t<false>(p, slots, s, mk, mq);
-  if (!make_tok_map(&mk, k, Hk, n_tok, ts.k) || !make_tok_map(&mq, q, Hk, n_tok, ts.q))
-    return cudaErrorInvalidValue;
-  return launch_prep_t<true>(p, slots, s, mk, mq);
+  const CUtensorMap none = {};
+  return fuse.bwd_gd_off ? launch_prep_t<true>(p, slots, s, *fuse.bwd_k, *fuse.bwd_q)
+                         : launch_prep_t<false>(p, slots, s, none, none);
 }
 
 }  // namespace gdn

@@ -226,6 +226,7 @@ struct ChunkFusion {
   const float* dt_bias = nullptr;
   // set: the backward pass's operands, its records and its scale Gamma Q tiles at these byte offsets
   size_t bwd_gd_off = 0, bwd_qg_off = 0;
+  const CUtensorMap *bwd_k = nullptr, *bwd_q = nullptr;
   float scale = 0.0f;
 };
 

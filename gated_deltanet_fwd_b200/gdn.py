@@ -324,7 +324,7 @@ def _all_cuda(*ts):
     dev = -1
     for t in ts:
         if t is not None:
-            d = t.get_device() if t.is_cuda else -1
+            d = t.get_device()  # -1 on the CPU
             if d < 0 or not t.is_contiguous():
                 raise ValueError("tensors must be contiguous CUDA tensors")
             if d != dev:
