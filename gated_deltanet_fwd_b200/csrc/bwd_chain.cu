@@ -18,7 +18,7 @@
 // columns) and, while the first product of a chunk runs, the carried matrix scaled by Gamma_63; warps
 // 8-11 its bf16 copy, and U or dv, to memory; warp 12 the TMA producer; warp 13 the MMA issuer.  What bounds
 // it is the latency of the critical sequence of one chunk, 3400 cycles forward and 3800 backward, not
-// traffic (32 v-heads, sequences of 16384, 8192, 6144 and 2048 tokens: 577 us for 2.8 GB).  Three things
+// traffic (32 v-heads, sequences of 16384, 8192, 6144 and 2048 tokens: 568 us for 2.8 GB).  Three things
 // that shorten it, by clock stamps of a 64-chunk run:
 //   - MMAs are issued under elect.sync, which tells the compiler that one thread is active, with
 //     descriptors that are loop-invariant but for constants (the stage is a template argument): about 10
@@ -611,7 +611,7 @@ __device__ __forceinline__ void chain(const CUtensorMap* map_k, const CUtensorMa
 
 // The two walks of a (sequence, v-head) do not depend on one another, so all of both are units of one
 // launch, the longest sequences first: with 32 heads and sequences of 16384, 8192, 6144 and 2048 tokens the
-// walks one after the other took 475 + 535 us, half of it with most SMs idle, together 585 us.
+// walks one after the other took 475 + 535 us, half of it with most SMs idle, together 568 us.
 __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
     const __grid_constant__ CUtensorMap map_do, const __grid_constant__ CUtensorMap map_t,

@@ -27,9 +27,9 @@
 // its bf16 copy loses only what the small off-diagonal entries lose, and beta is applied in fp32 by
 // whoever uses it.  The record then holds Gamma, d, beta and gamma log2 e, P carries the
 // output scale, and scale Gamma Q goes out next to it (operands of the backward chain, where scaling Q
-// cost 1400 cycles of a chunk).  8192 (chunk, k-head) items of two v-heads: 282 us, 16000 cycles an item
-// beside another one on the SM -- solve 5000, masks 2800, scale Gamma Q 2000, T~ 1700, the rest hand-offs and
-// loads; its 0.8 GB would take 123 us.
+// cost 1400 cycles of a chunk).  8192 (chunk, k-head) items of two v-heads: 250 us, some 14000 cycles an
+// item beside another one on the SM -- a third the solve, then masks, scale Gamma Q and T~ -- where its 0.8 GB
+// would take 123 us.
 #include "bwd_internal.cuh"
 #include "chunk_tm.cuh"
 #include "gdn_internal.cuh"
