@@ -305,13 +305,22 @@ def _kept(x):
     return x, None
 
 
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same without building a Stream object (2 us of a small call), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
 def _run(name, device, *args):
     """Calls the entry point on `device` and on torch's current stream there (the last argument)."""
-    if device.index == torch.cuda.current_device():
-        _check(name, getattr(_lib, name)(*args, torch.cuda.current_stream(device).cuda_stream))
+    i = device.index
+    if i == torch.cuda.current_device():
+        _check(name, getattr(_lib, name)(*args, _raw_stream(i)))
     else:
         with torch.cuda.device(device):
-            _check(name, getattr(_lib, name)(*args, torch.cuda.current_stream(device).cuda_stream))
+            _check(name, getattr(_lib, name)(*args, _raw_stream(i)))
 
 
 def _adr(t):
@@ -378,7 +387,7 @@ def gdn_chunk_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, cu_seq
     _shape((B, T, Hv, d_v), v, dout, dv)
     _shape((B, T, Hv), g, beta, dg, dbeta)
     _shape((N, Hv, d_v, d_k), initial_state, dfinal_state, dinitial_state)
-    new = lambda t, shape: torch.empty(shape, dtype=q.dtype, device=q.device) if t is None else t  # noqa: E731
+    new = lambda t, shape: dout.new_empty(shape) if t is None else t  # noqa: E731
     dq, dk, dv = new(dq, (B, T, Hk, d_k)), new(dk, (B, T, Hk, d_k)), new(dv, (B, T, Hv, d_v))
     dg, dbeta = new(dg, (B, T, Hv)), new(dbeta, (B, T, Hv))
     if output_dinitial_state is None:

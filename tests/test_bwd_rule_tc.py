@@ -183,3 +183,17 @@ def test_decay_gradients_far_below_the_terms_they_leave(dtype, lens):
     x["g"][:] = -15.0 + 0.1 * x["g"].clamp(-10, 0)
     tol = 2e-5 if dtype == "f32" else TC_TOL
     check(x, lens, run(x, lens) if dtype == "bf16" else call(x, 32), tol, D ** -0.5)
+
+
+@gpu
+def test_malformed_entry_met_by_running_blocks():
+    """More items than SMs in front of the bad entry: blocks meet it as a later item, and end."""
+    lens = [200, 200, 200]
+    x = make(lens, 64, 64, D, D, "bf16", False, seed=71)
+    good = run(x, lens)
+    ws = workspace(x, lens)
+    got = call(dict(x, cu=torch.tensor([0, 200, 400, 390], dtype=torch.int32)), workspace=ws)
+    assert gdn.workspace_status(ws) == gdn.GDN_ERR_DEVICE_ARG
+    assert all(torch.equal(a[:, :400], b[:, :400]) for a, b in zip(good[:5], got[:5]))  # well described
+    assert all(torch.equal(a, b) for a, b in zip(good[:5], call(x, workspace=ws)[:5]))
+    assert gdn.workspace_status(ws) == gdn.GDN_OK
