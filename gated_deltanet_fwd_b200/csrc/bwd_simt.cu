@@ -31,7 +31,10 @@
 // fp32 sum once |gamma| is in the hundreds.  The walks are bound by the latency of a chunk's few small
 // products and barriers: 1034 tokens in four ragged sequences, 4 v-heads, dk 64, dv 96, chunk 32, fp32: gprep 14,
 // gwalk 159, ggrad 45 us.
+#include <type_traits>
+
 #include "bwd_internal.cuh"
+#include "ptx.cuh"
 
 namespace gdn {
 namespace bwd {
@@ -72,6 +75,7 @@ struct SimtArgs {
   float scale;
   int64_t T, slots;
   int N, Hk, Hv, dk, dv, C;
+  int stages;  // of the walks (set at launch)
   void* ws;
   int* status;
 };
@@ -121,6 +125,21 @@ __device__ __forceinline__ void load_rows(const T* src, int64_t stride, int64_t 
 
 __device__ __forceinline__ void load_rows_f(const float* src, int C, int width, float* dst, int ld) {
   load_rows<float>(src, width, 0, C, C, width, dst, ld);
+}
+
+// load_rows without waiting where the source is fp32 (ptx::cp_async_wait_all does).
+template <typename T>
+__device__ __forceinline__ void fetch_rows(const T* src, int64_t stride, int64_t t0, int L, int C,
+                                           int width, float* dst, int ld) {
+  if constexpr (std::is_same<T, float>::value) {
+    const int w4 = width / 4;
+    for (int e = threadIdx.x; e < C * w4; e += THREADS) {
+      const int r = e / w4, c = 4 * (e - r * w4);
+      ptx::cp_async16_zfill(dst + r * ld + c, src + (t0 + (r < L ? r : 0)) * stride + c, r < L ? 16u : 0u);
+    }
+  } else {
+    load_rows(src, stride, t0, L, C, width, dst, ld);
+  }
 }
 
 __device__ __forceinline__ float dot4(float4 a, float4 b, float acc) {
@@ -234,7 +253,9 @@ __global__ void __launch_bounds__(THREADS) gprep_kernel(const SimtArgs P) {
 }
 
 // ------------------------------------------------------------------------------- gwalk -----
-// Block = (sequence, v-head, 16 value rows, direction).
+// Block = (sequence, v-head, 16 value rows, direction).  A chunk's inputs lie in one of `stages` buffers: with
+// two, which fp32 inputs get where two blocks still fit an SM, the next chunk's copies run beside this one's
+// products.
 struct Walk {
   int n, h, hk, j0;
   int64_t s_beg, s_end, slot0, nch;
@@ -300,12 +321,9 @@ __device__ __forceinline__ void walk_forward(const SimtArgs& P, const Walk& W, f
   constexpr int ldc = C + 4, R = C / 16;
   const int ldk = P.dk + 4, tid = threadIdx.x;
   float* Ss = sm;                 // [DVS][ldk]
-  float* Ks = Ss + DVS * ldk;     // [C][ldk]
-  float* Ts = Ks + C * ldk;       // [C][ldc]
-  float* Ws = Ts + C * ldc;       // [C][DVS]
-  float* Us = Ws + C * DVS;       // [C][DVS]
-  float* Gm = Us + C * DVS;
-  float* dd = Gm + C;
+  float* Us = Ss + DVS * ldk;     // [C][DVS]
+  float* buf = Us + C * DVS;      // K [C][ldk], T' [C][ldc], V then W [C][DVS], Gamma and d [2][C]
+  const int stage = C * (ldk + ldc + DVS + 2);
   const SimtWs w = simt_ws(P.ws, P.slots, P.Hv, P.dk, P.dv, C);
   const int64_t sbase = ((int64_t)W.n * P.Hv + W.h) * P.dv * P.dk + (int64_t)W.j0 * P.dk;
   const int w4 = P.dk / 4, jst = THREADS / w4, sj = tid / w4, si = 4 * (tid - sj * w4);
@@ -314,18 +332,32 @@ __device__ __forceinline__ void walk_forward(const SimtArgs& P, const Walk& W, f
     *reinterpret_cast<float4*>(Ss + jj * ldk + si) =
         P.S0 ? *reinterpret_cast<const float4*>(P.S0 + sbase + jj * P.dk + si)
              : make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int64_t c = 0; c < W.nch; ++c) {
+  auto fetch = [&](int64_t c) {
     const int64_t t0 = W.s_beg + c * C, sh = (W.slot0 + c) * P.Hv + W.h;
     const int L = (int)min((int64_t)C, W.s_end - t0);
+    float* b = buf + (P.stages == 2 ? (c & 1) * stage : 0);
+    fetch_rows((const T*)P.k + W.hk * P.dk, P.ts.k, t0, L, C, P.dk, b, ldk);
+    b += C * ldk;
+    fetch_rows<float>(w.tp + sh * 2 * C * C, C, 0, C, C, C, b, ldc);
+    b += C * ldc;
+    fetch_rows((const T*)P.v + W.h * P.dv + W.j0, P.ts.v, t0, L, C, DVS, b, DVS);
+    fetch_rows<float>(w.rec + sh * 5 * C, 0, 0, 1, 1, 2 * C, b + C * DVS, 2 * C);
+  };
+  if (W.nch > 0) fetch(0);
+  for (int64_t c = 0; c < W.nch; ++c) {
+    const int64_t sh = (W.slot0 + c) * P.Hv + W.h;
+    float* Ks = buf + (P.stages == 2 ? (c & 1) * stage : 0);
+    float *Ts = Ks + C * ldk, *Ws = Ts + C * ldc, *Gm = Ws + C * DVS, *dd = Gm + C;
+    if (P.stages == 1 && c > 0) {
+      __syncthreads();
+      fetch(c);
+    }
+    ptx::cp_async_wait_all();
     __syncthreads();
-    if (tid < 2 * C) Gm[tid] = w.rec[sh * 5 * C + tid];  // Gamma, d
-    load_rows((const T*)P.k + W.hk * P.dk, P.ts.k, t0, L, C, P.dk, Ks, ldk);
-    load_rows_f(w.tp + sh * 2 * C * C, C, C, Ts, ldc);
-    load_rows((const T*)P.v + W.h * P.dv + W.j0, P.ts.v, t0, L, C, DVS, Ws, DVS);
+    if (P.stages == 2 && c + 1 < W.nch) fetch(c + 1);
     float* So = w.S + sh * P.dv * P.dk + W.j0 * P.dk;
     for (int jj = sj; sj < jst && jj < DVS; jj += jst)
       *reinterpret_cast<float4*>(So + jj * P.dk + si) = *reinterpret_cast<float4*>(Ss + jj * ldk + si);
-    __syncthreads();
     {  // W = V - Gamma K S^T
       float acc[R] = {};
       rows_dot<R>(Ks, ldk, Ss + j * ldk, P.dk, rg, acc);
@@ -365,16 +397,11 @@ __device__ __forceinline__ void walk_backward(const SimtArgs& P, const Walk& W, 
   constexpr int ldc = C + 4, R = C / 16;
   const int ldk = P.dk + 4, tid = threadIdx.x;
   float* Ss = sm;              // [DVS][ldk] dS
-  float* Ks = Ss + DVS * ldk;  // [C][ldk]
-  float* Qs = Ks + C * ldk;    // [C][ldk]
-  float* Ts = Qs + C * ldk;    // [C][ldc] T'
-  float* Ps = Ts + C * ldc;    // [C][ldc] P
-  float* Os = Ps + C * ldc;    // [C][DVS] dO', then Gamma dO'
-  float* Us = Os + C * DVS;    // [C][DVS] dU
+  float* Us = Ss + DVS * ldk;  // [C][DVS] dU
   float* Ws = Us + C * DVS;    // [C][DVS] -Gamma dW
-  float* Gm = Ws + C * DVS;
-  float* dd = Gm + C;
-  float* bet = dd + C;
+  // K, Q [C][ldk], T', P [C][ldc], dO' then Gamma dO' [C][DVS], Gamma, d, beta [3][C]
+  float* buf = Ws + C * DVS;
+  const int stage = C * (2 * ldk + 2 * ldc + DVS + 3);
   const SimtWs w = simt_ws(P.ws, P.slots, P.Hv, P.dk, P.dv, C);
   const int64_t sbase = ((int64_t)W.n * P.Hv + W.h) * P.dv * P.dk + (int64_t)W.j0 * P.dk;
   const int w4 = P.dk / 4, jst = THREADS / w4, sj = tid / w4, si = 4 * (tid - sj * w4);
@@ -383,21 +410,41 @@ __device__ __forceinline__ void walk_backward(const SimtArgs& P, const Walk& W, 
     *reinterpret_cast<float4*>(Ss + jj * ldk + si) =
         P.dST ? *reinterpret_cast<const float4*>(P.dST + sbase + jj * P.dk + si)
               : make_float4(0.f, 0.f, 0.f, 0.f);
+  auto fetch = [&](int64_t c) {
+    const int64_t t0 = W.s_beg + c * C, sh = (W.slot0 + c) * P.Hv + W.h;
+    const int L = (int)min((int64_t)C, W.s_end - t0);
+    float* b = buf + (P.stages == 2 ? (c & 1) * stage : 0);
+    fetch_rows((const T*)P.k + W.hk * P.dk, P.ts.k, t0, L, C, P.dk, b, ldk);
+    b += C * ldk;
+    fetch_rows((const T*)P.q + W.hk * P.dk, P.ts.q, t0, L, C, P.dk, b, ldk);
+    b += C * ldk;
+    fetch_rows<float>(w.tp + sh * 2 * C * C, C, 0, 2 * C, 2 * C, C, b, ldc);  // T', P
+    b += 2 * C * ldc;
+    fetch_rows((const T*)P.dout + W.h * P.dv + W.j0, (int64_t)P.Hv * P.dv, t0, L, C, DVS, b, DVS);
+    fetch_rows<float>(w.rec + sh * 5 * C, 0, 0, 1, 1, 3 * C, b + C * DVS, 3 * C);
+  };
+  if (W.nch > 0) fetch(W.nch - 1);
   for (int64_t c = W.nch - 1; c >= 0; --c) {
     const int64_t t0 = W.s_beg + c * C, sh = (W.slot0 + c) * P.Hv + W.h;
     const int L = (int)min((int64_t)C, W.s_end - t0);
+    float* Ks = buf + (P.stages == 2 ? (c & 1) * stage : 0);
+    float *Qs = Ks + C * ldk, *Ts = Qs + C * ldk, *Ps = Ts + C * ldc, *Os = Ps + C * ldc;
+    float *Gm = Os + C * DVS, *dd = Gm + C, *bet = dd + C;
+    if (P.stages == 1 && c < W.nch - 1) {
+      __syncthreads();
+      fetch(c);
+    }
+    ptx::cp_async_wait_all();
+    for (int e = 4 * tid; e < C * DVS; e += 4 * THREADS) {  // this thread's own part of dO
+      float4 o = *reinterpret_cast<float4*>(Os + e);
+      o.x *= P.scale; o.y *= P.scale; o.z *= P.scale; o.w *= P.scale;
+      *reinterpret_cast<float4*>(Os + e) = o;
+    }
     __syncthreads();
-    if (tid < 3 * C) Gm[tid] = w.rec[sh * 5 * C + tid];  // Gamma, d, beta
-    load_rows((const T*)P.k + W.hk * P.dk, P.ts.k, t0, L, C, P.dk, Ks, ldk);
-    load_rows((const T*)P.q + W.hk * P.dk, P.ts.q, t0, L, C, P.dk, Qs, ldk);
-    load_rows_f(w.tp + sh * 2 * C * C, C, C, Ts, ldc);
-    load_rows_f(w.tp + sh * 2 * C * C + C * C, C, C, Ps, ldc);
-    load_rows((const T*)P.dout + W.h * P.dv + W.j0, (int64_t)P.Hv * P.dv, t0, L, C, DVS, Os, DVS,
-              P.scale);
+    if (P.stages == 2 && c > 0) fetch(c - 1);
     float* So = w.dS + sh * P.dv * P.dk + W.j0 * P.dk;
     for (int jj = sj; sj < jst && jj < DVS; jj += jst)
       *reinterpret_cast<float4*>(So + jj * P.dk + si) = *reinterpret_cast<float4*>(Ss + jj * ldk + si);
-    __syncthreads();
     {  // dU = P^T dO' + d K dS^T
       float acc[R] = {};
       rows_dot<R>(Ks, ldk, Ss + j * ldk, P.dk, rg, acc);
@@ -725,12 +772,15 @@ cudaError_t launch_grad(const SimtArgs& P, int cw, int64_t par, size_t bytes, cu
 }
 
 template <typename T, int C>
-cudaError_t launch_c(const SimtArgs& P, cudaStream_t s) {
+cudaError_t launch_c(SimtArgs P, cudaStream_t s) {
   const int ldk = P.dk + 4, ldv = P.dv + 4, ldc = C + 4;
   const size_t f = sizeof(float);
   const size_t sm_prep = (2 * (size_t)C * ldk + 3 * C * ldc + 3 * C) * f + C * 8;
-  const size_t sm_walk =  // the backward walk's; the forward one needs less
-      ((size_t)(DVS + 2 * C) * ldk + 2 * C * ldc + 3 * C * DVS + 3 * C) * f;
+  // the backward walk's; the forward one needs less
+  const size_t stage = (size_t)C * (2 * ldk + 2 * ldc + DVS + 3) * f, rest = ((size_t)DVS * ldk + 2 * C * DVS) * f;
+  const bool two = std::is_same<T, float>::value && rest + 2 * stage <= 113 * 1024;
+  const size_t sm_walk = rest + (two ? 2 : 1) * stage;
+  P.stages = two ? 2 : 1;
   const size_t sm_grad =
       (2 * (size_t)C * ldk + 3 * C * ldv + 2 * C * ldc + 6 * C + 8) * f + C * 8;
   auto set = [](auto kern, size_t bytes) {
