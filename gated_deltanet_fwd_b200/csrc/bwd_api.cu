@@ -78,12 +78,13 @@ constexpr int64_t TC_MIN_VALUES = 512;
 bool tensor_cores(gdn_dtype dtype, int64_t n_tok, int Hv, int dk, int dv, int chunk) {
   return dtype == GDN_BF16 && dk == 128 && dv == 128 && chunk == 64 && n_tok * Hv >= TC_MIN_VALUES;
 }
-// Chunk length on CUDA cores: the caller's, but shorter where a call is only too small for the tensor cores.
-// One v-head per k-head and 1 token: 33 us with chunks of 16, 49 with 32, 98 with 64; 100 tokens, 4 v-heads:
-// 84, 111, 185; 250 tokens, 2 v-heads: 129, 143, 221; 500 tokens, 1 v-head: 182, 172, 231.
-int simt_chunk(gdn_dtype dtype, int64_t n_tok, int dk, int dv, int chunk) {
-  if (dtype != GDN_BF16 || dk != 128 || dv != 128 || chunk != 64) return chunk;
-  return n_tok <= 256 ? 16 : 32;
+// Chunk length on CUDA cores: the caller's, but no longer than is fast (it changes no result beyond rounding).
+// bf16, d = 128, one v-head per k-head and 1 token: 33 us with chunks of 16, 49 with 32, 98 with 64; 250
+// tokens, 2 v-heads: 129, 143, 221; 500 tokens, 1 v-head: 182, 172, 231.  fp32, d = 128, 1024 tokens, 4
+// v-heads: 327, 290, 365; sixteen such sequences of 8 v-heads: 3.2 ms with 32, 3.5 with 64.
+int simt_chunk(int64_t n_tok, int chunk) {
+  const int most = n_tok <= 256 ? 16 : 32;
+  return chunk < most ? chunk : most;
 }
 bool norm_dim_ok(int dim) {
   return dim == 8 || dim == 16 || dim == 32 || dim == 64 || dim == 128 || dim == 256;
@@ -304,7 +305,7 @@ size_t gdn_chunk_bwd_workspace_size(gdn_dtype dtype, int N, int B, int64_t T, in
   return round256(tensor_cores(dtype, n_tok, Hv, dk, dv, chunk)
                       ? bwd::tc_workspace_bytes(N, n_tok, Hv)
                       : bwd::simt_workspace_bytes(N, n_tok, Hv, dk, dv,
-                                                  simt_chunk(dtype, n_tok, dk, dv, chunk)));
+                                                  simt_chunk(n_tok, chunk)));
 }
 
 gdn_status gdn_chunk_bwd(const void* q, int64_t q_tok_stride, const void* k, int64_t k_tok_stride,
@@ -368,7 +369,7 @@ gdn_status gdn_chunk_bwd(const void* q, int64_t q_tok_stride, const void* k, int
   const cudaStream_t s = as_stream(stream);
   if (tensor_cores(dtype, n_tok, Hv, dk, dv, chunk)) return from_cuda(bwd::launch_tc(a, s));
   if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return GDN_ERR_CUDA;  // status word
-  a.C = simt_chunk(dtype, n_tok, dk, dv, chunk);
+  a.C = simt_chunk(n_tok, chunk);
   return from_cuda(bwd::launch_simt(a, s));
 }
 

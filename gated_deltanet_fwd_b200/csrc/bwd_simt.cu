@@ -1,6 +1,6 @@
 // bwd_simt.cu -- gradients of the chunked gated delta rule on CUDA cores (fp32 FFMA): the all-fp32
 // mode and every shape the tensor-core path does not serve (dk, dv <= 128 in multiples of 16, chunk
-// 16/32/64).
+// 16 or 32; a caller's 64 runs as 32).
 //
 // With the chunk form of chunk_simt.cu (gamma the in-chunk cumulative log-decay, Gamma = e^gamma,
 // d_s = e^{gamma_L - gamma_s}, E_rs = e^{gamma_r - gamma_s}, T' = (I + A)^{-1} diag(beta),
@@ -29,8 +29,9 @@
 // v-heads that share the k-head are summed in registers in head order, so dq and dk do not depend on
 // scheduling.  Cumulative log-decays are kept in 64 bits: their differences lose half the digits of an
 // fp32 sum once |gamma| is in the hundreds.  The walks are bound by the latency of a chunk's few small
-// products and barriers: 1034 tokens in four ragged sequences, 4 v-heads, dk 64, dv 96, chunk 32, fp32: gprep 14,
-// gwalk 159, ggrad 45 us.
+// products and barriers: 1034 tokens in four ragged sequences, 4 v-heads, dk 64, dv 96, chunk 32, fp32: gprep 11,
+// gwalk 113, ggrad 36 us.  With each chunk's loads awaited before its products gwalk took 137; chunks of 64 are slower
+// than of 32 at every size tried.
 #include <type_traits>
 
 #include "bwd_internal.cuh"
@@ -81,32 +82,20 @@ struct SimtArgs {
 };
 
 // This chunk's gates of one v-head, by one warp per call site: gam (64-bit cumulative log-decay, constant
-// behind the end) and bet (as used in T').  C <= 64: lanes hold tokens lane and 32 + lane.
+// behind the end) and bet (as used in T').  C <= 32: a lane a token.
 __device__ __forceinline__ void scan_gates(const SimtArgs& P, int64_t t0, int L, int h, int lane,
                                            double* gam, float* bet) {
-  double x[2];
-  float b[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = 32 * i + lane;
-    x[i] = r < L ? (double)P.g[(t0 + r) * P.Hv + h] : 0.0;
-    b[i] = r < L ? floor_beta(P.beta[(t0 + r) * P.Hv + h]) : 0.0f;
-  }
+  double x = lane < L ? (double)P.g[(t0 + lane) * P.Hv + h] : 0.0;
+  const float b = lane < L ? floor_beta(P.beta[(t0 + lane) * P.Hv + h]) : 0.0f;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double y0 = __shfl_up_sync(0xffffffffu, x[0], o), y1 = __shfl_up_sync(0xffffffffu, x[1], o);
-    if (lane >= o) {
-      x[0] += y0;
-      x[1] += y1;
-    }
+    const double y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  x[1] += __shfl_sync(0xffffffffu, x[0], 31);
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (32 * i + lane < P.C) {
-      gam[32 * i + lane] = x[i];
-      bet[32 * i + lane] = b[i];
-    }
+  if (lane < P.C) {
+    gam[lane] = x;
+    bet[lane] = b;
+  }
 }
 
 // rows [t0, t0 + L) of a token tensor into smem [C][ld], zeros behind
@@ -716,34 +705,18 @@ __global__ void __launch_bounds__(THREADS) ggrad_kernel(const SimtArgs P, int CW
       for (int x = 0; x < THREADS / 32; ++x) f += red[x];
       f *= Gm[C - 1];
       // kappa, summed over earlier tokens
-      float k0 = lane < L ? kw[lane] : 0.0f, k1 = C > 32 && 32 + lane < L ? kw[32 + lane] : 0.0f;
+      float k0 = lane < L ? kw[lane] : 0.0f;
+      float a0 = lane < L ? dgm[lane] : 0.0f;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const float u0 = __shfl_up_sync(0xffffffffu, k0, o);
-        const float u1 = __shfl_up_sync(0xffffffffu, k1, o);
-        if (lane >= o) {
-          k0 += u0;
-          k1 += u1;
-        }
-      }
-      const float all0 = __shfl_sync(0xffffffffu, k0, 31);
-      k0 = __shfl_up_sync(0xffffffffu, k0, 1);
-      k1 = __shfl_up_sync(0xffffffffu, k1, 1);
-      k0 = lane > 0 ? k0 : 0.0f;
-      k1 = lane > 0 ? all0 + k1 : all0;
-      float a0 = lane < L ? dgm[lane] : 0.0f, a1 = C > 32 && 32 + lane < L ? dgm[32 + lane] : 0.0f;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
+        const float l0 = __shfl_up_sync(0xffffffffu, k0, o);
         const float u0 = __shfl_down_sync(0xffffffffu, a0, o);
-        const float u1 = __shfl_down_sync(0xffffffffu, a1, o);
-        if (lane + o < 32) {
-          a0 += u0;
-          a1 += u1;
-        }
+        if (lane >= o) k0 += l0;
+        if (lane + o < 32) a0 += u0;
       }
-      a0 += __shfl_sync(0xffffffffu, a1, 0);
+      k0 = __shfl_up_sync(0xffffffffu, k0, 1);
+      k0 = lane > 0 ? k0 : 0.0f;
       if (lane < L) ((T*)P.dg)[(t0 + lane) * P.Hv + h] = from_f<T>(a0 + f + k0);
-      if (32 + lane < L) ((T*)P.dg)[(t0 + 32 + lane) * P.Hv + h] = from_f<T>(a1 + f + k1);
     }
   }
   if (on) {
@@ -798,8 +771,7 @@ cudaError_t launch_c(SimtArgs P, cudaStream_t s) {
   int cw = 4;
   while (4 * cw < P.dk) cw *= 2;
   switch (C * cw / THREADS) {  // rows a thread
-    case 8: return launch_grad<T, C, C == 64 ? 8 : 1>(P, cw, par, sm_grad, s);
-    case 4: return launch_grad<T, C, C >= 32 ? 4 : 1>(P, cw, par, sm_grad, s);
+    case 4: return launch_grad<T, C, C == 32 ? 4 : 1>(P, cw, par, sm_grad, s);
     case 2: return launch_grad<T, C, 2>(P, cw, par, sm_grad, s);
     default: return launch_grad<T, C, 1>(P, cw, par, sm_grad, s);
   }
@@ -807,7 +779,7 @@ cudaError_t launch_c(SimtArgs P, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_t(const SimtArgs& P, cudaStream_t s) {
-  return P.C == 64 ? launch_c<T, 64>(P, s) : P.C == 32 ? launch_c<T, 32>(P, s) : launch_c<T, 16>(P, s);
+  return P.C == 32 ? launch_c<T, 32>(P, s) : launch_c<T, 16>(P, s);
 }
 
 }  // namespace
