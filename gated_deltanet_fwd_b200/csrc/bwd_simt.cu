@@ -716,6 +716,9 @@ __global__ void __launch_bounds__(THREADS) ggrad_kernel(const SimtArgs P, int CW
       }
       k0 = __shfl_up_sync(0xffffffffu, k0, 1);
       k0 = lane > 0 ? k0 : 0.0f;
+      // the first token's decay multiplies the initial state: without one its gradient is zero, where the pairs
+      // in a0 cancel only up to their rounding
+      if (lane == 0 && ch.first && !P.S0) a0 = f = 0.0f;
       if (lane < L) ((T*)P.dg)[(t0 + lane) * P.Hv + h] = from_f<T>(a0 + f + k0);
     }
   }

@@ -158,6 +158,23 @@ def test_against_differences(dtype, d):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,dk,dv,chunk", [("f32", 64, 96, 32), ("f32", 128, 128, 64), ("bf16", 48, 32, 16),
+                                               ("bf16", 128, 128, 32), ("bf16", 128, 128, 64)])
+@pytest.mark.parametrize("packed", [True, False])
+def test_first_token_without_a_state_has_no_decay_gradient(dtype, dk, dv, chunk, packed):
+    """Exactly zero, also on the CUDA-core path (the last bf16 case has fewer than 512 gate values); not so for
+    the first token of a later chunk, nor with a state."""
+    lens, Hv = ([100, 1, 0, 64, 35] if packed else [70, 70]), 2
+    x = make(lens, 1, Hv, dk, dv, dtype, False, packed, seed=83)
+    first = [sum(lens[:n]) for n in range(len(lens)) if lens[n]]
+    dg = call(x, chunk)[3].reshape(-1, Hv)
+    assert (dg[first] == 0).all()
+    assert (dg[1:chunk + 1] != 0).any(1).all()
+    x = make(lens, 1, Hv, dk, dv, dtype, True, packed, seed=83)
+    assert (call(x, chunk)[3].reshape(-1, Hv)[first] != 0).all()
+
+
+@gpu
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128)])
 def test_strided_inputs_match_dense(dtype, d):
     lens, Hk, Hv = [77, 60], 1, 2
