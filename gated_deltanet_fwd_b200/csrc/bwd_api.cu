@@ -90,6 +90,30 @@ bool norm_dim_ok(int dim) {
   return dim == 8 || dim == 16 || dim == 32 || dim == 64 || dim == 128 || dim == 256;
 }
 
+// gdn_gates_bwd of the tokens that cu_seqlens spans, of all where it is null
+gdn_status gates_bwd(const void* a, const void* b, gdn_dtype dtype, const float* A_log,
+                     const float* dt_bias, const void* dg, const void* dbeta,
+                     const int32_t* cu_seqlens, int N, int64_t n_tok, int Hv, void* da,
+                     void* db, float* dA_log, float* ddt_bias, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (bad_dtype(dtype) || n_tok < 0 || Hv < 1 || N < 0) return GDN_ERR_INVALID_ARG;
+  if (!A_log || !dt_bias || !dA_log || !ddt_bias) return GDN_ERR_INVALID_ARG;
+  if (n_tok > 0 && (!a || !b || !dg || !dbeta || !da || !db)) return GDN_ERR_INVALID_ARG;
+  if (!aligned_to(elem(dtype), a, b, dg, dbeta, da, db) ||
+      !aligned_to(4, A_log, dt_bias, dA_log, ddt_bias, cu_seqlens))
+    return GDN_ERR_INVALID_ARG;
+  if (!ws_ok(workspace, workspace_bytes, gdn_gates_bwd_workspace_size(n_tok, Hv)))
+    return GDN_ERR_INVALID_ARG;
+  const size_t n = (size_t)n_tok * Hv * elem(dtype), hb = (size_t)Hv * sizeof(float);
+  const Span in[] = {{a, n},      {b, n},        {dg, n}, {dbeta, n},
+                     {A_log, hb}, {dt_bias, hb}, {cu_seqlens, (size_t)(N + 1) * 4}};
+  const Span out[] = {{da, n}, {db, n}, {dA_log, hb}, {ddt_bias, hb}, {workspace, workspace_bytes}};
+  if (clash(in, out)) return GDN_ERR_INVALID_ARG;
+  return from_cuda(launch_gates_bwd(a, b, dtype, A_log, dt_bias, dg, dbeta, TokRange{cu_seqlens, N}, n_tok,
+                                    Hv, da, db, dA_log, ddt_bias, (float*)workspace,
+                                    gates_parts(n_tok), as_stream(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -106,21 +130,18 @@ gdn_status gdn_gates_bwd(const void* a, const void* b, gdn_dtype dtype, const fl
                          int Hv, void* da, void* db, float* dA_log, float* ddt_bias,
                          void* workspace, size_t workspace_bytes, void* stream) {
   CallRange range_("gdn_gates_bwd");
-  if (bad_dtype(dtype) || n_tok < 0 || Hv < 1) return GDN_ERR_INVALID_ARG;
-  if (!A_log || !dt_bias || !dA_log || !ddt_bias) return GDN_ERR_INVALID_ARG;
-  if (n_tok > 0 && (!a || !b || !dg || !dbeta || !da || !db)) return GDN_ERR_INVALID_ARG;
-  if (!aligned_to(elem(dtype), a, b, dg, dbeta, da, db) ||
-      !aligned_to(4, A_log, dt_bias, dA_log, ddt_bias))
-    return GDN_ERR_INVALID_ARG;
-  if (!ws_ok(workspace, workspace_bytes, gdn_gates_bwd_workspace_size(n_tok, Hv)))
-    return GDN_ERR_INVALID_ARG;
-  const size_t n = (size_t)n_tok * Hv * elem(dtype), hb = (size_t)Hv * sizeof(float);
-  const Span in[] = {{a, n}, {b, n}, {dg, n}, {dbeta, n}, {A_log, hb}, {dt_bias, hb}};
-  const Span out[] = {{da, n}, {db, n}, {dA_log, hb}, {ddt_bias, hb}, {workspace, workspace_bytes}};
-  if (clash(in, out)) return GDN_ERR_INVALID_ARG;
-  return from_cuda(launch_gates_bwd(a, b, dtype, A_log, dt_bias, dg, dbeta, n_tok, Hv, da, db,
-                                    dA_log, ddt_bias, (float*)workspace, gates_parts(n_tok),
-                                    as_stream(stream)));
+  return gates_bwd(a, b, dtype, A_log, dt_bias, dg, dbeta, nullptr, 0, n_tok, Hv, da, db, dA_log, ddt_bias,
+                   workspace, workspace_bytes, stream);
+}
+
+gdn_status gdn_gates_bwd_varlen(const void* a, const void* b, gdn_dtype dtype, const float* A_log,
+                                const float* dt_bias, const void* dg, const void* dbeta,
+                                const int32_t* cu_seqlens, int N, int64_t n_tok, int Hv, void* da,
+                                void* db, float* dA_log, float* ddt_bias, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  CallRange range_("gdn_gates_bwd_varlen");
+  return gates_bwd(a, b, dtype, A_log, dt_bias, dg, dbeta, cu_seqlens, N, n_tok, Hv, da, db, dA_log, ddt_bias,
+                   workspace, workspace_bytes, stream);
 }
 
 // ------------------------------------------------------------------- 8-bit checkpoints -----

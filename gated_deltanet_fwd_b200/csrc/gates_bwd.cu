@@ -18,7 +18,7 @@ template <typename T, int VEC>
 __global__ void __launch_bounds__(256) gates_bwd_kernel(
     const T* __restrict__ a, const T* __restrict__ b, const float* __restrict__ A_log,
     const float* __restrict__ dt_bias, const T* __restrict__ dg, const T* __restrict__ dbeta,
-    int64_t n_tok, int Hv, T* __restrict__ da, T* __restrict__ db, float* __restrict__ part) {
+    TokRange range, int64_t n_tok, int Hv, T* __restrict__ da, T* __restrict__ db, float* __restrict__ part) {
   const int cols = Hv / VEC;                      // head groups
   const int tile = cols < 256 ? cols : 256;       // of this block's width
   const int per = 256 / tile;                     // tokens at once
@@ -31,8 +31,10 @@ __global__ void __launch_bounds__(256) gates_bwd_kernel(
     eA[i] = on ? expf(__ldg(A_log + h + i)) : 0.0f;
     bias[i] = on ? __ldg(dt_bias + h + i) : 0.0f;
   }
+  int64_t t_beg, t_end;
+  tok_range(range, n_tok, t_beg, t_end);
   if (on) {
-    for (int64_t t = (int64_t)blockIdx.x * per + row; t < n_tok; t += (int64_t)gridDim.x * per) {
+    for (int64_t t = t_beg + (int64_t)blockIdx.x * per + row; t < t_end; t += (int64_t)gridDim.x * per) {
       const int64_t at = t * Hv + h;
       float av[VEC], bv[VEC], gv[VEC], ev[VEC];
       if constexpr (VEC == 8) {
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict
 
 template <typename T, int VEC>
 cudaError_t run(const T* a, const T* b, const float* A_log, const float* dt_bias, const T* dg,
-                const T* dbeta, int64_t n_tok, int Hv, T* da, T* db, float* dA, float* ddt, float* part,
+                const T* dbeta, TokRange range, int64_t n_tok, int Hv, T* da, T* db, float* dA, float* ddt, float* part,
                 int64_t max_parts, cudaStream_t s) {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
@@ -132,8 +134,8 @@ cudaError_t run(const T* a, const T* b, const float* A_log, const float* dt_bias
   if (blocks > cap) blocks = cap;
   const dim3 grid((unsigned)blocks, (unsigned)((cols + tile - 1) / tile));
   if (blocks > 0)
-    gates_bwd_kernel<T, VEC><<<grid, 256, 0, s>>>(a, b, A_log, dt_bias, dg, dbeta, n_tok, Hv, da,
-                                                  db, part);
+    gates_bwd_kernel<T, VEC><<<grid, 256, 0, s>>>(a, b, A_log, dt_bias, dg, dbeta, range, n_tok, Hv,
+                                                  da, db, part);
   const cudaError_t e = cudaGetLastError();
   const int64_t width = 2 * (int64_t)Hv;
   return e == cudaSuccess ? launch_sum_parts(part, blocks, width, Hv, dA, ddt, width, s) : e;
@@ -141,14 +143,14 @@ cudaError_t run(const T* a, const T* b, const float* A_log, const float* dt_bias
 
 template <typename T>
 cudaError_t pick(const void* a, const void* b, const float* A_log, const float* dt_bias,
-                 const void* dg, const void* dbeta, int64_t n_tok, int Hv, void* da, void* db,
+                 const void* dg, const void* dbeta, TokRange range, int64_t n_tok, int Hv, void* da, void* db,
                  float* dA, float* ddt, float* part, int64_t max_parts, cudaStream_t s) {
   // vector loads need whole 16-byte groups of heads
   const bool vec = Hv % 8 == 0 && aligned16(a) && aligned16(b) && aligned16(dg) &&
                    aligned16(dbeta) && aligned16(da) && aligned16(db);
-  return vec ? run<T, 8>((const T*)a, (const T*)b, A_log, dt_bias, (const T*)dg, (const T*)dbeta,
+  return vec ? run<T, 8>((const T*)a, (const T*)b, A_log, dt_bias, (const T*)dg, (const T*)dbeta, range,
                          n_tok, Hv, (T*)da, (T*)db, dA, ddt, part, max_parts, s)
-             : run<T, 1>((const T*)a, (const T*)b, A_log, dt_bias, (const T*)dg, (const T*)dbeta,
+             : run<T, 1>((const T*)a, (const T*)b, A_log, dt_bias, (const T*)dg, (const T*)dbeta, range,
                          n_tok, Hv, (T*)da, (T*)db, dA, ddt, part, max_parts, s);
 }
 
@@ -162,13 +164,13 @@ cudaError_t launch_sum_parts(const float* part, int64_t parts, int64_t width, in
 }
 
 cudaError_t launch_gates_bwd(const void* a, const void* b, gdn_dtype dt, const float* A_log,
-                             const float* dt_bias, const void* dg, const void* dbeta,
+                             const float* dt_bias, const void* dg, const void* dbeta, TokRange range,
                              int64_t n_tok, int Hv, void* da, void* db, float* dA, float* ddt,
                              float* part, int64_t max_parts, cudaStream_t s) {
-  return dt == GDN_BF16 ? pick<__nv_bfloat16>(a, b, A_log, dt_bias, dg, dbeta, n_tok, Hv, da, db,
-                                              dA, ddt, part, max_parts, s)
-                        : pick<float>(a, b, A_log, dt_bias, dg, dbeta, n_tok, Hv, da, db, dA, ddt,
-                                      part, max_parts, s);
+  return dt == GDN_BF16 ? pick<__nv_bfloat16>(a, b, A_log, dt_bias, dg, dbeta, range, n_tok, Hv, da,
+                                              db, dA, ddt, part, max_parts, s)
+                        : pick<float>(a, b, A_log, dt_bias, dg, dbeta, range, n_tok, Hv, da, db, dA,
+                                      ddt, part, max_parts, s);
 }
 
 }  // namespace gdn

@@ -160,8 +160,22 @@ cudaError_t launch_decode_fused(const void* mix, const void* a, const void* b, c
 // ---- training: backward passes and 8-bit activation checkpoints.  `part` holds up to max_parts partial
 // rows of the sums over tokens.
 
+// With cu set only the tokens of [cu[0], cu[N]) take part, clamped to the tensor.
+struct TokRange {
+  const int32_t* cu;
+  int N;
+};
+__device__ __forceinline__ void tok_range(const TokRange& r, int64_t n_tok, int64_t& beg, int64_t& end) {
+  beg = 0;
+  end = n_tok;
+  if (r.cu) {
+    beg = max((int64_t)0, min((int64_t)r.cu[0], n_tok));
+    end = max(beg, min((int64_t)r.cu[r.N], n_tok));
+  }
+}
+
 cudaError_t launch_gates_bwd(const void* a, const void* b, gdn_dtype dt, const float* A_log,
-                             const float* dt_bias, const void* dg, const void* dbeta,
+                             const float* dt_bias, const void* dg, const void* dbeta, TokRange range,
                              int64_t n_tok, int Hv, void* da, void* db, float* dA, float* ddt,
                              float* part, int64_t max_parts, cudaStream_t s);
 

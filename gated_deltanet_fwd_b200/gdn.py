@@ -48,6 +48,8 @@ SIGNATURES = {
                            _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "gdn_gates_bwd_workspace_size": (_SZ, [_I64, _I]),
     "gdn_gates_bwd": (_I, [_P, _P, _I, _P, _P, _P, _P, _I64, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "gdn_gates_bwd_varlen": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I64, _I, _P, _P, _P, _P, _P,
+                                  _SZ, _P]),
     "gdn_gated_rmsnorm_bwd_workspace_size": (_SZ, [_I64, _I]),
     "gdn_gated_rmsnorm_bwd": (_I, [_P, _P, _P, _P, _P, _I, _P, _F, _I64, _I, _P, _P, _P, _P, _SZ,
                                    _P]),
@@ -368,7 +370,10 @@ def gdn_chunk_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, cu_seq
     q, k, v (possibly strided views), g, beta, scale, initial_state, cu_seqlens as given to the forward;
     dout [B, T, Hv, dv]; dfinal_state [N, Hv, dv, dk] fp32 or None (zero).  dg and dbeta are of
     the activations' dtype.  dinitial_state is computed when initial_state is given, unless
-    output_dinitial_state says otherwise; else None.
+    output_dinitial_state says otherwise; else None.  Tokens outside every sequence of cu_seqlens are
+    not written: tensors that are given keep what they held there, dg and dbeta made here hold zeros, and
+    dq, dk and dv made here anything (gdn_causal_conv1d_silu_bwd with the same cu_seqlens does not
+    read those rows).
     """
     _all_cuda(g, beta, dout, initial_state, cu_seqlens, dfinal_state, dq, dk, dv, dg, dbeta,
               dinitial_state, workspace)
@@ -389,6 +394,8 @@ def gdn_chunk_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, cu_seq
     _shape((N, Hv, d_v, d_k), initial_state, dfinal_state, dinitial_state)
     new = lambda t, shape: dout.new_empty(shape) if t is None else t  # noqa: E731
     dq, dk, dv = new(dq, (B, T, Hk, d_k)), new(dk, (B, T, Hk, d_k)), new(dv, (B, T, Hv, d_v))
+    if cu_seqlens is not None and dg is None and dbeta is None:
+        dg, dbeta = dout.new_zeros((2, B, T, Hv)).unbind()
     dg, dbeta = new(dg, (B, T, Hv)), new(dbeta, (B, T, Hv))
     if output_dinitial_state is None:
         output_dinitial_state = initial_state is not None
@@ -406,9 +413,13 @@ def gdn_chunk_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, cu_seq
 
 
 def gdn_gates_bwd(a, b, A_log, dt_bias, dg, dbeta, da=None, db=None, dA_log=None, ddt_bias=None,
-                  workspace=None):
-    """Gradients of gdn_gates: (da, db, dA_log, ddt_bias).  a, b, dg, dbeta: [..., Hv] of one dtype."""
-    _all_cuda(a, b, A_log, dt_bias, dg, dbeta, da, db, dA_log, ddt_bias, workspace)
+                  workspace=None, cu_seqlens=None):
+    """Gradients of gdn_gates: (da, db, dA_log, ddt_bias).  a, b, dg, dbeta: [..., Hv] of one dtype.
+
+    With cu_seqlens, as after gdn_chunk_bwd with the same, tokens outside every sequence take no part:
+    da and db made here are zero there, tensors that are given keep what they held.
+    """
+    _all_cuda(a, b, A_log, dt_bias, dg, dbeta, da, db, dA_log, ddt_bias, workspace, cu_seqlens)
     Hv = A_log.numel()
     _same(a.dtype, b, dg, dbeta, da, db)
     _same(torch.float32, A_log, dt_bias, dA_log, ddt_bias)
@@ -416,15 +427,19 @@ def gdn_gates_bwd(a, b, A_log, dt_bias, dg, dbeta, da=None, db=None, dA_log=None
     _shape((Hv,), A_log, dt_bias, dA_log, ddt_bias)
     if a.shape[-1] != Hv:
         raise ValueError("the last dimension of a must be the number of heads")
-    da = torch.empty_like(a) if da is None else da
-    db = torch.empty_like(b) if db is None else db
+    new, N = torch.empty_like, 0
+    if cu_seqlens is not None:
+        _same(torch.int32, cu_seqlens)
+        new, N = torch.zeros_like, cu_seqlens.numel() - 1
+    da = new(a) if da is None else da
+    db = new(b) if db is None else db
     dA_log = torch.empty_like(A_log) if dA_log is None else dA_log
     ddt_bias = torch.empty_like(dt_bias) if ddt_bias is None else ddt_bias
     n_tok, lib = a.numel() // Hv, _lib
     ws, ws_b = _ws(lib.gdn_gates_bwd_workspace_size(n_tok, Hv), workspace, a.device)
-    _run("gdn_gates_bwd", a.device,
-        _adr(a), _adr(b), _dt(a), _adr(A_log), _adr(dt_bias), _adr(dg), _adr(dbeta), n_tok, Hv,
-        _adr(da), _adr(db), _adr(dA_log), _adr(ddt_bias), _adr(ws), ws_b)
+    _run("gdn_gates_bwd_varlen", a.device,
+        _adr(a), _adr(b), _dt(a), _adr(A_log), _adr(dt_bias), _adr(dg), _adr(dbeta),
+        _adr(cu_seqlens), N, n_tok, Hv, _adr(da), _adr(db), _adr(dA_log), _adr(ddt_bias), _adr(ws), ws_b)
     return da, db, dA_log, ddt_bias
 
 

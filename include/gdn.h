@@ -325,12 +325,21 @@ gdn_status gdn_chunk_bwd(const void* q, int64_t q_tok_stride, const void* k, int
  *     dA_log = sum over tokens of dg g              ddt_bias = sum over tokens of da
  * a, b, dg, dbeta, da, db : [n_tok, Hv] dtype.   A_log, dt_bias, dA_log, ddt_bias : [Hv] fp32.
  * n_tok = 0 writes zeros to dA_log and ddt_bias.
+ *
+ * gdn_gates_bwd_varlen takes the tokens [cu_seqlens[0], cu_seqlens[N]) alone, as gdn_chunk_bwd does: what
+ * the others hold reaches no sum, and their rows of da and db are not written.  cu_seqlens NULL: all
+ * tokens.  Entries outside the tensor are clamped to it.
  */
 size_t gdn_gates_bwd_workspace_size(int64_t n_tok, int Hv);
 gdn_status gdn_gates_bwd(const void* a, const void* b, gdn_dtype dtype, const float* A_log,
                          const float* dt_bias, const void* dg, const void* dbeta, int64_t n_tok,
                          int Hv, void* da, void* db, float* dA_log, float* ddt_bias,
                          void* workspace, size_t workspace_bytes, void* stream);
+gdn_status gdn_gates_bwd_varlen(const void* a, const void* b, gdn_dtype dtype, const float* A_log,
+                                const float* dt_bias, const void* dg, const void* dbeta,
+                                const int32_t* cu_seqlens, int N, int64_t n_tok, int Hv, void* da,
+                                void* db, float* dA_log, float* ddt_bias, void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 /*
  * gdn_gated_rmsnorm_bwd -- gradients of gdn_gated_rmsnorm.

@@ -376,6 +376,66 @@ def test_training_step_of_the_layer_core(ckpt):
         assert err <= 5e-5, (n, err)
 
 
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hv", [3, 16])
+@pytest.mark.parametrize("cu", [[0, 40, 75], [4, 4, 30], [0, 0], [100], [-9, 50, 300], [60, 20]])
+def test_gates_outside_every_sequence(cu, Hv, dtype):
+    """Only the tokens that cu_seqlens spans are read and written, whatever the others hold; entries outside the
+    tensor are clamped to it."""
+    gen = torch.Generator().manual_seed(6)
+    n, dt = 100, DT[dtype]
+    lo = min(max(cu[0], 0), n)
+    hi = min(max(cu[-1], lo), n)
+    x = [rn(gen, n, Hv).to(dt) for _ in range(4)]
+    A, bias = rn(gen, Hv), rn(gen, Hv, std=0.1)
+    want = ref.gates_grads(x[0][lo:hi], x[1][lo:hi], A, bias, x[2][lo:hi], x[3][lo:hi])
+    for t in x:
+        t[:lo] = t[hi:] = float("nan")
+    a, b, dg, db_ = (t.cuda() for t in x)
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    held = [torch.full((n, Hv), 7.0, dtype=dt, device="cuda") for _ in range(2)]
+    got = gdn.gdn_gates_bwd(a, b, A.cuda(), bias.cuda(), dg, db_, da=held[0], db=held[1], cu_seqlens=c)
+    new = gdn.gdn_gates_bwd(a, b, A.cuda(), bias.cuda(), dg, db_, cu_seqlens=c)
+    for i in range(2):
+        near(got[i][lo:hi], want[i], dtype)
+        assert torch.equal(got[i][lo:hi], new[i][lo:hi])
+        for rows in (slice(0, lo), slice(hi, n)):
+            assert (held[i][rows] == 7.0).all() and (new[i][rows] == 0.0).all()
+    for y, z, w in zip(got[2:], new[2:], want[2:]):
+        sums(y, w, dtype)
+        assert torch.equal(y, z)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,d", [("f32", 32), ("bf16", 128)])
+@pytest.mark.parametrize("given", [True, False])
+def test_gates_after_the_rule_on_a_padded_batch(given, dtype, d):
+    """The sums over tokens start from dg and dbeta of the rule, whose padding tokens are never written."""
+    from test_bwd_rule import make
+    lens, T, Hv, dt = [250, 0, 40], 320, 2, DT[dtype]
+    x = make(lens, 1, Hv, d, d, dtype, False, seed=89)
+    gen = torch.Generator().manual_seed(7)
+    x["a"], x["b"] = rn(gen, 290, Hv).to(dt), rn(gen, 290, Hv).to(dt)
+    A, bias, cu = rn(gen, Hv).cuda(), rn(gen, Hv, std=0.1).cuda(), x["cu"].cuda()
+    nan = lambda *s: torch.full(s, float("nan"), dtype=dt, device="cuda")
+    pad = lambda t: torch.cat([t, torch.full((T - 290, *t.shape[1:]), float("nan"), dtype=t.dtype)])[None].cuda()
+    t = {n: pad(x[n]) for n in ("q", "k", "v", "g", "beta", "dout", "a", "b")}
+    own = dict(dg=nan(1, T, Hv), dbeta=nan(1, T, Hv)) if given else {}
+    _, _, _, dg, dbeta, _ = gdn.gdn_chunk_bwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["dout"], cu_seqlens=cu,
+                                              **own)
+    if not given:
+        assert (dg[:, 290:] == 0).all() and (dbeta[:, 290:] == 0).all()
+    da, db, dA, ddt = gdn.gdn_gates_bwd(t["a"], t["b"], A, bias, dg, dbeta, cu_seqlens=cu)
+    want = gdn.gdn_gates_bwd(*(v[:, :290].contiguous() for v in (t["a"], t["b"])), A, bias,
+                             *(v[:, :290].contiguous() for v in (dg, dbeta)))
+    assert torch.equal(da[:, :290], want[0]) and torch.equal(db[:, :290], want[1])
+    assert (da[:, 290:] == 0).all() and (db[:, 290:] == 0).all()
+    # the same fp32 terms in another order: a thread's sum over its few tokens
+    for y, w in zip((dA, ddt), want[2:]):
+        sums(y, ref.d64(w), dtype)
+
+
 # ------------------------------------------------------------------------ refusals (CPU) ----
 
 P = 0x7f0000000000
@@ -398,6 +458,18 @@ def test_gates_refusals():
         assert c(**{n: None}) == E, n
     assert c(ws=at(11) + 8) == E and c(wsb=16) == E
     assert c(da=at(1)) == E and c(db=at(7) + 16) == E
+
+
+@no_gpu
+def test_gates_varlen_refusals():
+    f = gdn.load().gdn_gates_bwd_varlen
+
+    def c(a=at(1), cu=at(12), N=2, n=64, da=at(7), ws=at(11), wsb=BIG):
+        return f(a, at(2), 0, at(3), at(4), at(5), at(6), cu, N, n, 8, da, at(8), at(9), at(10), ws, wsb, None)
+
+    assert c(N=-1) == E and c(cu=at(12) + 2) == E and c(a=None) == E and c(n=-1) == E and c(wsb=16) == E
+    assert c(cu=at(7)) == E               # da over cu_seqlens
+    assert c(cu=at(11) + 8) == E          # the workspace over it
 
 
 @no_gpu
