@@ -114,6 +114,33 @@ gdn_status gates_bwd(const void* a, const void* b, gdn_dtype dtype, const float*
                                     gates_parts(n_tok), as_stream(stream)));
 }
 
+// gdn_gated_rmsnorm_bwd of the rows of the tokens that cu_seqlens spans, of all where it is null
+gdn_status rmsnorm_bwd(const void* dy, const void* x, const float* x_scales, const void* z,
+                       const float* z_scales, gdn_dtype dtype, const float* w, float eps,
+                       const int32_t* cu_seqlens, int N, int rows_per_token, int64_t n_rows, int dim,
+                       void* dx, void* dz, float* dw, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  if (bad_dtype(dtype) || n_rows < 0 || dim < 1 || !(eps >= 0.0f)) return GDN_ERR_INVALID_ARG;
+  if (N < 0 || rows_per_token < 1 || n_rows % rows_per_token != 0) return GDN_ERR_INVALID_ARG;
+  if (!norm_dim_ok(dim)) return GDN_ERR_UNSUPPORTED;
+  if (!w || !dw) return GDN_ERR_INVALID_ARG;
+  if (!ws_ok(workspace, workspace_bytes, gdn_gated_rmsnorm_bwd_workspace_size(n_rows, dim)))
+    return GDN_ERR_INVALID_ARG;
+  if ((x_scales == nullptr) != (z_scales == nullptr)) return GDN_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!ptr_ok(dy) || !ptr_ok(x) || !ptr_ok(z) || !ptr_ok(dx) || !ptr_ok(dz)))
+    return GDN_ERR_INVALID_ARG;
+  if (!aligned_to(4, x_scales, z_scales, cu_seqlens, w, dw)) return GDN_ERR_INVALID_ARG;
+  const size_t n = (size_t)n_rows * dim, nb = n * elem(dtype), kept = x_scales ? n : nb;
+  const size_t sb = x_scales ? (size_t)n_rows * sizeof(float) : 0, wb = dim * sizeof(float);
+  const Span in[] = {{dy, nb}, {x, kept}, {z, kept}, {x_scales, sb}, {z_scales, sb}, {w, wb},
+                     {cu_seqlens, (size_t)(N + 1) * 4}};
+  const Span out[] = {{dx, nb}, {dz, nb}, {dw, wb}, {workspace, workspace_bytes}};
+  if (clash(in, out)) return GDN_ERR_INVALID_ARG;
+  return from_cuda(launch_rmsnorm_bwd(dy, x, x_scales, z, z_scales, dtype, w, eps,
+                                      TokRange{cu_seqlens, N}, rows_per_token, n_rows, dim, dx, dz, dw,
+                                      (float*)workspace, norm_parts(n_rows, dim), as_stream(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -215,23 +242,19 @@ gdn_status gdn_gated_rmsnorm_bwd(const void* dy, const void* x, const float* x_s
                                  void* dz, float* dw, void* workspace, size_t workspace_bytes,
                                  void* stream) {
   CallRange range_("gdn_gated_rmsnorm_bwd");
-  if (bad_dtype(dtype) || n_rows < 0 || dim < 1 || !(eps >= 0.0f)) return GDN_ERR_INVALID_ARG;
-  if (!norm_dim_ok(dim)) return GDN_ERR_UNSUPPORTED;
-  if (!w || !dw) return GDN_ERR_INVALID_ARG;
-  if (!ws_ok(workspace, workspace_bytes, gdn_gated_rmsnorm_bwd_workspace_size(n_rows, dim)))
-    return GDN_ERR_INVALID_ARG;
-  if ((x_scales == nullptr) != (z_scales == nullptr)) return GDN_ERR_INVALID_ARG;
-  if (n_rows > 0 && (!ptr_ok(dy) || !ptr_ok(x) || !ptr_ok(z) || !ptr_ok(dx) || !ptr_ok(dz)))
-    return GDN_ERR_INVALID_ARG;
-  if (!aligned_to(4, x_scales, z_scales, w, dw)) return GDN_ERR_INVALID_ARG;
-  const size_t n = (size_t)n_rows * dim, nb = n * elem(dtype), kept = x_scales ? n : nb;
-  const size_t sb = x_scales ? (size_t)n_rows * sizeof(float) : 0, wb = dim * sizeof(float);
-  const Span in[] = {{dy, nb}, {x, kept}, {z, kept}, {x_scales, sb}, {z_scales, sb}, {w, wb}};
-  const Span out[] = {{dx, nb}, {dz, nb}, {dw, wb}, {workspace, workspace_bytes}};
-  if (clash(in, out)) return GDN_ERR_INVALID_ARG;
-  return from_cuda(launch_rmsnorm_bwd(dy, x, x_scales, z, z_scales, dtype, w, eps, n_rows, dim, dx,
-                                      dz, dw, (float*)workspace, norm_parts(n_rows, dim),
-                                      as_stream(stream)));
+  return rmsnorm_bwd(dy, x, x_scales, z, z_scales, dtype, w, eps, nullptr, 0, 1, n_rows, dim, dx, dz, dw,
+                     workspace, workspace_bytes, stream);
+}
+
+gdn_status gdn_gated_rmsnorm_bwd_varlen(const void* dy, const void* x, const float* x_scales,
+                                        const void* z, const float* z_scales, gdn_dtype dtype,
+                                        const float* w, float eps, const int32_t* cu_seqlens, int N,
+                                        int rows_per_token, int64_t n_rows, int dim, void* dx,
+                                        void* dz, float* dw, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  CallRange range_("gdn_gated_rmsnorm_bwd_varlen");
+  return rmsnorm_bwd(dy, x, x_scales, z, z_scales, dtype, w, eps, cu_seqlens, N, rows_per_token, n_rows,
+                     dim, dx, dz, dw, workspace, workspace_bytes, stream);
 }
 
 // -------------------------------------------------------------------------------- conv -----

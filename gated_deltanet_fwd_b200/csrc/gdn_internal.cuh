@@ -183,10 +183,10 @@ cudaError_t launch_rmsnorm_ckpt8(const void* x, const void* z, gdn_dtype dt, con
                                  float eps, int64_t rows, int dim, void* y, int8_t* xc, float* xs,
                                  int8_t* zc, float* zs, cudaStream_t s);
 
-// xs, zs set: x and z are int8 codes with one scale per row
+// xs, zs set: x and z are int8 codes with one scale per row.  A token of the range is `rpt` rows.
 cudaError_t launch_rmsnorm_bwd(const void* dy, const void* x, const float* xs, const void* z,
-                               const float* zs, gdn_dtype dt, const float* w, float eps,
-                               int64_t rows, int dim, void* dx, void* dz, float* dw, float* part,
+                               const float* zs, gdn_dtype dt, const float* w, float eps, TokRange range,
+                               int64_t rpt, int64_t rows, int dim, void* dx, void* dz, float* dw, float* part,
                                int64_t max_parts, cudaStream_t s);
 
 struct ConvBwdArgs {

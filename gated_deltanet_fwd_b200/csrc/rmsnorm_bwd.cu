@@ -114,14 +114,19 @@ template <typename T, int TPR, bool CK>
 __global__ void __launch_bounds__(256) rmsnorm_bwd_kernel(
     const T* __restrict__ dy, const void* __restrict__ x, const float* __restrict__ xs,
     const void* __restrict__ z, const float* __restrict__ zs, const float* __restrict__ w, float eps,
-    int64_t rows, T* __restrict__ dx, T* __restrict__ dz, float* __restrict__ part) {
+    TokRange range, int64_t rpt, int64_t n_tok, T* __restrict__ dx, T* __restrict__ dz,
+    float* __restrict__ part) {
   constexpr int DIM = TPR * 8, PER = 256 / TPR, U = rows_u<T>();
   const int sub = threadIdx.x % TPR, rsub = threadIdx.x / TPR;
   float wv[8], dw[8] = {};
 #pragma unroll
   for (int i = 0; i < 8; ++i) wv[i] = 1.0f + __ldg(w + sub * 8 + i);
+  int64_t beg, rows;
+  tok_range(range, n_tok, beg, rows);
+  beg *= rpt;
+  rows *= rpt;
   const int64_t stride = (int64_t)gridDim.x * PER;
-  for (int64_t rb = (int64_t)blockIdx.x * PER; rb < rows; rb += U * stride) {
+  for (int64_t rb = beg + (int64_t)blockIdx.x * PER; rb < rows; rb += U * stride) {
     Raw8<T> dr[U];
     Kept<T, CK> xr[U], zr[U];
 #pragma unroll
@@ -217,8 +222,8 @@ cudaError_t ckpt_t(const T* x, const T* z, const float* w, float eps, int64_t ro
 
 template <typename T, bool CK>
 cudaError_t bwd_t(const T* dy, const void* x, const float* xs, const void* z, const float* zs,
-                  const float* w, float eps, int64_t rows, int dim, T* dx, T* dz, float* dw,
-                  float* part, int64_t max_parts, cudaStream_t s) {
+                  const float* w, float eps, TokRange range, int64_t rpt, int64_t rows, int dim, T* dx,
+                  T* dz, float* dw, float* part, int64_t max_parts, cudaStream_t s) {
   const int tpr = dim / 8;
   const int64_t per = 256 / tpr * rows_u<T>();
   int64_t blocks = 0;
@@ -228,7 +233,8 @@ cudaError_t bwd_t(const T* dy, const void* x, const float* xs, const void* z, co
     blocks = blocks < cap ? blocks : cap;
     blocks = blocks < max_parts ? blocks : max_parts;
     if (blocks > 0)
-      kern<<<(unsigned)blocks, 256, 0, s>>>(dy, x, xs, z, zs, w, eps, rows, dx, dz, part);
+      kern<<<(unsigned)blocks, 256, 0, s>>>(dy, x, xs, z, zs, w, eps, range, rpt, rows / rpt, dx, dz,
+                                             part);
   };
   switch (tpr) {
     case 1: run(rmsnorm_bwd_kernel<T, 1, CK>); break;
@@ -256,18 +262,18 @@ cudaError_t launch_rmsnorm_ckpt8(const void* x, const void* z, gdn_dtype dt, con
 }
 
 cudaError_t launch_rmsnorm_bwd(const void* dy, const void* x, const float* xs, const void* z,
-                               const float* zs, gdn_dtype dt, const float* w, float eps,
-                               int64_t rows, int dim, void* dx, void* dz, float* dw, float* part,
-                               int64_t max_parts, cudaStream_t s) {
+                               const float* zs, gdn_dtype dt, const float* w, float eps, TokRange range,
+                               int64_t rpt, int64_t rows, int dim, void* dx, void* dz, float* dw,
+                               float* part, int64_t max_parts, cudaStream_t s) {
   using B = __nv_bfloat16;
   if (dt == GDN_BF16)
-    return xs ? bwd_t<B, true>((const B*)dy, x, xs, z, zs, w, eps, rows, dim, (B*)dx, (B*)dz, dw,
-                               part, max_parts, s)
-              : bwd_t<B, false>((const B*)dy, x, xs, z, zs, w, eps, rows, dim, (B*)dx, (B*)dz, dw,
-                                part, max_parts, s);
-  return xs ? bwd_t<float, true>((const float*)dy, x, xs, z, zs, w, eps, rows, dim, (float*)dx,
+    return xs ? bwd_t<B, true>((const B*)dy, x, xs, z, zs, w, eps, range, rpt, rows, dim, (B*)dx, (B*)dz,
+                               dw, part, max_parts, s)
+              : bwd_t<B, false>((const B*)dy, x, xs, z, zs, w, eps, range, rpt, rows, dim, (B*)dx, (B*)dz,
+                                dw, part, max_parts, s);
+  return xs ? bwd_t<float, true>((const float*)dy, x, xs, z, zs, w, eps, range, rpt, rows, dim, (float*)dx,
                                  (float*)dz, dw, part, max_parts, s)
-            : bwd_t<float, false>((const float*)dy, x, xs, z, zs, w, eps, rows, dim, (float*)dx,
+            : bwd_t<float, false>((const float*)dy, x, xs, z, zs, w, eps, range, rpt, rows, dim, (float*)dx,
                                   (float*)dz, dw, part, max_parts, s);
 }
 

@@ -53,6 +53,8 @@ SIGNATURES = {
     "gdn_gated_rmsnorm_bwd_workspace_size": (_SZ, [_I64, _I]),
     "gdn_gated_rmsnorm_bwd": (_I, [_P, _P, _P, _P, _P, _I, _P, _F, _I64, _I, _P, _P, _P, _P, _SZ,
                                    _P]),
+    "gdn_gated_rmsnorm_bwd_varlen": (_I, [_P, _P, _P, _P, _P, _I, _P, _F, _P, _I, _I, _I64, _I, _P,
+                                          _P, _P, _P, _SZ, _P]),
     "gdn_causal_conv1d_silu_bwd_workspace_size": (_SZ, [_I, _I64, _I, _I]),
     "gdn_causal_conv1d_silu_bwd": (_I, [_P, _P, _P, _I, _I, _P, _P, _I, _I64, _I, _I, _P, _I, _I,
                                         _I, _F, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
@@ -443,15 +445,24 @@ def gdn_gates_bwd(a, b, A_log, dt_bias, dg, dbeta, da=None, db=None, dA_log=None
     return da, db, dA_log, ddt_bias
 
 
-def gdn_gated_rmsnorm_bwd(dy, x, z, w, eps=1e-6, dx=None, dz=None, dw=None, workspace=None):
+def gdn_gated_rmsnorm_bwd(dy, x, z, w, eps=1e-6, dx=None, dz=None, dw=None, workspace=None,
+                          cu_seqlens=None):
     """Gradients of gdn_gated_rmsnorm: (dx, dz, dw).
 
-    x and z are the forward's inputs, or their 8-bit checkpoints as (codes, scales) pairs.
+    x and z are the forward's inputs, or their 8-bit checkpoints as (codes, scales) pairs.  With
+    cu_seqlens dy is [.., tokens, heads, dim] and tokens outside every sequence take no part: their rows of
+    dx and dz are not written (anything where they are made here).
     """
     (x, xs), (z, zs) = _kept(x), _kept(z)
     if (xs is None) != (zs is None):
         raise ValueError("x and z must both be activations or both be checkpoints")
-    _all_cuda(dy, x, xs, z, zs, w, dx, dz, dw, workspace)
+    _all_cuda(dy, x, xs, z, zs, w, dx, dz, dw, workspace, cu_seqlens)
+    _same(torch.int32, cu_seqlens)
+    N, per = 0, 1
+    if cu_seqlens is not None:
+        if dy.dim() < 3:
+            raise ValueError("with cu_seqlens dy must be [.., tokens, heads, dim]")
+        N, per = cu_seqlens.numel() - 1, dy.shape[-2]
     dim = dy.shape[-1]
     n_rows = dy.numel() // dim
     _shape(dy.shape, x, z, dx, dz)
@@ -466,8 +477,9 @@ def gdn_gated_rmsnorm_bwd(dy, x, z, w, eps=1e-6, dx=None, dz=None, dw=None, work
     dw = torch.empty_like(w) if dw is None else dw
     lib = _lib
     ws, ws_b = _ws(lib.gdn_gated_rmsnorm_bwd_workspace_size(n_rows, dim), workspace, dy.device)
-    _run("gdn_gated_rmsnorm_bwd", dy.device,
-        _adr(dy), _adr(x), _adr(xs), _adr(z), _adr(zs), _dt(dy), _adr(w), float(eps), n_rows, dim,
+    _run("gdn_gated_rmsnorm_bwd_varlen", dy.device,
+        _adr(dy), _adr(x), _adr(xs), _adr(z), _adr(zs), _dt(dy), _adr(w), float(eps),
+        _adr(cu_seqlens), N, per, n_rows, dim,
         _adr(dx), _adr(dz), _adr(dw), _adr(ws), ws_b)
     return dx, dz, dw
 

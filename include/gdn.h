@@ -348,6 +348,11 @@ gdn_status gdn_gates_bwd_varlen(const void* a, const void* b, gdn_dtype dtype, c
  *                  neither), their 8-bit checkpoints: int8 codes [n_rows, dim] with one fp32 scale
  *                  per row, as gdn_gated_rmsnorm_ckpt8 or gdn_act_pack8 (group = dim) write them.
  * Supported dims as gdn_gated_rmsnorm; dy, x, z, dx, dz 16-byte aligned.  n_rows = 0 writes zeros to dw.
+ *
+ * gdn_gated_rmsnorm_bwd_varlen takes the rows of the tokens [cu_seqlens[0], cu_seqlens[N]) alone, a token being
+ * rows_per_token consecutive rows (its v-heads; n_rows is a multiple): what the others hold, as x does where
+ * gdn_chunk_fwd left out unwritten, reaches no sum, and their rows of dx and dz are not written.
+ * cu_seqlens NULL: all rows.  Entries outside the tensor are clamped to it.
  */
 size_t gdn_gated_rmsnorm_bwd_workspace_size(int64_t n_rows, int dim);
 gdn_status gdn_gated_rmsnorm_bwd(const void* dy, const void* x, const float* x_scales,
@@ -355,6 +360,12 @@ gdn_status gdn_gated_rmsnorm_bwd(const void* dy, const void* x, const float* x_s
                                  const float* w, float eps, int64_t n_rows, int dim, void* dx,
                                  void* dz, float* dw, void* workspace, size_t workspace_bytes,
                                  void* stream);
+gdn_status gdn_gated_rmsnorm_bwd_varlen(const void* dy, const void* x, const float* x_scales,
+                                        const void* z, const float* z_scales, gdn_dtype dtype,
+                                        const float* w, float eps, const int32_t* cu_seqlens, int N,
+                                        int rows_per_token, int64_t n_rows, int dim, void* dx,
+                                        void* dz, float* dw, void* workspace,
+                                        size_t workspace_bytes, void* stream);
 
 /*
  * gdn_causal_conv1d_silu_bwd -- gradients of gdn_causal_conv1d_silu, whose arguments it shares.

@@ -436,6 +436,79 @@ def test_gates_after_the_rule_on_a_padded_batch(given, dtype, d):
         sums(y, ref.d64(w), dtype)
 
 
+@gpu
+@pytest.mark.parametrize("ckpt", [False, True])
+@pytest.mark.parametrize("dtype,H,dim", [("bf16", 3, 128), ("f32", 2, 64), ("bf16", 1, 8)])
+@pytest.mark.parametrize("cu", [[0, 40, 75], [4, 4, 30], [0, 0], [100], [-9, 50, 300], [60, 20]])
+def test_norm_outside_every_sequence(cu, dtype, H, dim, ckpt):
+    """As for the gates: rows of other tokens are neither read nor written."""
+    gen = torch.Generator().manual_seed(8)
+    n, dt, eps = 100, DT[dtype], 1e-6
+    lo = min(max(cu[0], 0), n)
+    hi = min(max(cu[-1], lo), n)
+    dy, x, z = (rn(gen, n, H, dim).to(dt) for _ in range(3))
+    w = rn(gen, dim, std=0.1)
+    for t in (dy, x, z):
+        t[:lo] = t[hi:] = float("nan")
+    dy, x, z = (t.cuda() for t in (dy, x, z))
+    kept = [gdn.gdn_act_pack8(t, dim) for t in (x, z)] if ckpt else [x, z]
+    vals = [ref.d64(k[0][lo:hi]) * ref.d64(k[1][lo:hi]) if ckpt else ref.d64(k[lo:hi]) for k in kept]
+    want = ref.norm_grads(dy[lo:hi], *vals, w, eps)
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    held = [torch.full((n, H, dim), 7.0, dtype=dt, device="cuda") for _ in range(2)]
+    got = gdn.gdn_gated_rmsnorm_bwd(dy, *kept, w.cuda(), dx=held[0], dz=held[1], cu_seqlens=c)
+    for y, v in zip(got[:2], want):
+        near(y[lo:hi], v, dtype)
+        assert (y[:lo] == 7.0).all() and (y[hi:] == 7.0).all()
+    sums(got[2], want[2], dtype)
+
+
+@gpu
+@pytest.mark.parametrize("ckpt", [False, True])
+@pytest.mark.parametrize("dtype,d", [("f32", 32), ("bf16", 128)])
+def test_training_step_on_a_padded_batch(dtype, d, ckpt):
+    """Sequences packed into a longer row: NaN in every padding row of the inputs and in every buffer that a
+    call leaves partly unwritten.  Each gradient has the bits, and each sum over tokens the value, of the
+    step on the packed tokens alone."""
+    lens, pad_, Hk, Hv, K, dt = [250, 0, 40], 30, 1, 2, 4, DT[dtype]
+    C, n = 2 * Hk * d + Hv * d, sum(lens)
+    gen = torch.Generator().manual_seed(9)
+    p = dict(mix=rn(gen, n, C), a=rn(gen, n, Hv), b=rn(gen, n, Hv), z=rn(gen, n, Hv, d), dy=rn(gen, n, Hv, d))
+    w = dict(w=(torch.rand(C, K, generator=gen) * 2 - 1) / 2, A=torch.log(torch.rand(Hv, generator=gen) * 3 + 1),
+             dt=rn(gen, Hv, std=0.1), nw=rn(gen, d, std=0.1))
+    w = {m: v.cuda() for m, v in w.items()}
+    cu = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32).cuda()
+
+    def step(T):
+        nan = lambda *s, t=dt: torch.full((1, T, *s), float("nan"), dtype=t, device="cuda")
+        t = {m: nan(*v.shape[1:]) for m, v in p.items()}
+        for m, v in p.items():
+            t[m][0, :n] = v.to(dt)
+        y = gdn.gdn_causal_conv1d_silu(t["mix"], w["w"], cu_seqlens=cu, n_l2norm_ch=2 * Hk * d, l2norm_group=d,
+                                       y=nan(C))
+        q, k, v = (s.unflatten(-1, (-1, d)) for s in y.split([Hk * d, Hk * d, Hv * d], -1))
+        g, beta = gdn.gdn_gates(t["a"], t["b"], w["A"], w["dt"])
+        # the rule's output, as any: what a forward leaves behind the last sequence is not defined
+        o = nan(Hv, d)
+        o[0, :n] = (v[0, :n].float() * beta[0, :n, :, None]).to(dt)
+        o8, z8 = (o, t["z"]) if not ckpt else gdn.gdn_gated_rmsnorm_ckpt8(o, t["z"], w["nw"])[1:]
+        mix8 = gdn.gdn_act_pack8(t["mix"], group=32) if ckpt else t["mix"]
+        do, dz, dnw = gdn.gdn_gated_rmsnorm_bwd(t["dy"], o8, z8, w["nw"], dx=nan(Hv, d), cu_seqlens=cu)
+        dq, dk, dv, dg, db, _ = gdn.gdn_chunk_bwd(q, k, v, g, beta, do, cu_seqlens=cu, dq=nan(Hk, d), dk=nan(Hk, d),
+                                                  dv=nan(Hv, d), dg=nan(Hv), dbeta=nan(Hv))
+        da, dbb, dA, ddt = gdn.gdn_gates_bwd(t["a"], t["b"], w["A"], w["dt"], dg, db, cu_seqlens=cu)
+        dmix, dw, _, _ = gdn.gdn_causal_conv1d_silu_bwd(torch.cat([s.flatten(2) for s in (dq, dk, dv)], -1), mix8,
+                                                        w["w"], cu_seqlens=cu, n_l2norm_ch=2 * Hk * d, l2norm_group=d)
+        return dict(dmix=dmix, dz=dz, da=da, db=dbb), dict(dw=dw, dnw=dnw, dA=dA, ddt=ddt)
+
+    rows, total = step(n)
+    padded, total2 = step(n + pad_)
+    for m in rows:
+        assert torch.equal(padded[m][:, :n], rows[m]), m
+    for m in total:  # the same terms, split into other ranges
+        sums(total2[m], ref.d64(total[m]), m)
+
+
 # ------------------------------------------------------------------------ refusals (CPU) ----
 
 P = 0x7f0000000000
@@ -494,6 +567,17 @@ def test_norm_refusals():
     for n in ("x", "z", "y", "xc", "xs", "zc", "zs"):
         assert k(**{n: None}) == E, n
     assert k(y=at(2)) == E and k(y=at(1) + 16) == E and k(zc=at(4)) == E and k(xc=at(1)) == E
+
+
+@no_gpu
+def test_norm_varlen_refusals():
+    f = gdn.load().gdn_gated_rmsnorm_bwd_varlen
+
+    def c(dy=at(1), cu=at(12), N=2, per=4, n=64, dx=at(5), ws=at(8), wsb=BIG):
+        return f(dy, at(2), None, at(3), None, 0, at(4), 1e-6, cu, N, per, n, 128, dx, at(6), at(7), ws, wsb, None)
+
+    assert c(N=-1) == E and c(per=0) == E and c(per=7) == E and c(cu=at(12) + 2) == E
+    assert c(dy=None) == E and c(wsb=64) == E and c(cu=at(5)) == E and c(cu=at(8) + 8) == E
 
 
 @no_gpu
