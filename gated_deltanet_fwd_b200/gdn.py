@@ -358,6 +358,13 @@ def _shape(shape, *ts):
             raise ValueError(f"expected tensors of shape {tuple(shape)}")
 
 
+def _width(t):
+    """The last dimension of a tensor, which must not be empty."""
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError("the last dimension must have at least one element")
+    return t.shape[-1]
+
+
 def chunk_bwd_workspace_size(dtype, N, B, T, Hk, Hv, dk, dv, chunk=64):
     """Bytes of workspace for gdn_chunk_bwd with activations of the torch dtype."""
     dt = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}[dtype]
@@ -427,7 +434,7 @@ def gdn_gates_bwd(a, b, A_log, dt_bias, dg, dbeta, da=None, db=None, dA_log=None
     _same(torch.float32, A_log, dt_bias, dA_log, ddt_bias)
     _shape(a.shape, b, dg, dbeta, da, db)
     _shape((Hv,), A_log, dt_bias, dA_log, ddt_bias)
-    if a.shape[-1] != Hv:
+    if Hv < 1 or a.shape[-1] != Hv:
         raise ValueError("the last dimension of a must be the number of heads")
     new, N = torch.empty_like, 0
     if cu_seqlens is not None:
@@ -463,7 +470,7 @@ def gdn_gated_rmsnorm_bwd(dy, x, z, w, eps=1e-6, dx=None, dz=None, dw=None, work
         if dy.dim() < 3:
             raise ValueError("with cu_seqlens dy must be [.., tokens, heads, dim]")
         N, per = cu_seqlens.numel() - 1, dy.shape[-2]
-    dim = dy.shape[-1]
+    dim = _width(dy)
     n_rows = dy.numel() // dim
     _shape(dy.shape, x, z, dx, dz)
     _shape((dim,), w, dw)
@@ -508,7 +515,7 @@ def gdn_causal_conv1d_silu_bwd(dy, x, w, bias=None, cu_seqlens=None, n_l2norm_ch
     _same(torch.int32, cu_seqlens)
     group = 0
     if xs is not None:
-        if xs.shape[:-1] != dy.shape[:-1] or C % xs.shape[-1]:
+        if xs.shape[:-1] != dy.shape[:-1] or C % _width(xs):
             raise ValueError("scales must be [B, T, C / group]")
         group = C // xs.shape[-1]
     dx = torch.empty_like(dy) if dx is None else dx
@@ -531,7 +538,7 @@ def gdn_causal_conv1d_silu_bwd(dy, x, w, bias=None, cu_seqlens=None, n_l2norm_ch
 def gdn_act_pack8(x, group=128, codes=None, scales=None):
     """x [..., dim] -> (codes int8 of x's shape, scales fp32 [..., dim / group])."""
     _all_cuda(x, codes, scales)
-    dim = x.shape[-1]
+    dim = _width(x)
     if group < 1 or dim % group:
         raise ValueError("group must divide the last dimension")
     codes = torch.empty(x.shape, dtype=torch.int8, device=x.device) if codes is None else codes
@@ -551,8 +558,8 @@ def gdn_act_unpack8(codes, scales, dtype=torch.bfloat16, x=None):
     _all_cuda(codes, scales, x)
     _same(torch.int8, codes)
     _same(torch.float32, scales)
-    dim = codes.shape[-1]
-    if codes.shape[:-1] != scales.shape[:-1] or dim % scales.shape[-1]:
+    dim = _width(codes)
+    if codes.shape[:-1] != scales.shape[:-1] or dim % _width(scales):
         raise ValueError("scales must be [..., dim / group]")
     x = torch.empty(codes.shape, dtype=dtype, device=codes.device) if x is None else x
     _shape(codes.shape, x)
@@ -568,7 +575,7 @@ def gdn_gated_rmsnorm_ckpt8(x, z, w, eps=1e-6, y=None):
     The pairs go to gdn_gated_rmsnorm_bwd; y may be x (in place).
     """
     _all_cuda(x, z, w, y)
-    dim = x.shape[-1]
+    dim = _width(x)
     y = torch.empty_like(x) if y is None else y
     _shape(x.shape, z, y)
     _shape((dim,), w)

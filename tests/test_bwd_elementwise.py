@@ -649,6 +649,28 @@ def test_binding_refusals():
                           workspace=z(64, dt=torch.uint8))
 
 
+@gpu
+def test_binding_refuses_empty_last_dimensions():
+    """ValueError, as for every other shape that does not fit; no rows at all are not refused."""
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")
+    i8, f32 = torch.int8, torch.float32
+    ck = lambda *s: (z(*s, 64, dt=i8), z(*s, 0, dt=f32))
+    for call in (lambda: gdn.gdn_act_unpack8(*ck(2)),
+                 lambda: gdn.gdn_act_unpack8(*ck(0)),
+                 lambda: gdn.gdn_act_unpack8(z(2, 0, dt=i8), z(2, 1, dt=f32)),
+                 lambda: gdn.gdn_act_pack8(z(2, 0), group=64),
+                 lambda: gdn.gdn_act_pack8(z(()), group=64),
+                 lambda: gdn.gdn_gated_rmsnorm_bwd(z(2, 0), z(2, 0), z(2, 0), z(0, dt=f32)),
+                 lambda: gdn.gdn_gated_rmsnorm_ckpt8(z(2, 0), z(2, 0), z(0, dt=f32)),
+                 lambda: gdn.gdn_gates_bwd(z(2, 0), z(2, 0), z(0, dt=f32), z(0, dt=f32), z(2, 0), z(2, 0)),
+                 lambda: gdn.gdn_causal_conv1d_silu_bwd(z(1, 0, 64), ck(1, 0), z(64, 4, dt=f32))):
+        with pytest.raises(ValueError):
+            call()
+    assert gdn.gdn_act_unpack8(z(0, 64, dt=i8), z(0, 1, dt=f32)).shape == (0, 64)
+    assert gdn.gdn_act_pack8(z(0, 64), group=64)[1].shape == (0, 1)
+    assert gdn.gdn_gated_rmsnorm_ckpt8(z(0, 64), z(0, 64), z(64, dt=f32))[0].shape == (0, 64)
+
+
 @no_gpu
 def test_addresses_between_elements_are_refused():
     """Vectors that are read one element at a time have to lie on a multiple of that element."""
