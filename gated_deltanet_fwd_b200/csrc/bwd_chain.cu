@@ -665,8 +665,7 @@ cudaError_t launch_bwd_chain(const Args& a, const TcMaps& m, cudaStream_t s) {
   p.Hk = a.Hk;
   p.Hv = a.Hv;
   constexpr uint32_t bytes = Sm<true>::BYTES > Sm<false>::BYTES ? Sm<true>::BYTES : Sm<false>::BYTES;
-  int sms = 0;
-  const cudaError_t e = prepare_kernel<bwd_chain_kernel>(bytes, sms);
+  const cudaError_t e = allow_smem(bwd_chain_kernel, bytes);
   if (e != cudaSuccess) return e;
   bwd_chain_kernel<<<(unsigned)units, THREADS, bytes, s>>>(m.k, m.v, m.dout, m.t, m.tp, m.dv, p);
   return cudaGetLastError();

@@ -749,7 +749,8 @@ cudaError_t launch_bwd_grads(const Args& a, const TcMaps& m, cudaStream_t s) {
   p.Hk = a.Hk;
   p.Hv = a.Hv;
   int sms = 0;
-  const cudaError_t e = prepare_kernel<bwd_grads_kernel>(SM_BYTES, sms);
+  cudaError_t e = sm_count(sms);
+  if (e == cudaSuccess) e = allow_smem(bwd_grads_kernel, SM_BYTES);
   if (e != cudaSuccess) return e;
   const int64_t grid = p.items < sms ? p.items : sms;
   bwd_grads_kernel<<<(unsigned)grid, THREADS, SM_BYTES, s>>>(m.k, m.q, m.dout, m.dv, m.dq, m.dk, p);

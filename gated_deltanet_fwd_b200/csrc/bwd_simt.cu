@@ -740,8 +740,7 @@ __global__ void __launch_bounds__(THREADS) ggrad_kernel(const SimtArgs P, int CW
 
 template <typename T, int C, int RPT>
 cudaError_t launch_grad(const SimtArgs& P, int cw, int64_t par, size_t bytes, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(
-      ggrad_kernel<T, C, RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  const cudaError_t e = allow_smem(ggrad_kernel<T, C, RPT>, bytes);
   if (e != cudaSuccess) return e;
   ggrad_kernel<T, C, RPT><<<(unsigned)par, THREADS, bytes, s>>>(P, cw);
   return cudaGetLastError();
@@ -759,11 +758,8 @@ cudaError_t launch_c(SimtArgs P, cudaStream_t s) {
   P.stages = two ? 2 : 1;
   const size_t sm_grad =
       (2 * (size_t)C * ldk + 3 * C * ldv + 2 * C * ldc + 6 * C + 8) * f + C * 8;
-  auto set = [](auto kern, size_t bytes) {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  };
-  cudaError_t e = set(gprep_kernel<T, C>, sm_prep);
-  if (e == cudaSuccess) e = set(gwalk_kernel<T, C>, sm_walk);
+  cudaError_t e = allow_smem(gprep_kernel<T, C>, sm_prep);
+  if (e == cudaSuccess) e = allow_smem(gwalk_kernel<T, C>, sm_walk);
   if (e != cudaSuccess) return e;
   const int64_t par = P.slots * P.Hk, walks = 2 * (int64_t)P.N * P.Hv * (P.dv / DVS);
   if (par > 0x7fffffff || walks > 0x7fffffff) return cudaErrorInvalidConfiguration;

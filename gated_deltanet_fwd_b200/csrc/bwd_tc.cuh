@@ -61,21 +61,6 @@ struct TcMaps {
   CUtensorMap q, k, v, dout, dq, dk, dv, t, tp;
 };
 
-// Allows a kernel `bytes` of shared memory on the current device and tells the device's SMs; both are asked
-// for once per device and kernel (a benign race between host threads).
-template <auto Kernel>
-cudaError_t prepare_kernel(uint32_t bytes, int& sms) {
-  static int sms_of[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  sms = e == cudaSuccess && dev < 64 ? sms_of[dev] : 0;
-  if (sms > 0 || e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess && dev < 64) sms_of[dev] = sms;
-  return e;
-}
-
 cudaError_t launch_bwd_chain(const Args& a, const TcMaps& m, cudaStream_t s);
 cudaError_t launch_bwd_grads(const Args& a, const TcMaps& m, cudaStream_t s);
 

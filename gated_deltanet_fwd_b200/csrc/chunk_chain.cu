@@ -609,13 +609,8 @@ cudaError_t launch_chunk_chain(const void* q, const void* k, const void* v, TokS
                     : reinterpret_cast<float*>(wsb + tm::states_offset(N, n_tok, Hv));
   p.debug_skip_chunk = g_debug_skip_chunk;
   p.trace = g_chain_trace;
-  static bool attr_set = false;  // idempotent attribute; a benign race between host threads
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(chunk_chain_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, CH_SMEM);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  const cudaError_t e = allow_smem(chunk_chain_kernel, CH_SMEM);
+  if (e != cudaSuccess) return e;
   chunk_chain_kernel<<<(unsigned)units, CH_THREADS, CH_SMEM, s>>>(mq, mk, mv, mtp, p);
   return cudaGetLastError();
 }

@@ -637,22 +637,13 @@ namespace {
 template <bool BWD>
 cudaError_t launch_prep_t(const PrepParams& p, int64_t slots, cudaStream_t s, const CUtensorMap& mk,
                           const CUtensorMap& mq) {
-  static int sms_of[64] = {};  // per device; idempotent, a benign race between host threads
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  int sms = 0;
+  cudaError_t e = sm_count(sms);
+  if (e == cudaSuccess) e = allow_smem(chunk_prep_kernel<BWD>, PP_SMEM);
+  // all of the unified L1 / shared-memory space as shared memory: two CTAs per SM
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(chunk_prep_kernel<BWD>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   if (e != cudaSuccess) return e;
-  int sms = dev < 64 ? sms_of[dev] : 0;
-  if (sms == 0) {
-    e = cudaFuncSetAttribute(chunk_prep_kernel<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             PP_SMEM);
-    // all of the unified L1 / shared-memory space as shared memory: two CTAs per SM
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(chunk_prep_kernel<BWD>,
-                               cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) sms_of[dev] = sms;
-  }
   // persistent: two CTAs per SM, each taking every grid-th (slot, k-head) item
   const int64_t items = slots * p.Hk;
   const int64_t grid = items < 2 * (int64_t)sms ? items : 2 * (int64_t)sms;

@@ -236,13 +236,8 @@ cudaError_t launch_scan_prefix(const int32_t* cu, int N, int B, int64_t T, int H
   float* st = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(ws) +
                                        tm::states_offset(N, n_tok, Hv));
   const size_t smem = PX_SMEM;
-  static bool attr_set = false;  // idempotent attribute; a benign race between host threads
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(scan_prefix_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  const cudaError_t e = allow_smem(scan_prefix_kernel, smem);
+  if (e != cudaSuccess) return e;
   scan_prefix_kernel<<<dim3((unsigned)N, (unsigned)Hv, tm::D / PX_ROWS), PX_THREADS, smem, s>>>(
       cu, T, N, Hv, plan, tm::max_segs(N, n_tok, lseg), st, status);
   return cudaGetLastError();

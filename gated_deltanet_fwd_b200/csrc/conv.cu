@@ -386,13 +386,8 @@ static cudaError_t launch_conv_k(int sms, int64_t n_tok, int slabs, const T* x, 
   if (cols < 1) cols = 1;
   const dim3 grid((unsigned)cols, (unsigned)slabs);
   constexpr int smem = CONV_RING_BYTES * CONV_THREADS;
-  static bool attr_set = false;  // idempotent attribute; a benign race between host threads
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(conv_silu_kernel<T, K>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  const cudaError_t e = allow_smem(conv_silu_kernel<T, K>, smem);
+  if (e != cudaSuccess) return e;
   conv_silu_kernel<T, K><<<grid, CONV_THREADS, smem, s>>>(x, w, bias, n_tok, T_, C, cu, N, n_l2,
                                                           group, l2_eps, cs_in, cs_out, y);
   return cudaGetLastError();

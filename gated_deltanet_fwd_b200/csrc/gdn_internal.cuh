@@ -160,6 +160,18 @@ cudaError_t launch_decode_fused(const void* mix, const void* a, const void* b, c
 // ---- training: backward passes and 8-bit activation checkpoints.  `part` holds up to max_parts partial
 // rows of the sums over tokens.
 
+// Allows a kernel `bytes` of dynamic shared memory on the current device.  Asked at every launch (60 ns): the
+// setting belongs to the device's context, and a process may use several devices, or reset one.
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel* kern, size_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+inline cudaError_t sm_count(int& sms) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
 // With cu set only the tokens of [cu[0], cu[N]) take part, clamped to the tensor.
 struct TokRange {
   const int32_t* cu;
