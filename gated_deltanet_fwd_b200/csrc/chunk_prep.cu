@@ -84,6 +84,7 @@ struct PrepParams {
   int64_t gd_off;  // byte offset of the GD array
   int N, Hk, Hv;
   unsigned long long* trace;  // phase timing (trace builds only), else unused
+  int debug_thread;  // failure-test builds only: this thread's first wait counts as run out
   // fused gates: g and beta computed here from a, b (bf16) when a is set
   const __nv_bfloat16* a;
   const __nv_bfloat16* b;
@@ -424,11 +425,16 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(
     }
     if (h0 == 0) {
       ok = mbar_wait(bar, mma_phase);
+#ifdef GDN_FAULT_INJECTION
+      if (tid == P.debug_thread) ok = false;
+#endif
       mma_phase ^= 1;
       if (!ok) report(P.status, GDN_ERR_TIMEOUT);
     }
     tc_fence_before();
-    if (!__syncthreads_and(ok)) break;
+    // one answer for the CTA: a thread that went on alone would wait at barriers the others never reach
+    ok = __syncthreads_and(ok) != 0;
+    if (!ok) break;
     tc_fence_after();
     // scale Gamma Q of the pair as the swizzled image of two 64-column halves
     if (BWD) {
@@ -631,6 +637,7 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(
 }  // namespace
 
 unsigned long long* g_prep_trace = nullptr;  // trace builds: device buffer of 8 stamps per CTA
+int g_debug_prep_thread = -1;                // failure-test builds: see PrepParams::debug_thread
 
 namespace {
 
@@ -677,6 +684,7 @@ cudaError_t launch_chunk_prep(const void* q, const void* k, TokStrides ts, const
   p.Hk = Hk;
   p.Hv = Hv;
   p.trace = g_prep_trace;
+  p.debug_thread = g_debug_prep_thread;
   p.a = fuse.a;
   p.b = fuse.b;
   p.A_log = fuse.A_log;
@@ -689,6 +697,12 @@ cudaError_t launch_chunk_prep(const void* q, const void* k, TokStrides ts, const
 }
 
 }  // namespace gdn
+
+#ifdef GDN_FAULT_INJECTION
+// Failure-test builds only: in the next prefills and backward passes on the tensor-core path the wait of thread
+// `t` of every preparation CTA counts as run out (-1: none), the other threads' do not.
+extern "C" void gdn_debug_set_prep_thread(int t) { gdn::g_debug_prep_thread = t; }
+#endif
 
 #ifdef GDN_PREP_TRACE
 // Trace builds only: device buffer (8 stamps of 8 bytes per prep CTA) for the phase stamps.

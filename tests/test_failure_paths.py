@@ -134,3 +134,42 @@ def test_chunk_wait_timeout_reports_and_recovers(T, skip):
         assert_bf16_close(S, S_ref, "after a timed-out call: state")
     finally:
         gdn._lib = prev
+
+
+@pytest.mark.parametrize("thread", [0, 37, 255])
+@pytest.mark.parametrize("backward", [False, True])
+def test_one_thread_of_the_preparation_times_out(backward, thread):
+    """The wait for a chunk's products runs out for one thread of each preparation CTA and for no other (an
+    outcome near the limit).  All threads must leave together: each CTA has several items, and a thread that went on
+    to the next would wait at barriers the others never reach.  The call reports it and the next one is right."""
+    import ctypes
+    assert os.path.exists(DEBUG_LIB), "build the failure-test library: __graft_entry__.build()"
+    prev = gdn._lib
+    gdn._lib = None
+    try:
+        lib = gdn.load(DEBUG_LIB)
+        lib.gdn_debug_set_prep_thread.argtypes = [ctypes.c_int]
+        lib.gdn_debug_set_prep_thread.restype = None
+        T, Hk, Hv = 64 * 8, 80, 80  # 640 items on at most 296 CTAs
+        x = inputs.rule_inputs(B=1, T=T, Hk=Hk, Hv=Hv, dk=128, dv=128, seed=3, a_mean=-6.0)
+        g, beta = oracle_gates_f32(x)
+        args = tuple(t.to(DEV) for t in (x["q"], x["k"], x["v"], g, beta))
+        size = gdn.chunk_bwd_workspace_size(torch.bfloat16, 1, 1, T, Hk, Hv, 128, 128) if backward else \
+            gdn.workspace_size(1, 1, T, Hk, Hv, 128, 128, 64)
+        ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+        call = (lambda: gdn.gdn_chunk_bwd(*args, args[2], workspace=ws)) if backward else \
+            (lambda: gdn.gdn_chunk_fwd(*args, workspace=ws))
+        good = call()
+        assert gdn.workspace_status(ws) == gdn.GDN_OK
+        lib.gdn_debug_set_prep_thread(thread)
+        try:
+            call()
+            assert gdn.workspace_status(ws) == gdn.GDN_ERR_TIMEOUT
+        finally:
+            lib.gdn_debug_set_prep_thread(-1)
+        again = call()
+        assert gdn.workspace_status(ws) == gdn.GDN_OK
+        for a, b in zip(good, again):
+            assert b is None or torch.equal(a, b)
+    finally:
+        gdn._lib = prev
