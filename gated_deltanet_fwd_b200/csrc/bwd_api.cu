@@ -70,10 +70,13 @@ int64_t conv_parts(int64_t n_tok, int C) {
   return need < 1 ? 1 : need < most ? need : most;
 }
 // Whether the rule's backward pass runs on tensor cores: the shape of the forward's tensor-core path, and
-// at least 512 gate values (tokens x v-heads).  The tensor-core kernels round their operands to bf16; over
-// many values the relative error of dg and dbeta is 3 to 4e-3, but of a handful each is one dot product,
-// and the norm of that few can be off by more than the 5e-3 promised (5.05e-3 measured at 6 values).  The
-// CUDA-core kernels carry fp32 throughout.  At 100 tokens and 4 v-heads they take 84 us, the tensor cores 47.
+// at least 512 gate values (tokens x v-heads).  The tensor-core kernels round their operands to bf16.  That costs
+// dg 3e-3 of its norm where many independent values make it up, and more where few do, since their sum of squares
+// may happen to be small.  Share of one-head calls whose dg is over 5e-3 of its norm off, 512 to 1024 calls each,
+// at 16, 64, 128, 256, 512 and 1024 tokens: 16, 8, 5, 2, 0.4 and 0.2 % where a token keeps e^-6 of the state on
+// average, 12, 8, 6, 2, 1 and 0.6 % where it keeps 97 % -- but 14 to 31 % at every length where it
+// keeps more than the call is long, which no count of values tells.  The CUDA-core kernels carry fp32
+// throughout.  At 100 tokens and 4 v-heads they take 84 us, the tensor cores 47.
 constexpr int64_t TC_MIN_VALUES = 512;
 bool tensor_cores(gdn_dtype dtype, int64_t n_tok, int Hv, int dk, int dv, int chunk) {
   return dtype == GDN_BF16 && dk == 128 && dv == 128 && chunk == 64 && n_tok * Hv >= TC_MIN_VALUES;

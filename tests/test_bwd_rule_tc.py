@@ -197,3 +197,103 @@ def test_malformed_entry_met_by_running_blocks():
     assert all(torch.equal(a[:, :400], b[:, :400]) for a, b in zip(good[:5], got[:5]))  # well described
     assert all(torch.equal(a, b) for a, b in zip(good[:5], call(x, workspace=ws)[:5]))
     assert gdn.workspace_status(ws) == gdn.GDN_OK
+
+
+def many_heads(T, H, a_mean, kind, states, seed):
+    """A call of H heads, each with its own q and k: for the kernels the same as H calls of one head."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    unit = lambda t: (t / t.norm(dim=-1, keepdim=True)).to(torch.bfloat16)
+    x = dict(q=unit(rn(1, T, H, D)), k=unit(rn(1, T, H, D) + (rn(1, 1, H, D) if kind == "alike" else 0.0)),
+             v=rn(1, T, H, D).to(torch.bfloat16), dout=rn(1, T, H, D).to(torch.bfloat16))
+    A = torch.rand(H, generator=gen, device="cuda") * 15 + 1
+    x["g"] = -A * torch.nn.functional.softplus(rn(1, T, H) + a_mean)
+    x["beta"] = torch.sigmoid(rn(1, T, H) + (2.0 if kind == "strong" else 0.0))
+    x["S0"], x["dST"] = (rn(1, H, D, D) * 0.1 if states else None for _ in range(2))
+    return x
+
+
+def exact_heads(x):
+    """All gradients token by token in 64 bits, and the root sum of squares of the products that dg sums."""
+    f = torch.float64
+    q, k, v, do, beta, decay = (x[n][0].to(f) for n in ("q", "k", "v", "dout", "beta", "g"))
+    decay, scale = decay.exp(), D ** -0.5
+    T, H = beta.shape
+    S = x["S0"][0].to(f) if x["S0"] is not None else torch.zeros(H, D, D, device="cuda", dtype=f)
+    dS = x["dST"][0].to(f) if x["dST"] is not None else torch.zeros_like(S)
+
+    def step(S, t):
+        E = S * decay[t][:, None, None]
+        e = v[t] - (E @ k[t][..., None])[..., 0]
+        return E, e, E + (beta[t][:, None] * e)[..., None] * k[t][:, None, :]
+
+    at = []
+    for t in range(T):
+        at.append(S)
+        S = step(S, t)[2]
+    out = {n: torch.zeros_like(y) for n, y in dict(dq=q, dk=k, dv=v, dg=beta, dbeta=beta, size=beta).items()}
+    for t in reversed(range(T)):
+        E, e, S = step(at.pop(), t)
+        dS = dS + (scale * do[t])[..., None] * q[t][:, None, :]
+        du = (dS @ k[t][..., None])[..., 0]
+        u, b = beta[t][:, None] * e, beta[t][:, None] * du
+        out["dq"][t] = scale * (do[t][:, None, :] @ S)[:, 0]
+        out["dbeta"][t], out["dv"][t] = (du * e).sum(-1), b
+        out["dk"][t] = (u[:, None, :] @ dS)[:, 0] - (b[:, None, :] @ E)[:, 0]
+        dE = dS - b[..., None] * k[t][:, None, :]
+        products = E * dE
+        out["dg"][t], out["size"][t] = products.sum((-1, -2)), products.square().sum((-1, -2)).sqrt()
+        dS = dE * decay[t][:, None, None]
+    return out
+
+
+def errors_by_head(x, chunk=64):
+    """For each output the heads' errors, and their norms; dg's is taken with that of its products."""
+    ws = torch.empty(gdn.chunk_bwd_workspace_size(torch.bfloat16, 1, *x["v"].shape[:2], *[x["v"].shape[2]] * 2, D, D,
+                                                  chunk), dtype=torch.uint8, device="cuda")
+    got = gdn.gdn_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["beta"], x["dout"], initial_state=x["S0"],
+                            dfinal_state=x["dST"], chunk=chunk, workspace=ws)
+    assert gdn.workspace_status(ws) == gdn.GDN_OK
+    want = exact_heads(x)
+    heads = lambda y: y.transpose(0, 1).flatten(1).norm(dim=1)
+    found = {}
+    for n, y in zip(("dq", "dk", "dv", "dg", "dbeta"), got):
+        found[n] = heads(y[0].double() - want[n]), heads(want[n]), heads(want["size"]) if n == "dg" else 0.0
+    return found
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["random", "strong", "alike"])
+@pytest.mark.parametrize("T,H,a_mean,states", [(512, 96, 0.0, False), (520, 64, -6.0, True), (1024, 64, -8.0, False),
+                                               (1000, 64, -10.0, False), (1024, 64, -20.0, True),
+                                               (2048, 32, -10.0, False)])
+def test_errors_of_many_calls(T, H, a_mean, states, kind):
+    """What the header says of the tensor-core path, for each of many one-head calls: keys at random, with strong
+    writes, and with a direction in common; decays from e^-8 a token to none.
+
+    Rounding to bf16 costs 2^-8 / sqrt(6) = 1.6e-3 of an operand's norm.  There are fifteen such operands (T~, P,
+    scale Gamma Q; in either walk the state's copy, X, the update's operand; U, dV, the copies of S and dS, dN, dM:
+    two walks share T~) and the output: if an output depends on all of them in full, sqrt(16) * 1.6e-3 = 6.4e-3.
+    dg[t] = sum of (state x state gradient): the states are made of the updates' operands and their copies are
+    rounded, which is four roundings in full, sqrt(4) * 1.6e-3 = 3.2e-3 of the products' root sum of squares;
+    the others take part through half of a state or less (T~, P, U, the copies and X in the walks: eight at 0.8e-3),
+    together 3.9e-3.  That is one standard deviation, and with one head that forgets nothing all tokens share
+    nearly the same error.  Divided by both norms together, which are alike in the mean, it is 2.8e-3; 1e-2 leaves
+    three and a half of those."""
+    for n, (err, norm, size) in errors_by_head(many_heads(T, H, a_mean, kind, states, seed=97 + T)).items():
+        if n == "dg":
+            r = err / (norm * norm + size * size).sqrt()
+            print(f"MARGIN {n} {r.max():.2e} of 1.0e-02, of its own norm {(err / norm).max():.2e}")
+            assert (r <= 1e-2).all(), (n, r.max().item())
+        else:
+            r = err / norm
+            print(f"MARGIN {n} {r.max():.2e} of 6.5e-03")
+            assert (r <= 6.5e-3).all(), (n, r.max().item())
+
+
+@gpu
+@pytest.mark.parametrize("chunk", [16, 32])
+def test_shorter_chunks_keep_fp32_inside(chunk):
+    """The way out that the header names: each head's outputs lose their own rounding alone."""
+    for n, (err, norm, _) in errors_by_head(many_heads(600, 16, -10.0, "random", True, seed=101), chunk).items():
+        assert (err <= (2.0 ** -8 + 2e-5) * norm).all(), (n, (err / norm).max().item())
