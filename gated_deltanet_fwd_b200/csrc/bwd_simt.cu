@@ -85,7 +85,7 @@ struct SimtArgs {
 // behind the end) and bet (as used in T').  C <= 32: a lane a token.
 __device__ __forceinline__ void scan_gates(const SimtArgs& P, int64_t t0, int L, int h, int lane,
                                            double* gam, float* bet) {
-  double x = lane < L ? (double)P.g[(t0 + lane) * P.Hv + h] : 0.0;
+  double x = lane < L ? (double)floor_decay(P.g[(t0 + lane) * P.Hv + h]) : 0.0;
   const float b = lane < L ? floor_beta(P.beta[(t0 + lane) * P.Hv + h]) : 0.0f;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {

@@ -310,6 +310,8 @@ __global__ void __launch_bounds__(PP_THREADS, 2) chunk_prep_kernel(
         b1 = P.beta[(t0 + 32 + lane) * P.Hv + h];
       }
     }
+    x0 = floor_decay(x0);
+    x1 = floor_decay(x1);
   };
 
   // BWD: a whole chunk comes as boxes of tensor maps, which cost the warps no instructions; the rows behind

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(SIMT_THREADS) chunk_simt_kernel(
     if (tid == 0) {
       float acc = 0.0f;
       for (int r = 0; r < L; ++r) {
-        acc += g[(c_beg + r) * Hv + h];
+        acc += floor_decay(g[(c_beg + r) * Hv + h]);
         gam[r] = acc;
         bet[r] = beta[(c_beg + r) * Hv + h];
       }

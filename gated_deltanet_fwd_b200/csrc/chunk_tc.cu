@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) chunk_tc_kernel(
         cp_async_wait_all();
         __syncwarp();
         const float* gc = gx + (c & 1) * 128;
-        float x0 = gc[lane], x1 = gc[32 + lane];
+        float x0 = floor_decay(gc[lane]), x1 = floor_decay(gc[32 + lane]);
         const float b0 = gc[64 + lane], b1 = gc[96 + lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) chunk_tc_kernel(
       unsigned char* vt = smem + CH_V + st * V_STAGE;
       TC_TS(7);
       // in-chunk cumulative log-decay (inclusive scan over the chunk's 64 rows)
-      float gl = gx[(c & 1) * 64 + lane], gh = gx[(c & 1) * 64 + 32 + lane];
+      float gl = floor_decay(gx[(c & 1) * 64 + lane]), gh = floor_decay(gx[(c & 1) * 64 + 32 + lane]);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const float y0 = __shfl_up_sync(0xffffffffu, gl, o);

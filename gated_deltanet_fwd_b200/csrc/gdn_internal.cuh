@@ -112,6 +112,11 @@ __device__ __forceinline__ float softplusf_(float x) {
   return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
 }
 
+// The log-decay that the chunked kernels add up.  e^-256 is zero in fp32 and in every product, and so is every decay
+// across such a token; but a sum that passes a larger magnitude (a state reset by -1e9 or -infinity) has lost
+// the differences between the tokens behind it.  NaN stays NaN.
+__device__ __forceinline__ float floor_decay(float g) { return g < -256.0f ? -256.0f : g; }
+
 // Device-side fault reporting: the first error wins; never traps.
 __device__ __forceinline__ void report(int* status, int code) {
   if (status) atomicCAS(status, 0, code);

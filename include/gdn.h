@@ -106,7 +106,8 @@ gdn_status gdn_causal_conv1d_silu(const void* x, gdn_dtype dtype, const float* w
  * tokens an intra-chunk triangular system gives the corrections, and the state is propagated
  * between chunks with the cumulative decay.
  * q, k           : [B, T, Hk, dk] dtype.   v, out: [B, T, Hv, dv] dtype.
- * g, beta        : [B, T, Hv] fp32 (log-decay and write strength, e.g. from gdn_gates).
+ * g, beta        : [B, T, Hv] fp32 (log-decay and write strength, e.g. from gdn_gates).  g below -256, down
+ *                  to -infinity, resets the state: it counts as -256, whose exponential is zero in fp32.
  * scale          : multiplies S_t q_t (dk^-0.5 in Qwen3-Next).
  * initial_state  : [N, Hv, dv, dk] fp32 or NULL (zero state).
  * final_state    : [N, Hv, dv, dk] fp32 or NULL (not written).  May not overlap initial_state.
