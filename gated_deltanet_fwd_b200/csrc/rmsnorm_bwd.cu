@@ -110,23 +110,19 @@ struct Kept<T, true> {
   }
 };
 
+// The first `rows` rows; dw's sums over them go to this block's partial row.
 template <typename T, int TPR, bool CK>
-__global__ void __launch_bounds__(256) rmsnorm_bwd_kernel(
+__device__ __forceinline__ void bwd_rows(
     const T* __restrict__ dy, const void* __restrict__ x, const float* __restrict__ xs,
     const void* __restrict__ z, const float* __restrict__ zs, const float* __restrict__ w, float eps,
-    TokRange range, int64_t rpt, int64_t n_tok, T* __restrict__ dx, T* __restrict__ dz,
-    float* __restrict__ part) {
+    int64_t rows, T* __restrict__ dx, T* __restrict__ dz, float* __restrict__ part) {
   constexpr int DIM = TPR * 8, PER = 256 / TPR, U = rows_u<T>();
   const int sub = threadIdx.x % TPR, rsub = threadIdx.x / TPR;
   float wv[8], dw[8] = {};
 #pragma unroll
   for (int i = 0; i < 8; ++i) wv[i] = 1.0f + __ldg(w + sub * 8 + i);
-  int64_t beg, rows;
-  tok_range(range, n_tok, beg, rows);
-  beg *= rpt;
-  rows *= rpt;
   const int64_t stride = (int64_t)gridDim.x * PER;
-  for (int64_t rb = beg + (int64_t)blockIdx.x * PER; rb < rows; rb += U * stride) {
+  for (int64_t rb = (int64_t)blockIdx.x * PER; rb < rows; rb += U * stride) {
     Raw8<T> dr[U];
     Kept<T, CK> xr[U], zr[U];
 #pragma unroll
@@ -190,6 +186,22 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_kernel(
   }
 }
 
+// The rows of a range of tokens, `rpt` rows each.  The range moves the pointers: as bounds of the loop it cost bf16
+// 216 registers for 125, one block an SM for two, and 27 of 244 us.
+template <typename T, int TPR, bool CK>
+__global__ void __launch_bounds__(256) rmsnorm_bwd_kernel(
+    const T* __restrict__ dy, const void* __restrict__ x, const float* __restrict__ xs,
+    const void* __restrict__ z, const float* __restrict__ zs, const float* __restrict__ w, float eps,
+    TokRange range, int64_t rpt, int64_t n_tok, T* __restrict__ dx, T* __restrict__ dz,
+    float* __restrict__ part) {
+  int64_t beg, end;
+  tok_range(range, n_tok, beg, end);
+  const int64_t row = beg * rpt, at = row * (TPR * 8), kept = at * (CK ? 1 : sizeof(T));
+  bwd_rows<T, TPR, CK>(dy + at, (const unsigned char*)x + kept, CK ? xs + row : nullptr,
+                       (const unsigned char*)z + kept, CK ? zs + row : nullptr, w, eps, (end - beg) * rpt,
+                       dx + at, dz + at, part);
+}
+
 template <typename K>
 int64_t wave_cap(K kern) {
   int dev = 0, sms = 148, per = 1;
@@ -233,8 +245,7 @@ cudaError_t bwd_t(const T* dy, const void* x, const float* xs, const void* z, co
     blocks = blocks < cap ? blocks : cap;
     blocks = blocks < max_parts ? blocks : max_parts;
     if (blocks > 0)
-      kern<<<(unsigned)blocks, 256, 0, s>>>(dy, x, xs, z, zs, w, eps, range, rpt, rows / rpt, dx, dz,
-                                             part);
+      kern<<<(unsigned)blocks, 256, 0, s>>>(dy, x, xs, z, zs, w, eps, range, rpt, rows / rpt, dx, dz, part);
   };
   switch (tpr) {
     case 1: run(rmsnorm_bwd_kernel<T, 1, CK>); break;
