@@ -403,8 +403,9 @@ def gdn_chunk_bwd(q, k, v, g, beta, dout, scale=None, initial_state=None, cu_seq
     _shape((N, Hv, d_v, d_k), initial_state, dfinal_state, dinitial_state)
     new = lambda t, shape: dout.new_empty(shape) if t is None else t  # noqa: E731
     dq, dk, dv = new(dq, (B, T, Hk, d_k)), new(dk, (B, T, Hk, d_k)), new(dv, (B, T, Hv, d_v))
-    if cu_seqlens is not None and dg is None and dbeta is None:
-        dg, dbeta = dout.new_zeros((2, B, T, Hv)).unbind()
+    if cu_seqlens is not None and (dg is None or dbeta is None):  # zeros, from one allocation
+        zeros = dout.new_zeros((2, B, T, Hv)).unbind()
+        dg, dbeta = (z if t is None else t for t, z in zip((dg, dbeta), zeros))
     dg, dbeta = new(dg, (B, T, Hv)), new(dbeta, (B, T, Hv))
     if output_dinitial_state is None:
         output_dinitial_state = initial_state is not None
@@ -497,7 +498,8 @@ def gdn_causal_conv1d_silu_bwd(dy, x, w, bias=None, cu_seqlens=None, n_l2norm_ch
     """Gradients of gdn_causal_conv1d_silu: (dx, dw, dbias, dconv_state_in).
 
     x [B, T, C] is the forward's input, or its 8-bit checkpoint as a (codes, scales) pair.  dbias is
-    None without bias; dconv_state_in [N, C, K-1] is computed when conv_state_in is given.
+    None without bias; dconv_state_in [N, C, K-1] is computed when conv_state_in is given.  Rows of dx of
+    tokens outside every sequence of cu_seqlens are not written (anything where dx is made here).
     """
     x, xs = _kept(x)
     _all_cuda(dy, x, xs, w, bias, cu_seqlens, conv_state_in, dconv_state_out, dx, dw, dbias,

@@ -426,6 +426,11 @@ def test_gates_after_the_rule_on_a_padded_batch(given, dtype, d):
                                               **own)
     if not given:
         assert (dg[:, 290:] == 0).all() and (dbeta[:, 290:] == 0).all()
+        for n in ("dg", "dbeta"):  # one given, one made
+            two = gdn.gdn_chunk_bwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["dout"], cu_seqlens=cu,
+                                    **{n: nan(1, T, Hv)})[3:5]
+            made, kept = two[n == "dg"], two[n != "dg"]
+            assert (made[:, 290:] == 0).all() and kept[:, 290:].isnan().all()
     da, db, dA, ddt = gdn.gdn_gates_bwd(t["a"], t["b"], A, bias, dg, dbeta, cu_seqlens=cu)
     want = gdn.gdn_gates_bwd(*(v[:, :290].contiguous() for v in (t["a"], t["b"])), A, bias,
                              *(v[:, :290].contiguous() for v in (dg, dbeta)))
