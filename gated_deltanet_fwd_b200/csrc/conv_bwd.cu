@@ -8,10 +8,12 @@
 // An input in front of its sequence is conv_state_in; its gradient is the same sum at a negative place.
 // conv_state_out is a copy of the last K-1 of (history, inputs), so dconv_state_out is added there.
 //
-// dy and x in, dx out, once each (and K-1 tokens of halo at the ends of a token range).  What bounds it is
-// instructions: with packed arithmetic (two channels an instruction) still 149 for four channels of a token,
-// eight of them on the special-function unit.  2 x 16384 tokens of 8192 channels bf16, 4 taps: 461 us for
-// 1.61 GB, 3.5 TB/s, 53 % of a copy, and 14 us for the partial rows.
+// dy and x in, dx out, once each (and K-1 tokens of halo at the ends of a token range).  2 x 16384 tokens of 8192
+// channels bf16, 4 taps: 461 us for 1.61 GB, 3.5 TB/s, 53 % of a copy, and 14 us for the partial rows.  The 149
+// instructions for four channels of a token (packed arithmetic, two channels each; eight on the special-function
+// unit) would take 269 us of that if every issue slot were used, and 58 % are: what bounds it is latency inside
+// a warp, with sixteen warps an SM (128 registers).  For each pair of tokens the norm's sums are seven dependent
+// shuffles, a reciprocal root and two exchanges before a dpre exists.
 // A thread holds 4 channels and streams a range of tokens forward: x[t-KT+1 .. t] and
 // dpre[t-KT+1 .. t] are register windows, so each token is loaded and each dpre computed once; dx is
 // stored KT-1 tokens late.  Whole batches of tokens inside a range and a sequence run unrolled without

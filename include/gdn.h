@@ -313,6 +313,8 @@ gdn_status gdn_gated_rmsnorm(const void* x, const void* z, gdn_dtype dtype, cons
  * the norm for fp32 outputs): bf16 calls that need this pass chunk = 16 or 32, at several times the time.
  * A beta of magnitude below 2^-30 takes part as +-2^-30, but for dv; without an initial state dg of a
  * sequence's first token is exactly zero.
+ * Workspace: on tensor cores 115 KB per chunk and v-head (1.9 GB for 32768 tokens of 32 v-heads); else
+ * (2 chunk^2 + 2 dk dv + 2 chunk dv + 5 chunk) fp32 each, in chunks of at most 32 tokens (5.7 GB for the same).
  */
 size_t gdn_chunk_bwd_workspace_size(gdn_dtype dtype, int N, int B, int64_t T, int Hk, int Hv,
                                     int dk, int dv, int chunk);

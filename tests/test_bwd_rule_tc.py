@@ -269,7 +269,7 @@ def errors_by_head(x, chunk=64):
                                                (2048, 32, -10.0, False)])
 def test_errors_of_many_calls(T, H, a_mean, states, kind):
     """What the header says of the tensor-core path, for each of many one-head calls: keys at random, with strong
-    writes, and with a direction in common; decays from e^-8 a token to none.
+    writes, and with a direction in common; decays from e^-6 a token to none.
 
     Rounding to bf16 costs 2^-8 / sqrt(6) = 1.6e-3 of an operand's norm.  There are fifteen such operands (T~, P,
     scale Gamma Q; in either walk the state's copy, X, the update's operand; U, dV, the copies of S and dS, dN, dM:
