@@ -124,8 +124,12 @@ def _cuda(*ts):
 def _tok_stride(t):
     """Token stride of a [B, T, H, d] view whose heads are packed inside each token, else None."""
     B, T, H, d = t.shape
-    if not t.is_cuda or t.stride(3) != 1 or t.stride(2) != d:
+    if not t.is_cuda or t.stride(3) != 1 or (H > 1 and t.stride(2) != d):
         return None
+    if B * T < 2:  # no distance between tokens
+        return H * d
+    if T == 1:
+        return t.stride(0)
     if B > 1 and t.stride(0) != T * t.stride(1):
         return None
     return t.stride(1)

@@ -192,6 +192,24 @@ def test_strided_inputs_match_dense(dtype, d):
 
 
 @gpu
+@pytest.mark.parametrize("B,T,Hk", [(3, 1, 2), (1, 1, 1), (300, 1, 1), (2, 5, 1)])
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128)])
+def test_strided_single_tokens(dtype, d, B, T, Hk):
+    """Slices of [q | k | v] with one token a sequence: the tokens' distance is the sequences'."""
+    Hv = 2 * Hk
+    x = make([T] * B, Hk, Hv, d, d, dtype, True, packed=False, seed=15)
+    mix = torch.cat([x["q"].flatten(1), x["k"].flatten(1), x["v"].flatten(1)], 1).view(B, T, -1).cuda()
+    q, k, v = (t.unflatten(-1, (-1, d)) for t in mix.split([Hk * d, Hk * d, Hv * d], -1))
+    g, beta, do = (x[n].view(B, T, *x[n].shape[1:]).cuda() for n in ("g", "beta", "dout"))
+    S0, dST = x["S0"].cuda(), x["dST"].cuda()
+    got = gdn.gdn_chunk_bwd(q, k, v, g, beta, do, initial_state=S0, dfinal_state=dST)
+    assert all(torch.equal(a, b) for a, b in zip(call(x), got))
+    one = gdn.gdn_chunk_fwd(q, k, v, g, beta, initial_state=S0)
+    two = gdn.gdn_chunk_fwd(q.contiguous(), k.contiguous(), v.contiguous(), g, beta, initial_state=S0)
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+
+
+@gpu
 @pytest.mark.parametrize("dtype,d,chunk", [("f32", 64, 32), ("bf16", 128, 64)])
 def test_bits_graph_and_streams(dtype, d, chunk):
     """Twice the same bits; two calls at once on two streams; captured, and replayed on new inputs."""
