@@ -107,11 +107,12 @@ __device__ __forceinline__ void ld64(uint32_t taddr, float* v) {
   ld32(taddr + 32, v + 32);
 }
 
-// One walk: sequence n, v-head h.  map_x: V forward, dO backward; map_tp: boxes of T~, backward of [T~; P].
+// One walk: sequence n, its tokens [s_beg, s_end), chunks from slot0 on; v-head h.  map_x: V forward, dO backward; map_tp: boxes of T~, backward of [T~; P].
 template <bool BACK>
 __device__ __forceinline__ void chain(const CUtensorMap* map_k, const CUtensorMap* map_x,
                                       const CUtensorMap* map_tp, const CUtensorMap* map_dv,
-                                      const ChainParams& P, unsigned char* smem, int n, int h) {
+                                      const ChainParams& P, unsigned char* smem, int n, int h,
+                                      int64_t s_beg, int64_t s_end, int64_t slot0) {
   using L_ = Sm<BACK>;
   const float* S_in = BACK ? P.dS_T : P.S0;
   const uint32_t sbase = smem_u32(smem);
@@ -121,11 +122,6 @@ __device__ __forceinline__ void chain(const CUtensorMap* map_k, const CUtensorMa
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = h / (P.Hv / P.Hk);
-  int64_t s_beg, s_end, slot0;
-  if (!seq_range(P.cu, P.T, n, tm::C, s_beg, s_end, slot0)) {
-    if (tid == 0) report(P.status, GDN_ERR_DEVICE_ARG);
-    return;  // nothing allocated yet
-  }
   const size_t sidx = ((size_t)n * P.Hv + h) * tm::STATE_FLOATS;
   const int nch = (int)((s_end - s_beg + tm::C - 1) / tm::C);
   if (nch == 0) {  // empty sequence: the gradient passes through
@@ -625,24 +621,27 @@ __global__ void __launch_bounds__(THREADS, 1) bwd_chain_kernel(
   int n = blockIdx.x / (2 * P.Hv);
   // the n-th longest sequence; many sequences balance without
   if (P.cu && P.N > 1 && P.N <= MAX_SORTED) {
-    __shared__ int pick;
+    __shared__ int pick, len[MAX_SORTED];
     const int i = threadIdx.x;
+    if (i < P.N) len[i] = P.cu[i + 1] - P.cu[i];
+    __syncthreads();
     if (i < P.N) {
-      const int len = P.cu[i + 1] - P.cu[i];
       int rank = 0;
-      for (int m = 0; m < P.N; ++m) {
-        const int o = P.cu[m + 1] - P.cu[m];
-        rank += o > len || (o == len && m < i);
-      }
+      for (int m = 0; m < P.N; ++m) rank += len[m] > len[i] || (len[m] == len[i] && m < i);
       if (rank == n) pick = i;  // ranks are a permutation whatever cu_seqlens holds
     }
     __syncthreads();
     n = pick;
   }
+  int64_t s_beg, s_end, slot0;
+  if (!seq_range(P.cu, P.T, n, tm::C, s_beg, s_end, slot0)) {
+    if (threadIdx.x == 0) report(P.status, GDN_ERR_DEVICE_ARG);
+    return;  // nothing allocated yet
+  }
   if (back)
-    chain<true>(&map_k, &map_do, &map_tp, &map_dv, P, smem, n, h);
+    chain<true>(&map_k, &map_do, &map_tp, &map_dv, P, smem, n, h, s_beg, s_end, slot0);
   else
-    chain<false>(&map_k, &map_v, &map_t, &map_dv, P, smem, n, h);
+    chain<false>(&map_k, &map_v, &map_t, &map_dv, P, smem, n, h, s_beg, s_end, slot0);
 }
 
 }  // namespace

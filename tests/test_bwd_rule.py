@@ -284,6 +284,35 @@ def test_malformed_cu_seqlens_is_reported(dtype, d, bad):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,d,chunk", [("f32", 32, 16), ("bf16", 128, 64)])
+def test_many_sequences(dtype, d, chunk):
+    """Several rounds of the warps' searches in cu_seqlens (32 and 128 entries each): each sequence's gradients have
+    the bits of a call of its neighbours alone, and an entry that is malformed stops what lies behind it."""
+    gen = torch.Generator().manual_seed(107)
+    lens = [int(n) for n in torch.randint(0, 4, (700,), generator=gen)]
+    lens[130], lens[300], lens[699] = 70, 0, 33
+    x = make(lens, 1, 2, d, d, dtype, True, seed=109)
+    got = call(x, chunk)
+    check(x, lens, got, F32_TOL if dtype == "f32" else TC_TOL, d ** -0.5)
+    at = np.cumsum([0] + lens)
+    for lo, hi in ((0, 500), (100, 420), (290, 700)):  # bf16: enough gate values for the same path
+        part = {n: x[n][at[lo]:at[hi]] for n in ("q", "k", "v", "g", "beta", "dout")}
+        part.update(S0=x["S0"][lo:hi], dST=x["dST"][lo:hi], B=1, T=int(at[hi] - at[lo]),
+                    cu=torch.tensor(at[lo:hi + 1] - at[lo], dtype=torch.int32))
+        for a, b in zip(call(part, chunk)[:5], got[:5]):
+            assert torch.equal(a, b[:, at[lo]:at[hi]])
+    dt = x["q"].dtype
+    ws = torch.empty(gdn.chunk_bwd_workspace_size(dt, 700, 1, x["T"], 1, 2, d, d, chunk), dtype=torch.uint8,
+                     device="cuda")
+    for bad in (1, 31, 32, 33, 128, 129, 411, 700):
+        cu = x["cu"].clone()
+        cu[bad] = -1
+        part = call(dict(x, cu=cu), chunk, workspace=ws)
+        assert gdn.workspace_status(ws) == gdn.GDN_ERR_DEVICE_ARG
+        assert all(torch.equal(a[:, :at[bad - 1]], b[:, :at[bad - 1]]) for a, b in zip(part[:5], got[:5])), bad
+
+
+@gpu
 @pytest.mark.parametrize("dtype,d", [("f32", 32), ("bf16", 128)])
 def test_no_tokens_passes_the_state_gradient(dtype, d):
     x = make([0, 0], 1, 2, d, d, dtype, True)
