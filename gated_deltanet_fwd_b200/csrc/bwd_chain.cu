@@ -107,7 +107,8 @@ __device__ __forceinline__ void ld64(uint32_t taddr, float* v) {
   ld32(taddr + 32, v + 32);
 }
 
-// One walk: sequence n, its tokens [s_beg, s_end), chunks from slot0 on; v-head h.  map_x: V forward, dO backward; map_tp: boxes of T~, backward of [T~; P].
+// One walk: sequence n, its tokens [s_beg, s_end), chunks from slot0 on; v-head h.  map_x: V forward, dO
+// backward; map_tp: boxes of T~, backward of [T~; P].
 template <bool BACK>
 __device__ __forceinline__ void chain(const CUtensorMap* map_k, const CUtensorMap* map_x,
                                       const CUtensorMap* map_tp, const CUtensorMap* map_dv,

@@ -304,10 +304,10 @@ gdn_status gdn_gated_rmsnorm(const void* x, const void* z, gdn_dtype dtype, cons
  * workspace's status word (gdn_workspace_status).  All pointers but dg, dbeta and cu_seqlens 16-byte
  * aligned; dg and dbeta on a multiple of their element.
  * bf16 with dk = dv = 128, chunk = 64 and B * T * Hv >= 512 runs on tensor cores, whose operands are
- * rounded to bf16.  Each head's dq, dk, dv and dbeta are then within 6.5e-3 of their norm (measured: 2.4 to
+ * rounded to bf16.  dq, dk, dv and dbeta are then each within 6.5e-3 of their norm (measured: 2.4 to
  * 5.9e-3, the most where nothing decays).  dg[t] is a sum of dv * dk products of either sign, of state and
- * state gradient; a head's dg is within 1e-2 of the norm of (dg, root sum of squares of those products),
- * taken over its tokens (measured: 2 to 7e-3).  Over many heads or short memories that is 3 to 5e-3 of dg's own
+ * state gradient; dg is within 1e-2 of the norm of (dg, root sum of squares of those products), taken
+ * over all its values (measured: 2 to 7e-3).  Over many heads or short memories that is 3 to 5e-3 of dg's own
  * norm; of one head with slow decay, whose dg[t] all follow the same few numbers, up to 1.5e-2 when these
  * happen to be small.  Everything else keeps fp32 inside, and loses only the output's own rounding (2e-5 of
  * the norm for fp32 outputs): bf16 calls that need this pass chunk = 16 or 32, at several times the time.
